@@ -17,6 +17,17 @@ Entry points (same names and arguments as the C ABI):
 plus ``pack(W, q_group_size, zero_point)`` / ``linear(x, packed)`` which pick
 GEMV up to 8 tokens and GEMM otherwise, following ``quant_config``'s
 ``version`` ("Optimization Awq", section "Quantizar seu próprio modelo").
+
+The layer with its epilogue and the layers of experts:
+
+* ``linear_fused(x, packed, bias, activation, gated, residual)``
+* ``route_experts(logits, top_k, renormalize)`` -> ``ExpertRoute``
+* ``pack_experts(W, q_group_size, zero_point)`` -> ``PackedExperts``
+* ``linear_experts(x, experts, route, bias, activation, gated)``
+* ``combine_experts(h, experts, route, bias, residual)``
+* ``expert_mlp(x, logits, gate_up, down, top_k)``: the four together
+
+and ``mlp(x, gate_up, down, residual)``, a decoder block's MLP in two launches.
 """
 from __future__ import annotations
 
@@ -38,12 +49,19 @@ AWQ_ERR_UNSUPPORTED = -5
 AWQ_ERR_WORKSPACE = -6
 AWQ_ERR_HIP = -7
 AWQ_ERR_SCRATCH = -8
+AWQ_ERR_OPTION = -9
+
+# awq_activation: the activations of the fused layers' epilogue
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 EXPORTED = ("awq_pack", "awq_dequant", "awq_gemv", "awq_gemm", "awq_gemm_workspace_bytes", "awq_strerror",
             "awq_scale_candidates", "awq_scale_candidates_workspace_bytes", "awq_scale_loss",
             "awq_scale_loss_workspace_bytes", "awq_scale_columns", "awq_clip_search",
             "awq_clip_search_workspace_bytes", "awq_scale_search", "awq_scale_search_workspace_bytes",
-            "awq_gemm_noalloc", "awq_gemm_noalloc_max_workspace_bytes")
+            "awq_gemm_noalloc", "awq_gemm_noalloc_max_workspace_bytes",
+            "awq_linear_fused", "awq_linear_fused_workspace_bytes", "awq_route_experts",
+            "awq_route_experts_workspace_bytes", "awq_linear_experts", "awq_linear_experts_workspace_bytes",
+            "awq_combine_experts", "awq_combine_experts_workspace_bytes")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -98,6 +116,24 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.awq_clip_search.restype = ctypes.c_int
     lib.awq_clip_search_workspace_bytes.argtypes = [I32, I32, I32, I32, I32]
     lib.awq_clip_search_workspace_bytes.restype = SZ
+    lib.awq_linear_fused.argtypes = [P, I32, P, P, P, P, I32, I32, P, I32, P, I32, I32, I32, I32, I32, I32, P, SZ, P]
+    lib.awq_linear_fused.restype = ctypes.c_int
+    lib.awq_linear_fused_workspace_bytes.argtypes = [I32, I32, I32, I32, I32]
+    lib.awq_linear_fused_workspace_bytes.restype = SZ
+    lib.awq_route_experts.argtypes = [P, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P, SZ, P]
+    lib.awq_route_experts.restype = ctypes.c_int
+    lib.awq_route_experts_workspace_bytes.argtypes = [I32, I32]
+    lib.awq_route_experts_workspace_bytes.restype = SZ
+    lib.awq_linear_experts.argtypes = [P, I32, I32, P, I32, P, I32, I32, P, P, P, P, I32, I32, P, I32, I32, I32, I32,
+                                       I32, P, SZ, P]
+    lib.awq_linear_experts.restype = ctypes.c_int
+    lib.awq_linear_experts_workspace_bytes.argtypes = [I32, I32, I32, I32, I32, I32]
+    lib.awq_linear_experts_workspace_bytes.restype = SZ
+    lib.awq_combine_experts.argtypes = [P, I32, P, P, P, I32, I32, I32, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32,
+                                        P, SZ, P]
+    lib.awq_combine_experts.restype = ctypes.c_int
+    lib.awq_combine_experts_workspace_bytes.argtypes = [I32, I32, I32, I32, I32, I32]
+    lib.awq_combine_experts_workspace_bytes.restype = SZ
     _lib = lib
     return lib
 
@@ -456,3 +492,224 @@ def quantize_awq(w: torch.Tensor, x: torch.Tensor, q_group_size: int = 128, zero
         xs = awq_scale_columns(x, res.scale, divide=True)
         ws, _ = awq_clip_search(xs, ws, q_group_size, zero_point, clip_ratios)
     return QuantizedLinear(pack(ws, q_group_size, zero_point), res.scale, res)
+
+
+def _rows2d(t: torch.Tensor, width: int, what: str):
+    """(address, row stride) of a float16 matrix on the GPU whose rows are contiguous and 16-byte aligned."""
+    if t.dtype != torch.float16 or t.dim() != 2 or t.shape[1] != width:
+        raise ValueError(f"{what} must be a 2-D float16 tensor with {width} columns")
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the AWQ kernels must live on the GPU")
+    ld, inner = t.stride()
+    if t.shape[0] == 1:
+        ld = (width + 7) & ~7
+    if (inner != 1 and width > 1) or ld < width:
+        raise ValueError(f"{what} must have contiguous rows that do not overlap")
+    return t.data_ptr(), ld
+
+
+def _flat(t: Optional[torch.Tensor], shape, dtype, what: str) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be a {str(dtype).split('.')[-1]} tensor of shape {tuple(shape)}")
+    return _ptr(t)
+
+
+def _activation(name: str) -> int:
+    try:
+        return ACTIVATIONS[name]
+    except KeyError:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}; got {name!r}") from None
+
+
+def _scratch(need: int, t: torch.Tensor, workspace: Optional[torch.Tensor]):
+    """(address, bytes) of the caller's workspace, or of the stream's own."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = gemm_workspace(need, t.device)
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def linear_fused(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor] = None, activation: str = "none",
+                 gated: bool = False, residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """act(x . W'^T + bias) + residual for fp16 ``x`` [..., K], in one call.  With ``gated`` the first half of
+    ``pw``'s rows is the gate (``pack_fused([gate, up])``): act(gate) * up, half as many columns.  ``x``,
+    ``residual`` and ``y`` may be 2-D views with a row stride (a multiple of 8 elements); ``y`` may be
+    ``residual`` itself.  One rounding to fp16."""
+    lib = load_library()
+    x2 = x if x.dim() == 2 else x.reshape(-1, pw.K)
+    M, width = x2.shape[0], pw.N // 2 if gated else pw.N
+    xp, ldx = _rows2d(x2, pw.K, "x")
+    act = _activation(activation)
+    rp, ldr = None, 0
+    if residual is not None:
+        residual = residual if residual.dim() == 2 else residual.reshape(-1, width)
+        if residual.shape[0] != M:
+            raise ValueError(f"residual must have x's {M} rows")
+        rp, ldr = _rows2d(residual, width, "residual")
+    out = torch.empty((M, width), dtype=torch.float16, device=x.device) if y is None else y
+    if out.dim() != 2 or out.shape[0] != M:
+        raise ValueError(f"y must be [{M}, {width}]")
+    yp, ldy = _rows2d(out, width, "y")
+    need = lib.awq_linear_fused_workspace_bytes(M, pw.N, pw.K, pw.group_size, int(gated))
+    ws, ws_bytes = _scratch(need, x2, workspace)
+    st = lib.awq_linear_fused(xp, ldx, _ptr(pw.qweight), _ptr(pw.scales), _ptr(pw.qzeros) if pw.zero_point else None,
+                              _flat(bias, (pw.N,), torch.float16, "bias"), act, int(gated), rp, ldr, yp, ldy, M, pw.N,
+                              pw.K, pw.group_size, int(pw.zero_point), ws, ws_bytes, _stream(x2))
+    _check(st, "awq_linear_fused")
+    return out if y is not None or x.dim() == 2 else out.reshape(*x.shape[:-1], width)
+
+
+def mlp(x: torch.Tensor, gate_up: PackedWeight, down: PackedWeight, activation: str = "silu",
+        residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A decoder block's gated MLP, down(act(gate(x)) * up(x)) + residual, in two fused layers."""
+    return linear_fused(linear_fused(x, gate_up, activation=activation, gated=True), down, residual=residual)
+
+
+class ExpertRoute(NamedTuple):
+    ids: torch.Tensor        # int32 [T, top_k]: each slot's expert, -1 for none
+    weights: torch.Tensor    # fp32 [T, top_k]
+    offsets: torch.Tensor    # int32 [E + 1]: expert e's rows are offsets[e] .. offsets[e + 1] - 1
+    rows: torch.Tensor       # int32 [T * top_k]: the slot t * top_k + j of each row, -1 past offsets[E]
+    positions: torch.Tensor  # int32 [T, top_k]: each slot's row, -1 for none
+
+
+def route_experts(logits: torch.Tensor, top_k: int, renormalize: bool = True,
+                  workspace: Optional[torch.Tensor] = None) -> ExpertRoute:
+    """The ``top_k`` largest of each token's expert logits (fp16 or fp32 [T, E]; the lower index first among equal
+    ones), their softmax weights (over the chosen ones, or over all E without ``renormalize``), and the tokens'
+    slots sorted by expert.  Logits of -inf or NaN are masked; a slot left without an expert has id -1."""
+    lib = load_library()
+    if logits.dim() != 2 or logits.dtype not in (torch.float16, torch.float32):
+        raise ValueError("logits must be a 2-D float16 or float32 tensor [T, E]")
+    if not logits.is_cuda:
+        raise ValueError("tensors passed to the AWQ kernels must live on the GPU")
+    T, E = logits.shape
+    ld, inner = logits.stride()
+    if T == 1:
+        ld = E
+    if inner != 1 and E > 1:
+        raise ValueError("logits must have contiguous rows")
+    if not 1 <= top_k <= min(E, 64):
+        raise AwqError(AWQ_ERR_OPTION, "awq_route_experts")
+    dev, slots = logits.device, T * top_k
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    rows = torch.empty(slots, dtype=torch.int32, device=dev)
+    positions = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    need = lib.awq_route_experts_workspace_bytes(T, E)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws, ws_bytes = _scratch(need, logits, workspace)
+    st = lib.awq_route_experts(logits.data_ptr(), ld, int(logits.dtype == torch.float32), T, E, top_k,
+                               int(renormalize), ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
+                               rows.data_ptr(), positions.data_ptr(), ws, ws_bytes, _stream(logits))
+    _check(st, "awq_route_experts")
+    return ExpertRoute(ids, weights, offsets, rows, positions)
+
+
+class PackedExperts(NamedTuple):
+    qweight: torch.Tensor            # int32 [E, N, K / 8]
+    scales: torch.Tensor             # fp16 [E, N / 8, G, 8]
+    qzeros: Optional[torch.Tensor]   # int32 [E, N / 8, G]
+    E: int
+    N: int
+    K: int
+    group_size: int
+    zero_point: bool
+
+
+def pack_experts(W, q_group_size: int = 128, zero_point: bool = True) -> PackedExperts:
+    """Quantize the experts' weights [E, out, in] (a tensor, or a list of [out, in]).  Expert by expert the same
+    bits as ``pack``: the rows of all experts are one tall weight to ``awq_pack``."""
+    W = W if isinstance(W, torch.Tensor) else torch.stack(list(W))
+    if W.dtype != torch.float16 or W.dim() != 3:
+        raise ValueError("W must be a 3-D float16 tensor [E, N, K]")
+    E, N, K = W.shape
+    G = K // q_group_size if q_group_size > 0 else 0
+    qweight = torch.empty((E, N, K // 8), dtype=torch.int32, device=W.device)
+    scales = torch.empty((E, N // 8, G, 8), dtype=torch.float16, device=W.device)
+    qzeros = torch.empty((E, N // 8, G), dtype=torch.int32, device=W.device) if zero_point else None
+    for e in range(E):
+        awq_pack(W[e], q_group_size, zero_point, qweight[e], scales[e], qzeros[e] if zero_point else None)
+    return PackedExperts(qweight, scales, qzeros, E, N, K, q_group_size, bool(zero_point))
+
+
+def _check_route(route: ExpertRoute, pe: PackedExperts):
+    T, top_k = route.ids.shape
+    _flat(route.offsets, (pe.E + 1,), torch.int32, "route.offsets")
+    _flat(route.rows, (T * top_k,), torch.int32, "route.rows")
+    return T, top_k
+
+
+def linear_experts(x: torch.Tensor, pe: PackedExperts, route: ExpertRoute, bias: Optional[torch.Tensor] = None,
+                   activation: str = "none", gated: bool = False, y: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Every routed slot's token (fp16 ``x`` [T, K]) through its expert's layer and epilogue (``bias`` [E, N],
+    ``gated`` as in ``linear_fused``): fp16 [T * top_k, N or N / 2], rows sorted by expert as ``route.rows`` says.
+    Rows past ``route.offsets[E]`` (slots without an expert) are not written."""
+    lib = load_library()
+    T, top_k = _check_route(route, pe)
+    xp, ldx = _rows2d(x, pe.K, "x")
+    if x.shape[0] != T:
+        raise ValueError(f"x must have the route's {T} tokens")
+    R, width = T * top_k, pe.N // 2 if gated else pe.N
+    act = _activation(activation)
+    out = torch.empty((R, width), dtype=torch.float16, device=x.device) if y is None else y
+    if out.dim() != 2 or out.shape[0] != R:
+        raise ValueError(f"y must be [{R}, {width}]")
+    yp, ldy = _rows2d(out, width, "y")
+    need = lib.awq_linear_experts_workspace_bytes(R, pe.E, pe.N, pe.K, pe.group_size, int(gated))
+    ws, ws_bytes = _scratch(need, x, workspace)
+    st = lib.awq_linear_experts(xp, ldx, T, route.rows.data_ptr(), top_k, route.offsets.data_ptr(), R, pe.E,
+                                _ptr(pe.qweight), _ptr(pe.scales), _ptr(pe.qzeros) if pe.zero_point else None,
+                                _flat(bias, (pe.E, pe.N), torch.float16, "bias"), act, int(gated), yp, ldy, pe.N, pe.K,
+                                pe.group_size, int(pe.zero_point), ws, ws_bytes, _stream(x))
+    _check(st, "awq_linear_experts")
+    return out
+
+
+def combine_experts(h: torch.Tensor, pe: PackedExperts, route: ExpertRoute, bias: Optional[torch.Tensor] = None,
+                    residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The experts' second layer on the sorted rows ``h`` [T * top_k, K] and each token's weighted sum, plus
+    ``residual`` [T, N]: fp16 [T, N], one rounding."""
+    lib = load_library()
+    T, top_k = _check_route(route, pe)
+    _flat(route.positions, (T, top_k), torch.int32, "route.positions")
+    _flat(route.weights, (T, top_k), torch.float32, "route.weights")
+    hp, ldh = _rows2d(h, pe.K, "h")
+    if h.shape[0] != T * top_k:
+        raise ValueError(f"h must have the route's {T * top_k} rows")
+    rp, ldr = None, 0
+    if residual is not None:
+        if residual.dim() != 2 or residual.shape[0] != T:
+            raise ValueError(f"residual must be [{T}, {pe.N}]")
+        rp, ldr = _rows2d(residual, pe.N, "residual")
+    out = torch.empty((T, pe.N), dtype=torch.float16, device=h.device) if y is None else y
+    if out.dim() != 2 or out.shape[0] != T:
+        raise ValueError(f"y must be [{T}, {pe.N}]")
+    yp, ldy = _rows2d(out, pe.N, "y")
+    need = lib.awq_combine_experts_workspace_bytes(T, top_k, pe.E, pe.N, pe.K, pe.group_size)
+    ws, ws_bytes = _scratch(need, h, workspace)
+    st = lib.awq_combine_experts(hp, ldh, route.offsets.data_ptr(), route.positions.data_ptr(),
+                                 route.weights.data_ptr(), T, top_k, pe.E, _ptr(pe.qweight), _ptr(pe.scales),
+                                 _ptr(pe.qzeros) if pe.zero_point else None,
+                                 _flat(bias, (pe.E, pe.N), torch.float16, "bias"), rp, ldr, yp, ldy, pe.N, pe.K,
+                                 pe.group_size, int(pe.zero_point), ws, ws_bytes, _stream(h))
+    _check(st, "awq_combine_experts")
+    return out
+
+
+def expert_mlp(x: torch.Tensor, logits: torch.Tensor, gate_up: PackedExperts, down: PackedExperts, top_k: int,
+               activation: str = "silu", renormalize: bool = True,
+               residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A mixture-of-experts MLP: route each token of ``x`` [T, K] by its ``logits`` [T, E], the experts' gated first
+    layers, their second layers weighted and added up, plus ``residual``.  Nothing is read back to the host."""
+    route = route_experts(logits, top_k, renormalize)
+    h = linear_experts(x, gate_up, route, activation=activation, gated=True)
+    return combine_experts(h, down, route, residual=residual)

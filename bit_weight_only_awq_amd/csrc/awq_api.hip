@@ -213,6 +213,7 @@ const char* awq_strerror(int status) {
     case AWQ_ERR_SCRATCH:
       return "the shape needs more split-K workspace than awq_gemm_noalloc's fixed scratch "
              "(awq_gemm_noalloc_max_workspace_bytes()); use awq_gemm with a workspace";
+    case AWQ_ERR_OPTION: return "an option is out of range: activation, top_k (1 .. min(E, 64)) or slots_per_row";
     default: return "unknown awq status";
   }
 }

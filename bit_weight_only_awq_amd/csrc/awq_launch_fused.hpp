@@ -1,0 +1,63 @@
+// Host-side launchers of the fused layer, the expert products and the expert
+// router.  Arguments are validated by the C ABI layer; each launcher returns
+// hipGetLastError() after enqueueing its kernels on `stream`.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace awq {
+
+// A stack of E packed weights of one shape (E = 1: a single layer).
+struct PackedArgs {
+  const uint32_t* qweight;
+  const uint16_t* scales;
+  const uint32_t* qzeros;  // NULL: symmetric
+  int E, N, K, group_size;
+};
+
+// Y[r] = act(X[row(r)] W'_e^T + bias_e) [* the second half of the columns] +
+// residual[r] for R rows; `offsets` NULL: one expert holds all R rows.
+struct ProductArgs {
+  const _Float16* x;
+  int64_t ldx;
+  int x_rows;                // rows of x
+  const int* rows;           // NULL: row r of x; else row rows[r] / slots_per_row
+  int slots_per_row;
+  const int* offsets;        // [E + 1], or NULL
+  int R;
+  const _Float16* bias;      // [E][N], or NULL
+  int activation;            // awq_activation
+  bool gated;
+  const _Float16* residual;  // [R][N_out] at stride ldr, or NULL
+  int64_t ldr;
+  _Float16* y;               // [R][N_out] at stride ldy
+  int64_t ldy;
+};
+
+// The weighted sum over each token's slots: y[t] = sum_j weights[t][j] *
+// (product row positions[t][j]) + residual[t].
+struct CombineArgs {
+  const int* positions;  // [T][top_k], negative: not routed
+  const float* weights;  // [T][top_k]
+  int T, top_k;
+  const _Float16* residual;
+  int64_t ldr;
+  _Float16* y;
+  int64_t ldy;
+};
+
+size_t product_workspace_bytes(int R, int E, int N, int K, bool gated);
+hipError_t launch_product(const PackedArgs& w, const ProductArgs& p, void* workspace, hipStream_t stream);
+
+// `p` describes the product (x already sorted by expert, no gather, gate or
+// residual); its y is not used.
+size_t combine_workspace_bytes(int T, int top_k, int E, int N, int K);
+hipError_t launch_combine(const PackedArgs& w, const ProductArgs& p, const CombineArgs& c, void* workspace,
+                          hipStream_t stream);
+
+size_t route_workspace_bytes(int T, int E);
+hipError_t launch_route(const void* logits, int ld, bool fp32, int T, int E, int top_k, bool renormalize, int* ids,
+                        float* weights, int* offsets, int* rows, int* positions, void* workspace, hipStream_t stream);
+
+}  // namespace awq

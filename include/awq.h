@@ -61,7 +61,17 @@ enum awq_status {
   AWQ_ERR_UNSUPPORTED = -5, /* valid arguments this entry point does not take  */
   AWQ_ERR_WORKSPACE = -6,   /* workspace smaller than awq_gemm_workspace_bytes */
   AWQ_ERR_HIP = -7,         /* the HIP runtime reported an error at launch     */
-  AWQ_ERR_SCRATCH = -8      /* awq_gemm_noalloc: shape needs more than its scratch */
+  AWQ_ERR_SCRATCH = -8,     /* awq_gemm_noalloc: shape needs more than its scratch */
+  AWQ_ERR_OPTION = -9       /* an option (activation, top_k, slots) out of range */
+};
+
+/* Activations of the fused layers' epilogue, in fp32 on the sum. */
+enum awq_activation {
+  AWQ_ACT_NONE = 0,
+  AWQ_ACT_RELU = 1,
+  AWQ_ACT_SILU = 2,     /* v / (1 + exp(-v))                                         */
+  AWQ_ACT_GELU = 3,     /* v (1 + erf(v / sqrt 2)) / 2                               */
+  AWQ_ACT_GELU_TANH = 4 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2         */
 };
 
 /*
@@ -293,6 +303,103 @@ int awq_clip_search(const void* x, const void* w, int32_t M, int32_t N, int32_t 
                     int32_t zero_point, const float* ratios, int32_t count, void* w_clipped, int32_t* choice,
                     void* workspace, size_t workspace_bytes, void* stream);
 size_t awq_clip_search_workspace_bytes(int32_t count, int32_t M, int32_t N, int32_t K, int32_t group_size);
+
+/*
+ * awq_linear_fused - the quantized linear layer with its epilogue, any M >= 1:
+ *   y[m][n] = act(sum_k x[m][k] w'[n][k] + bias[n]) + residual[m][n]
+ * or, gated (gate and up packed as one weight of N = 2 F rows, the gate's
+ * first, as the fused gate_up projection stores them), F outputs per token:
+ *   y[m][f] = act(g[m][f] + bias[f]) * (u[m][f] + bias[F + f]) + residual[m][f]
+ * ("AI-Research-SKILLs AWQ 高级使用指南", section 层融合: gate and up fused; the
+ * MLP's activation, the bias and the residual stream are what a decoder
+ * block puts around the layer.)  Sums, bias, activation, product and residual
+ * are fp32; the output is rounded once to fp16.  Weights are exact (q - z
+ * times the group scale on fp32 sums) up to 8 tokens and rounded once to fp16
+ * above, as awq_gemm's.
+ * x         in   fp16, row m at x + m * ldx; bias fp16 [N] or NULL.
+ * residual  in   fp16, row m at residual + m * ldr, or NULL.
+ * y         out  fp16, row m at y + m * ldy; must not overlap an input, except
+ *                that it may be the residual itself (same address and stride).
+ * Strides are in elements, multiples of 8 and at least the row.  N a multiple
+ * of 8 (gated: of 16); M <= 2^24.
+ * workspace: awq_linear_fused_workspace_bytes() bytes (NULL when 0), under the
+ * contract of awq_gemm's workspace: its first 512 KiB are zero at first use and
+ * every call leaves them zero, so both share one buffer in stream order.
+ */
+int awq_linear_fused(const void* x, int32_t ldx, const uint32_t* qweight, const void* scales, const uint32_t* qzeros,
+                     const void* bias, int32_t activation, int32_t gated, const void* residual, int32_t ldr, void* y,
+                     int32_t ldy, int32_t M, int32_t N, int32_t K, int32_t group_size, int32_t zero_point,
+                     void* workspace, size_t workspace_bytes, void* stream);
+size_t awq_linear_fused_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t group_size, int32_t gated);
+
+/*
+ * awq_route_experts - the router of a mixture-of-experts layer.  For each of T
+ * tokens the top_k largest of its E logits, the lower index first among equal
+ * ones, and their weights: with m the largest logit,
+ *   w_j = exp(l_j - m) / S,  S = the sum of exp(l - m) over the chosen logits
+ * (renormalize != 0) or over all E, in fp32.  Slot t * top_k + j is token t's
+ * j-th choice.  A logit of -inf or NaN is masked: never chosen and of weight 0;
+ * a slot left without an expert (a token with fewer than top_k logits that are
+ * not masked, all of them for a token to skip) has id -1, weight 0 and
+ * position -1.  Logits of +inf share the weight equally.
+ * logits     in   fp16 or (fp32_logits != 0) fp32, row t at logits + t * ld elements, ld >= E.
+ * ids        out  int32 [T][top_k];  weights out fp32 [T][top_k].
+ * offsets    out  int32 [E + 1]: the routed slots sorted by expert, and by slot
+ *                 within one, put expert e's at offsets[e] .. offsets[e + 1] - 1.
+ * rows       out  int32 [T * top_k]: the slot at each place of that order, -1 past offsets[E].
+ * positions  out  int32 [T][top_k]: each slot's place in that order.
+ * 1 <= E <= 1024, top_k <= min(E, 64), T * top_k <= 2^24.  Deterministic.
+ * workspace: awq_route_experts_workspace_bytes() bytes, contents not needed
+ * before or after (NULL when 0).
+ */
+int awq_route_experts(const void* logits, int32_t ld, int32_t fp32_logits, int32_t T, int32_t E, int32_t top_k,
+                      int32_t renormalize, int32_t* ids, float* weights, int32_t* offsets, int32_t* rows,
+                      int32_t* positions, void* workspace, size_t workspace_bytes, void* stream);
+size_t awq_route_experts_workspace_bytes(int32_t T, int32_t E);
+
+/*
+ * awq_linear_experts - the quantized layers of E experts over rows grouped by
+ * expert: expert e multiplies rows offsets[e] .. offsets[e + 1] - 1 (ragged,
+ * known on the device only) with its own packed weight, and the epilogue of
+ * awq_linear_fused (bias, activation, gate) follows:
+ *   y[r] = act(x[src(r)] . W'_e^T + bias_e) [* (x[src(r)] . U'_e^T + ...)]
+ * src(r) = rows[r] / slots_per_row (rows as awq_route_experts leaves them,
+ * slots_per_row = top_k: the slot's token), or r with rows NULL.
+ * qweight, scales, qzeros  in  [E] packed weights of one shape, one after the other.
+ * bias     in   fp16 [E][N] or NULL.
+ * offsets  in   int32 [E + 1] (device), ascending, offsets[E] <= R; values are
+ *               clamped to [0, R], rows to x's x_rows rows, so that wrong ones
+ *               give wrong results but never lead outside the buffers.
+ * y        out  fp16, row r at y + r * ldy, r < offsets[E]; rows past it are left as they are.
+ * R rows at most (R = T * top_k after a router), 1 <= R <= 2^24, E <= 1024; the rest
+ * as in awq_linear_fused; workspace likewise, awq_linear_experts_workspace_bytes().
+ */
+int awq_linear_experts(const void* x, int32_t ldx, int32_t x_rows, const int32_t* rows, int32_t slots_per_row,
+                       const int32_t* offsets, int32_t R, int32_t E, const uint32_t* qweight, const void* scales,
+                       const uint32_t* qzeros, const void* bias, int32_t activation, int32_t gated, void* y,
+                       int32_t ldy, int32_t N, int32_t K, int32_t group_size, int32_t zero_point, void* workspace,
+                       size_t workspace_bytes, void* stream);
+size_t awq_linear_experts_workspace_bytes(int32_t R, int32_t E, int32_t N, int32_t K, int32_t group_size,
+                                          int32_t gated);
+
+/*
+ * awq_combine_experts - the experts' second layer and the weighted sum per token:
+ *   y[t] = sum_j weights[t][j] (x[positions[t][j]] . W'_e^T + bias_e) + residual[t]
+ * x holds the T * top_k rows sorted by expert (awq_linear_experts' output), e
+ * the expert whose range of offsets holds the row.  Slots with a negative
+ * position add nothing (a token without any: y = residual, or 0).  The sum
+ * runs over j in order, in fp32, on unrounded products; one rounding to fp16.
+ * positions, weights  in  int32, fp32 [T][top_k]; the other arguments as above.
+ * workspace: awq_combine_experts_workspace_bytes() bytes, under the contract
+ * of awq_gemm's workspace.
+ */
+int awq_combine_experts(const void* x, int32_t ldx, const int32_t* offsets, const int32_t* positions,
+                        const float* weights, int32_t T, int32_t top_k, int32_t E, const uint32_t* qweight,
+                        const void* scales, const uint32_t* qzeros, const void* bias, const void* residual,
+                        int32_t ldr, void* y, int32_t ldy, int32_t N, int32_t K, int32_t group_size,
+                        int32_t zero_point, void* workspace, size_t workspace_bytes, void* stream);
+size_t awq_combine_experts_workspace_bytes(int32_t T, int32_t top_k, int32_t E, int32_t N, int32_t K,
+                                           int32_t group_size);
 
 /* Static, NUL-terminated description of a status code. */
 const char* awq_strerror(int status);
