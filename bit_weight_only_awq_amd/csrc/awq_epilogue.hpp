@@ -5,6 +5,7 @@
 
 #include "awq_device.hpp"
 #include "awq_launch.hpp"
+#include "awq_launch_fused.hpp"
 
 namespace awq {
 
@@ -24,48 +25,128 @@ __device__ __forceinline__ float activate(float v, int act) {
   }
 }
 
+template <int ACT>
+__device__ __forceinline__ void activate8_as(float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = activate(v[k], ACT);
+}
+__device__ __forceinline__ void activate8(float (&v)[8], int act) {
+  switch (act) {
+    case 1: return activate8_as<1>(v);
+    case 2: return activate8_as<2>(v);
+    case 3: return activate8_as<3>(v);
+    case 4: return activate8_as<4>(v);
+    default: return;
+  }
+}
+
+// Eight consecutive outputs n .. n + 7 of row r: bias, activation, gate and
+// residual on the fp32 sums v (and u, the gate's partners), one rounding.
+template <bool GATED>
+__device__ __forceinline__ void finish8(float (&v)[8], const float (&u)[8], const ProductArgs& p, size_t wrow, int width,
+                                        int64_t r, int n, int act) {
+  half8_t b, ub, res, out;
+  if (p.bias) {
+    b = *reinterpret_cast<const half8_t*>(p.bias + wrow + n);
+    if constexpr (GATED) ub = *reinterpret_cast<const half8_t*>(p.bias + wrow + width + n);
+  }
+  if (p.residual) res = *reinterpret_cast<const half8_t*>(p.residual + r * p.ldr + n);
+  if (p.bias)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += (float)b[k];
+  activate8(v, act);
+  if constexpr (GATED) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= p.bias ? u[k] + (float)ub[k] : u[k];
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) out[k] = (_Float16)(p.residual ? v[k] + (float)res[k] : v[k]);
+  *reinterpret_cast<half8_t*>(p.y + r * p.ldy + n) = out;
+}
+
 // The rows of one workgroup: `count` consecutive rows from `row0`, all of
 // expert `expert` (count 0: the workgroup has nothing to do).
 struct RowTile {
   int expert, row0, count;
 };
 
-// Tile `slot` of the rows sorted by expert, cut into tiles of at most `tile`
-// rows of one expert each: expert e holds the rows offsets[e] ..
-// offsets[e + 1] - 1.  The counts live on the device only, so the host launches
-// row_tiles(R, E, tile) tiles and each wave finds its own here, 64 experts at a
-// time: lane l counts expert l's tiles, a prefix sum over the lanes places them,
-// and the first lane whose sum passes `slot` is the expert.  Offsets are
-// clamped into [0, R], so no wrong value leads outside the buffers.
-__device__ __forceinline__ RowTile find_row_tile(const int* __restrict__ offsets, int E, int R, int tile, int slot) {
-  if (offsets == nullptr) return RowTile{0, slot * tile, min(tile, R - slot * tile)};
-  const int lane = __lane_id();
-  int seen = 0;
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = e0 + lane;
-    int lo = 0, n = 0;
-    if (e < E) {
-      lo = min(max(offsets[e], 0), R);
-      n = max(min(offsets[e + 1], R) - lo, 0);
-    }
-    int sum = (n + tile - 1) / tile;  // inclusive prefix sum over the lanes
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(sum, d);
-      if (lane >= d) sum += up;
-    }
-    const unsigned long long past = __ballot(seen + sum > slot);
-    if (past != 0) {
-      const int l = __builtin_ctzll(past);
-      const int elo = __builtin_amdgcn_readlane(lo, l), en = __builtin_amdgcn_readlane(n, l);
-      const int before = seen + __builtin_amdgcn_readlane(sum, l) - (en + tile - 1) / tile;
-      const int first = (slot - before) * tile;
-      return RowTile{e0 + l, elo + first, min(tile, en - first)};
-    }
-    seen += __builtin_amdgcn_readlane(sum, 63);
-  }
-  return RowTile{0, 0, 0};
+// Sum of v over this lane and the lanes below it, in registers (DPP shifts
+// within 16 lanes, then the last lane of each 16 and 32 to those above).
+__device__ __forceinline__ int prefix_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31
+  return v;
 }
+
+// 64 experts' row ranges and tiles, one expert per lane.
+struct ExpertLanes {
+  int lo, n, tiles, sum;  // first row, rows, tiles, tiles of the lanes up to this one
+};
+__device__ __forceinline__ ExpertLanes expert_lanes(const int* __restrict__ offsets, int E, int R, int tile, int e0) {
+  const int e = e0 + __lane_id();
+  ExpertLanes x{0, 0, 0, 0};
+  if (e < E) {
+    x.lo = min(max(offsets[e], 0), R);
+    x.n = max(min(offsets[e + 1], R) - x.lo, 0);
+  }
+  x.tiles = (x.n + tile - 1) / tile;
+  x.sum = prefix_sum(x.tiles);
+  return x;
+}
+
+// The rows sorted by expert (expert e: offsets[e] .. offsets[e + 1] - 1), cut into
+// tiles of at most `tile` rows of one expert each, an expert's rows shared
+// evenly among its tiles (in multiples of `unit` rows).  The counts live on
+// the device only, so the host launches for row_tiles(R, E, tile) tiles and
+// each wave finds its own here, 64 experts at a time: lane l counts expert l's
+// tiles, a prefix sum over the lanes places them, and the first lane whose sum
+// passes the wanted tile is the expert.  Offsets are clamped into [0, R], so no
+// wrong value leads outside the buffers.  With `offsets` NULL one expert holds
+// all R rows.
+struct RowTiles {
+  const int* offsets;
+  int E, R, tile, unit, total;
+  ExpertLanes first;  // the first 64 experts
+
+  __device__ __forceinline__ RowTiles(const int* o, int experts, int rows, int t, int u)
+      : offsets(o), E(experts), R(rows), tile(t), unit(u), first{0, 0, 0, 0} {
+    if (offsets == nullptr) {
+      total = (R + tile - 1) / tile;
+      return;
+    }
+    first = expert_lanes(offsets, E, R, tile, 0);
+    total = __builtin_amdgcn_readlane(first.sum, 63);
+    for (int e0 = 64; e0 < E; e0 += 64)
+      total += __builtin_amdgcn_readlane(expert_lanes(offsets, E, R, tile, e0).sum, 63);
+  }
+
+  __device__ __forceinline__ RowTile cut(int expert, int lo, int n, int tiles, int nth) const {
+    const int each = ((n + tiles - 1) / tiles + unit - 1) / unit * unit;
+    return RowTile{expert, lo + nth * each, min(each, n - nth * each)};
+  }
+
+  // 0 <= slot < total
+  __device__ __forceinline__ RowTile operator[](int slot) const {
+    if (offsets == nullptr) return cut(0, 0, R, total, slot);
+    int seen = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      const ExpertLanes x = e0 == 0 ? first : expert_lanes(offsets, E, R, tile, e0);
+      const unsigned long long past = __ballot(seen + x.sum > slot);
+      if (past != 0) {
+        const int l = __builtin_ctzll(past);
+        const int tiles = __builtin_amdgcn_readlane(x.tiles, l);
+        return cut(e0 + l, __builtin_amdgcn_readlane(x.lo, l), __builtin_amdgcn_readlane(x.n, l), tiles,
+                   slot - (seen + __builtin_amdgcn_readlane(x.sum, l) - tiles));
+      }
+      seen += __builtin_amdgcn_readlane(x.sum, 63);
+    }
+    return RowTile{0, 0, 0};
+  }
+};
 
 // Most tiles that R rows of E experts can take: every expert but the last
 // has one row, or all rows fill tiles and every expert has one ragged tile.

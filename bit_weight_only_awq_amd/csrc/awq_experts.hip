@@ -8,6 +8,8 @@
 #include "awq_epilogue.hpp"
 #include "awq_launch_fused.hpp"
 
+#include <math.h>
+
 namespace awq {
 namespace {
 
@@ -27,7 +29,9 @@ __global__ __launch_bounds__(256) void product_kernel(PackedArgs w, ProductArgs 
   const int width = GATED ? w.N >> 1 : w.N, G = w.K >> gshift;
   const int columns = (width + 63) / 64;  // blocks of 64 columns
   const int slot = blockIdx.x / columns, n0 = ((blockIdx.x - slot * columns) * 4 + wave) * 16;
-  const RowTile t = find_row_tile(p.offsets, w.E, p.R, 16, slot);
+  const RowTiles tiles(p.offsets, w.E, p.R, 16, 16);
+  if (slot >= tiles.total) return;
+  const RowTile t = tiles[slot];
   if (t.count <= 0 || n0 >= width) return;
   const DecodeConsts kc;
   int r = t.row0 + min(li, t.count - 1);
@@ -88,9 +92,40 @@ __global__ __launch_bounds__(256) void product_kernel(PackedArgs w, ProductArgs 
   if (!part) *reinterpret_cast<half4_t*>(p.y + row * p.ldy + n) = out;
 }
 
+// part[row][n .. n + 3] summed over the K slices in order.
+__device__ __forceinline__ float4_t slices_sum(const float* __restrict__ part, int splits, int64_t rows, int N,
+                                               int64_t row, int n) {
+  float4_t v = *reinterpret_cast<const float4_t*>(part + row * N + n);
+  for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const float4_t*>(part + (s * rows + row) * N + n);
+  return v;
+}
+
+// The epilogue of a product whose K was split: four columns per thread.
+__global__ __launch_bounds__(256) void finish_kernel(const float* __restrict__ part, int splits, PackedArgs w,
+                                                     ProductArgs p) {
+  const int width = p.gated ? w.N >> 1 : w.N, quads = width >> 2;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = i / quads;
+  const int n = (int)(i - row * quads) * 4;
+  if (row >= p.R || (p.offsets && row >= min(p.offsets[w.E], p.R))) return;
+  float4_t v = slices_sum(part, splits, p.R, w.N, row, n);
+  float4_t up = {1.f, 1.f, 1.f, 1.f};
+  if (p.gated) up = slices_sum(part, splits, p.R, w.N, row, width + n);
+  half4_t out;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float o = activate(v[k], p.activation);
+    if (p.gated) o *= up[k];
+    if (p.residual) o += (float)p.residual[row * p.ldr + n + k];
+    out[k] = (_Float16)o;
+  }
+  *reinterpret_cast<half4_t*>(p.y + row * p.ldy + n) = out;
+}
+
 // y[t] = sum over the slots j, in order, of weights[t][j] * part[positions[t][j]]
 // + residual[t], four columns per thread.
-__global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ part, CombineArgs c, int R, int N) {
+__global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ part, int splits, CombineArgs c, int R,
+                                                      int N) {
   const int quads = N >> 2;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (int64_t)c.T * quads) return;
@@ -100,7 +135,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ 
   for (int j = 0; j < c.top_k; ++j) {
     const int at = c.positions[t * c.top_k + j];
     if (at < 0 || at >= R) continue;
-    sum += c.weights[t * c.top_k + j] * *reinterpret_cast<const float4_t*>(part + (int64_t)at * N + n);
+    sum += c.weights[t * c.top_k + j] * slices_sum(part, splits, R, N, at, n);
   }
   half4_t out;
 #pragma unroll
@@ -120,25 +155,91 @@ hipError_t launch_rows(const PackedArgs& w, const ProductArgs& p, float* part, h
   return hipGetLastError();
 }
 
-}  // namespace
+// More than this many rows per expert on average: matrix-core tiles.
+constexpr int kFewRows = 64;
 
-size_t product_workspace_bytes(int, int, int, int, bool) { return 0; }
+struct Plan {
+  bool tiles;
+  TilePlan tile;
+};
 
-hipError_t launch_product(const PackedArgs& w, const ProductArgs& p, void*, hipStream_t stream) {
-  return launch_rows(w, p, nullptr, stream);
+// Tile height and K split of the matrix-core tiles, from a time model: rounds of
+// workgroups over the compute units, each a tile's steps (a 64-channel step of
+// 256 rows 1.75 us, of 128 rows 1.0, of 64 rows 0.66: 0.29 + 0.18 per 32 rows)
+// and ~6 us to begin and end it (256 weight rows, gated or not); with K split, the fp32 partials written and
+// read at ~4 TB/s and one more launch.
+TilePlan plan_tiles(int R, int experts, int N, int K) {
+  const int steps = (K + 63) / 64, columns = (N + 255) / 256;
+  constexpr double kUnits = 256;
+  TilePlan best{256, 1, steps};
+  double best_us = 1e300;
+  for (int rows : {256, 128, 64}) {
+    // ragged experts end in half a tile each on average
+    const double tiles = experts == 1 ? (R + rows - 1) / rows : experts * ((double)R / experts / rows + 0.5);
+    const double height = R / tiles / 32;
+    const double step_us = 0.29 + 0.18 * (experts == 1 ? ceil(height) : height < 2 ? 2 : height);
+    for (int s = 1; s <= 16 && s <= steps; ++s) {
+      const int per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
+      const double rounds = ceil(tiles * columns * splits / kUnits);
+      const double us = rounds * (per * step_us + 6.0) + (splits > 1 ? splits * (double)R * N * 8 / 4e6 + 3.0 : 0.0);
+      if (us < best_us) best_us = us, best = TilePlan{rows, splits, per};
+    }
+  }
+  return best;
 }
 
-size_t combine_workspace_bytes(int T, int top_k, int, int N, int) {
-  return gemm_counter_bytes() + (size_t)T * top_k * N * 4;
+Plan plan_product(int R, int E, int N, int K) {
+  const int experts = E == 0 ? 1 : E < R ? E : R;  // E = 0: one expert, R rows known to the host
+  if (R / experts <= kFewRows) return Plan{false, {0, 1, 0}};
+  return Plan{true, plan_tiles(R, experts, N, K)};
+}
+
+size_t part_bytes(const Plan& plan, int R, int N) {
+  return gemm_counter_bytes() + (size_t)(plan.tiles ? plan.tile.splits : 1) * R * N * 4;
+}
+
+float* part_of(void* workspace) {
+  return reinterpret_cast<float*>(static_cast<char*>(workspace) + gemm_counter_bytes());
+}
+
+hipError_t launch_planned(const PackedArgs& w, const ProductArgs& p, const Plan& plan, float* part,
+                          hipStream_t stream) {
+  return plan.tiles ? launch_tiles(w, p, log2_group(w.group_size), plan.tile, part, stream)
+                    : launch_rows(w, p, part, stream);
+}
+
+}  // namespace
+
+size_t product_workspace_bytes(int R, int E, int N, int K, bool) {
+  const Plan plan = plan_product(R, E, N, K);
+  return plan.tiles && plan.tile.splits > 1 ? part_bytes(plan, R, N) : 0;
+}
+
+hipError_t launch_product(const PackedArgs& w, const ProductArgs& p, void* workspace, hipStream_t stream) {
+  const Plan plan = plan_product(p.R, p.offsets ? w.E : 0, w.N, w.K);
+  if (!plan.tiles || plan.tile.splits <= 1) return launch_planned(w, p, plan, nullptr, stream);
+  float* part = part_of(workspace);
+  const hipError_t e = launch_planned(w, p, plan, part, stream);
+  if (e != hipSuccess) return e;
+  const int64_t quads = (int64_t)p.R * ((p.gated ? w.N / 2 : w.N) / 4);
+  hipLaunchKernelGGL(finish_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, part, plan.tile.splits,
+                     w, p);
+  return hipGetLastError();
+}
+
+size_t combine_workspace_bytes(int T, int top_k, int E, int N, int K) {
+  return part_bytes(plan_product(T * top_k, E, N, K), T * top_k, N);
 }
 
 hipError_t launch_combine(const PackedArgs& w, const ProductArgs& p, const CombineArgs& c, void* workspace,
                           hipStream_t stream) {
-  float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + gemm_counter_bytes());
-  const hipError_t e = launch_rows(w, p, part, stream);
+  const Plan plan = plan_product(p.R, w.E, w.N, w.K);
+  float* part = part_of(workspace);
+  const hipError_t e = launch_planned(w, p, plan, part, stream);
   if (e != hipSuccess) return e;
   const int64_t quads = (int64_t)c.T * (w.N / 4);
-  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, part, c, p.R, w.N);
+  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, part,
+                     plan.tiles ? plan.tile.splits : 1, c, p.R, w.N);
   return hipGetLastError();
 }
 

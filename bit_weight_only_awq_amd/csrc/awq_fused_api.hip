@@ -17,8 +17,12 @@ constexpr int32_t kMaxRows = 1 << 24;     // tokens, slots: keeps launch grids a
 constexpr int32_t kMaxExperts = 1024;
 constexpr int32_t kMaxTopK = 64;
 
-// A row stride: at least the row, rows 16-byte aligned.
-bool stride_ok(int32_t ld, int32_t row) { return ld >= row && (ld & 7) == 0; }
+// A row stride: at least the row, rows 16-byte aligned, a tile of 256 rows
+// within the kernels' 32-bit byte offsets.
+bool stride_ok(int32_t ld, int32_t row) { return ld >= row && ld <= kMaxDim && (ld & 7) == 0; }
+
+// Gathered rows of x are addressed with 31-bit byte offsets from its first.
+bool gather_ok(int32_t rows, int32_t ld) { return (int64_t)rows * ld < ((int64_t)1 << 30); }
 
 // The weight's shape and pointers, the epilogue's options and pointers: what
 // every product checks.
@@ -120,7 +124,8 @@ int awq_linear_experts(const void* x, int32_t ldx, int32_t x_rows, const int32_t
   int st = check_product(N, K, group_size, zero_point, qweight, scales, qzeros, bias, activation, gated, nullptr, 0, x,
                          ldx, y, ldy);
   if (st != AWQ_OK) return st;
-  if (R < 1 || R > kMaxRows || E < 1 || E > kMaxExperts || x_rows < 1 || x_rows > kMaxRows || (!rows && x_rows < R))
+  if (R < 1 || R > kMaxRows || E < 1 || E > kMaxExperts || x_rows < 1 || x_rows > kMaxRows ||
+      (rows ? !gather_ok(x_rows, ldx) : x_rows < R))
     return AWQ_ERR_SHAPE;
   if (rows && slots_per_row < 1) return AWQ_ERR_OPTION;
   if (!offsets) return AWQ_ERR_NULL;

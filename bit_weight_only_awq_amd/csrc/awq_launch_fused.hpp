@@ -47,6 +47,14 @@ struct CombineArgs {
   int64_t ldy;
 };
 
+// Matrix-core tiles (awq_expert_tiles.hip): most rows of a tile, K split.  With
+// `part` the raw sums (the bias in slice 0's) go to part[split][R][N].
+struct TilePlan {
+  int rows, splits, steps_per_split;
+};
+hipError_t launch_tiles(const PackedArgs& w, const ProductArgs& p, int gshift, const TilePlan& plan, float* part,
+                        hipStream_t stream);
+
 size_t product_workspace_bytes(int R, int E, int N, int K, bool gated);
 hipError_t launch_product(const PackedArgs& w, const ProductArgs& p, void* workspace, hipStream_t stream);
 
