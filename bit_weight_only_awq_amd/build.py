@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 ARCH = "gfx950"
 SOURCES = ("awq_api.hip", "awq_pack.hip", "awq_gemv.hip", "awq_gemv_small.hip", "awq_gemm.hip", "awq_scale.hip",
-           "awq_noalloc.hip", "awq_experts.hip", "awq_expert_tiles.hip", "awq_route.hip", "awq_fused_api.hip")
+           "awq_noalloc.hip", "awq_experts.hip", "awq_expert_tiles.hip", "awq_expert_stream.hip",
+           "awq_fused_gemv.hip", "awq_fused_few.hip", "awq_route.hip", "awq_fused_api.hip")
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

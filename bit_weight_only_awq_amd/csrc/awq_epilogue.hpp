@@ -125,6 +125,7 @@ struct RowTiles {
   }
 
   __device__ __forceinline__ RowTile cut(int expert, int lo, int n, int tiles, int nth) const {
+    if (tiles == 1) return RowTile{expert, lo, n};
     const int each = ((n + tiles - 1) / tiles + unit - 1) / unit * unit;
     return RowTile{expert, lo + nth * each, min(each, n - nth * each)};
   }

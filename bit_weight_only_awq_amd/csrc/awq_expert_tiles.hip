@@ -118,6 +118,7 @@ __global__ __launch_bounds__(256) void tile_kernel(PackedArgs w, ProductArgs p, 
   uint32_t xoff[MAXT];
   int xlast = 0;  // 32-row tiles - 1
   const int xrow = 8 * wave + (lane >> 3), xchunk = swz_chunk(xrow, lane & 7);  // 32 j more rows: the same chunk
+  const uint32_t xpast = xchunk >= 4 ? kOutOfRange : 0u;
   // W: lane (i, h) = (lane % 32, lane / 32) of this wave holds row i of each of
   // its NB blocks of 32 weight rows; rows past N lie past the resources and read as 0
   const uint32_t woff = (uint32_t)fi * (K >> 1) + fh * 16;
@@ -150,10 +151,8 @@ __global__ __launch_bounds__(256) void tile_kernel(PackedArgs w, ProductArgs p, 
   // past K is sent out of range by its lane offset, and past the slice's last
   // step the whole buffer is empty (its loads read 0 and cost no traffic).
   auto load_x1 = [&](int step, int s1, int buf, int j) __attribute__((always_inline)) {
-    uint32_t off = xoff[j];
-    if constexpr (KTAIL) {
-      if (step * BK + 8 * xchunk >= K) off = kOutOfRange;
-    }
+    // (K a multiple of 32: the last step's second half)
+    const uint32_t off = xoff[j] | (KTAIL && step == nsteps - 1 ? xpast : 0u);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         make_rsrc(xbase, step < s1 ? xbytes : 0u), (__attribute__((address_space(3))) void*)((buf ? lx1 : lx0) + 1024 * (wave + 4 * j)), 16, off, step * BK * 2,
         0, 0);
@@ -168,7 +167,7 @@ __global__ __launch_bounds__(256) void tile_kernel(PackedArgs w, ProductArgs p, 
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       r.w[b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                             make_rsrc(wbase[b], step < s1 ? wbytes[b] : 0u), !KTAIL || k0 < K ? woff : kOutOfRange, step * (BK / 2), 0));
+                                             make_rsrc(wbase[b], step < s1 ? wbytes[b] : 0u), woff | (KTAIL && k0 >= K ? kOutOfRange : 0u), step * (BK / 2), 0));
       r.s[b] = __builtin_amdgcn_raw_buffer_load_b16(rs[b], soff + grp * 16, 0, 0);
       r.z[b] = ZP ? __builtin_amdgcn_raw_buffer_load_b32(rz[b], zoff + grp * 4, 0, 0) : 0u;
     }
@@ -259,10 +258,12 @@ __global__ __launch_bounds__(256) void tile_kernel(PackedArgs w, ProductArgs p, 
       interleave();
       __builtin_amdgcn_sched_barrier(0);
     };
+    float zero = 0.0f;
+    asm volatile("" : "+v"(zero));  // (a constant would be kept as a tuple of registers, or spilled as one)
 #pragma unroll
     for (int a = 0; a < WMT; ++a)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) acc[a][b] = float16_t(0.0f);
+      for (int b = 0; b < NB; ++b) acc[a][b] = float16_t(zero);
     load_x(x.s0 + 1, 1);
     prep(w0);
     read_a(0, 0, 0);

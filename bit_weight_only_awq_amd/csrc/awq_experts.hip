@@ -15,83 +15,6 @@ namespace {
 
 int log2_group(int g) { return g == 32 ? 5 : g == 64 ? 6 : g == 128 ? 7 : 8; }
 
-// One wave: 16 output columns (and their gate's partners) of a tile of 16
-// rows, all of K.  v_mfma_f32_16x16x32_f16 with the weights as the A operand:
-// lane (i, h) = (lane % 16, lane / 16) holds 8 channels of weight row i and
-// of token row i, and the sums of token i with weight rows 4 h .. 4 h + 3.  The
-// channels of a 128-channel step go to the lanes 32 at a time (one 128-bit
-// load of packed words), the same way for both operands.
-template <bool ZP, bool GATED>
-__global__ __launch_bounds__(256) void product_kernel(PackedArgs w, ProductArgs p, int gshift, float* part) {
-  constexpr int NB = GATED ? 2 : 1;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int li = lane & 15, lh = lane >> 4;
-  const int width = GATED ? w.N >> 1 : w.N, G = w.K >> gshift;
-  const int columns = (width + 63) / 64;  // blocks of 64 columns
-  const int slot = blockIdx.x / columns, n0 = ((blockIdx.x - slot * columns) * 4 + wave) * 16;
-  const RowTiles tiles(p.offsets, w.E, p.R, 16, 16);
-  if (slot >= tiles.total) return;
-  const RowTile t = tiles[slot];
-  if (t.count <= 0 || n0 >= width) return;
-  const DecodeConsts kc;
-  int r = t.row0 + min(li, t.count - 1);
-  if (p.rows) r = min(max(p.rows[r] / p.slots_per_row, 0), p.x_rows - 1);
-  const _Float16* x = p.x + r * p.ldx;
-  const size_t e = t.expert;
-  const uint32_t* qw[NB];
-  const uint16_t* sc[NB];
-  const uint32_t* qz[NB];
-  int zs[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int n = b * width + min(n0 + li, width - 1);
-    qw[b] = w.qweight + (e * w.N + n) * (w.K >> 3);
-    sc[b] = w.scales + e * w.N * G + scale_index(n, 0, G);
-    qz[b] = ZP ? w.qzeros + e * (w.N >> 3) * G + zero_word_index(n, 0, G) : nullptr;
-    zs[b] = 4 * (n & 7);
-  }
-  float4_t acc[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) acc[b] = float4_t{0.f, 0.f, 0.f, 0.f};
-  for (int k = 32 * lh; k < ((w.K + 127) & ~127); k += 128) {
-    const bool in = k < w.K;
-    u32x4 xv[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      xv[i] = in ? *reinterpret_cast<const u32x4*>(x + k + 8 * i) : u32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int g = min(k, w.K - 1) >> gshift;
-      const u32x4 wv = in ? *reinterpret_cast<const u32x4*>(qw[b] + (k >> 3)) : u32x4{0, 0, 0, 0};
-      const ZeroBias zb = zero_bias(ZP ? (qz[b][g] >> zs[b]) & 15u : 8u);
-      const half2_t s2 = splat2(__builtin_bit_cast(_Float16, sc[b][(size_t)g * 8]));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(decode_word_scaled(wv[i], zb, kc, s2), as_half8(xv[i]), acc[b],
-                                                        0, 0, 0);
-    }
-  }
-  const int n = n0 + 4 * lh;
-  if (li >= t.count || n >= width) return;
-  const int64_t row = t.row0 + li;
-  half4_t out;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float v = acc[0][j];
-    if (p.bias) v += (float)p.bias[e * w.N + n + j];
-    v = activate(v, p.activation);
-    if constexpr (GATED) {
-      float u = acc[NB - 1][j];
-      if (p.bias) u += (float)p.bias[e * w.N + width + n + j];
-      v *= u;
-    }
-    if (p.residual) v += (float)p.residual[row * p.ldr + n + j];
-    if (part) part[row * width + n + j] = v;
-    out[j] = (_Float16)v;
-  }
-  if (!part) *reinterpret_cast<half4_t*>(p.y + row * p.ldy + n) = out;
-}
-
 // part[row][n .. n + 3] summed over the K slices in order.
 __device__ __forceinline__ float4_t slices_sum(const float* __restrict__ part, int splits, int64_t rows, int N,
                                                int64_t row, int n) {
@@ -146,22 +69,19 @@ __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ 
   *reinterpret_cast<half4_t*>(c.y + t * c.ldy + n) = out;
 }
 
-hipError_t launch_rows(const PackedArgs& w, const ProductArgs& p, float* part, hipStream_t stream) {
-  const int width = p.gated ? w.N / 2 : w.N, gs = log2_group(w.group_size);
-  const dim3 grid((width + 63) / 64 * (p.offsets ? row_tiles(p.R, w.E, 16) : (p.R + 15) / 16));
-  const auto kernel = w.qzeros ? (p.gated ? product_kernel<true, true> : product_kernel<true, false>)
-                               : (p.gated ? product_kernel<false, true> : product_kernel<false, false>);
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, w, p, gs, part);
-  return hipGetLastError();
-}
-
-// More than this many rows per expert on average: matrix-core tiles.
-constexpr int kFewRows = 64;
-
+// How a product runs, by the rows per expert (on average: the host does not
+// know the counts): a few, the weight stream, or the matrix cores.
 struct Plan {
-  bool tiles;
+  enum Kind { kFew, kStream, kTiles } kind;
+  int few_rows;
+  StreamPlan stream;
   TilePlan tile;
+  int splits() const { return kind == kStream ? stream.splits : kind == kTiles ? tile.splits : 1; }
 };
+
+// One row per workgroup set: a single token, or so few rows that experts with
+// two are rare (their weights are then read twice, the second time from L2).
+bool one_row_each(int R, int E) { return R == 1 || 2 * R <= E; }
 
 // Tile height and K split of the matrix-core tiles, from a time model: rounds of
 // workgroups over the compute units, each a tile's steps (a 64-channel step of
@@ -188,14 +108,55 @@ TilePlan plan_tiles(int R, int experts, int N, int K) {
   return best;
 }
 
+// Weight-stream tiles, by how many there are.  Many (c: 128-row columns times
+// row tiles): 4 waves side by side.  Fewer: the waves of a workgroup split K, and
+// then the workgroups do, until about 256 of them run.  us on the 7B shapes,
+// the variant chosen / the one on the other side of the rule:
+//   13 x 11008 -> 4096: 2 x 2 waves, K in 4: 14.9 / 2 x 4 waves, no split: 23.0
+//   16 x 4096 -> 4096: 2 x 4: 9.1 / 4 x 1: 16.8;  16 x 4096 -> 11008: 11.6 / 17.9
+//   48 tokens x 6 of 64, 2048 -> 2816: 4 x 1: 44.9 / 2 x 2: 53.5
+//   61 x 4096 -> 11008 (32-row tiles): 4 x 2: 17.9 / 4 x 1: 20.8; 64 rows: 22.2
+//   100 x 4096 -> 4096: 4 x 2, K in 2: 14.0 / 4 x 1: 27
+//   200 x 4096 -> 11008: 4 x 1: 42.5 / 4 x 2: 46.5
+StreamPlan plan_stream(int R, int experts, int N, int K) {
+  const double each = (double)R / experts;
+  auto plan = [&](int rows, int cw, int kw, int splits) {
+    // no empty slice: every slice but the last has the same number of stages
+    const int channels = (rows <= 32 ? 256 : 128) * kw, stages = (K + channels - 1) / channels;
+    if (splits > stages / 2) splits = stages / 2;
+    if (splits < 1) splits = 1;
+    const int per = (stages + splits - 1) / splits;
+    return StreamPlan{rows, cw, kw, (stages + per - 1) / per};
+  };
+  const int c64 = experts * ((N + 63) / 64);
+  if (each <= (experts == 1 ? 16 : 10) || (experts == 1 && R <= 32 && K <= 6144 && 2 * c64 <= 160)) {
+    const int c = each <= 16 ? c64 : 2 * c64;
+    if (c >= 512) return plan(16, 4, 1, 1);
+    if (c >= 224) return plan(16, 2, 2, 1);
+    if (c >= 96 || K <= 6144) return plan(16, 2, 4, 1);
+    return plan(16, 2, 2, c >= 64 ? 4 : 8);
+  }
+  if (experts > 1 && each > 40) return plan(64, 4, 1, 1);
+  const double tiles = experts == 1 ? (R + 31) / 32 : experts * (each / 32 + 0.5);
+  const double c = tiles * ((N + 127) / 128);
+  if (c >= 320) return plan(32, 4, 1, 1);
+  if (c >= 160) return plan(32, 4, 2, 1);
+  return plan(32, 4, 2, c > 128 ? 1 : c > 80 ? 2 : c > 40 ? 4 : 8);
+}
+
 Plan plan_product(int R, int E, int N, int K) {
   const int experts = E == 0 ? 1 : E < R ? E : R;  // E = 0: one expert, R rows known to the host
-  if (R / experts <= kFewRows) return Plan{false, {0, 1, 0}};
-  return Plan{true, plan_tiles(R, experts, N, K)};
+  const double each = (double)R / experts;
+  // (the first two kernels address an expert's packed words with 31 bits)
+  if ((int64_t)N * K < ((int64_t)1 << 32)) {
+    if (each <= (E == 0 ? 8 : 2)) return Plan{Plan::kFew, E == 0 && R > 4 ? 8 : 4, {}, {}};
+    if (each <= (E == 0 ? 256 : 64)) return Plan{Plan::kStream, 0, plan_stream(R, experts, N, K), {}};
+  }
+  return Plan{Plan::kTiles, 0, {}, plan_tiles(R, experts, N, K)};
 }
 
 size_t part_bytes(const Plan& plan, int R, int N) {
-  return gemm_counter_bytes() + (size_t)(plan.tiles ? plan.tile.splits : 1) * R * N * 4;
+  return gemm_counter_bytes() + (size_t)plan.splits() * R * N * 4;
 }
 
 float* part_of(void* workspace) {
@@ -204,42 +165,49 @@ float* part_of(void* workspace) {
 
 hipError_t launch_planned(const PackedArgs& w, const ProductArgs& p, const Plan& plan, float* part,
                           hipStream_t stream) {
-  return plan.tiles ? launch_tiles(w, p, log2_group(w.group_size), plan.tile, part, stream)
-                    : launch_rows(w, p, part, stream);
+  const int gs = log2_group(w.group_size);
+  switch (plan.kind) {
+    case Plan::kFew: return launch_few(w, p, gs, plan.few_rows, part, stream);
+    case Plan::kStream: return launch_stream(w, p, gs, plan.stream, part, stream);
+    default: return launch_tiles(w, p, gs, plan.tile, part, stream);
+  }
 }
 
 }  // namespace
 
 size_t product_workspace_bytes(int R, int E, int N, int K, bool) {
+  if (one_row_each(R, E)) return 0;
   const Plan plan = plan_product(R, E, N, K);
-  return plan.tiles && plan.tile.splits > 1 ? part_bytes(plan, R, N) : 0;
+  return plan.splits() > 1 ? part_bytes(plan, R, N) : 0;
 }
 
 hipError_t launch_product(const PackedArgs& w, const ProductArgs& p, void* workspace, hipStream_t stream) {
+  if (one_row_each(p.R, p.offsets ? w.E : 0)) return launch_fused_gemv(w, p, log2_group(w.group_size), stream);
   const Plan plan = plan_product(p.R, p.offsets ? w.E : 0, w.N, w.K);
-  if (!plan.tiles || plan.tile.splits <= 1) return launch_planned(w, p, plan, nullptr, stream);
+  if (plan.splits() <= 1) return launch_planned(w, p, plan, nullptr, stream);
   float* part = part_of(workspace);
   const hipError_t e = launch_planned(w, p, plan, part, stream);
   if (e != hipSuccess) return e;
   const int64_t quads = (int64_t)p.R * ((p.gated ? w.N / 2 : w.N) / 4);
-  hipLaunchKernelGGL(finish_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, part, plan.tile.splits,
-                     w, p);
+  hipLaunchKernelGGL(finish_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, part, plan.splits(), w, p);
   return hipGetLastError();
 }
 
 size_t combine_workspace_bytes(int T, int top_k, int E, int N, int K) {
+  if (one_row_each(T * top_k, E)) return 0;
   return part_bytes(plan_product(T * top_k, E, N, K), T * top_k, N);
 }
 
 hipError_t launch_combine(const PackedArgs& w, const ProductArgs& p, const CombineArgs& c, void* workspace,
                           hipStream_t stream) {
+  if (one_row_each(p.R, w.E)) return launch_combine_gemv(w, p, c, log2_group(w.group_size), stream);
   const Plan plan = plan_product(p.R, w.E, w.N, w.K);
   float* part = part_of(workspace);
   const hipError_t e = launch_planned(w, p, plan, part, stream);
   if (e != hipSuccess) return e;
   const int64_t quads = (int64_t)c.T * (w.N / 4);
   hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, part,
-                     plan.tiles ? plan.tile.splits : 1, c, p.R, w.N);
+                     plan.splits(), c, p.R, w.N);
   return hipGetLastError();
 }
 

@@ -55,6 +55,23 @@ struct TilePlan {
 hipError_t launch_tiles(const PackedArgs& w, const ProductArgs& p, int gshift, const TilePlan& plan, float* part,
                         hipStream_t stream);
 
+// Weight-stream tiles (awq_expert_stream.hip): most rows of a tile (16, 32, 64),
+// waves along the weight rows and along K, K split across workgroups.
+struct StreamPlan {
+  int rows, cw, kw, splits;
+};
+hipError_t launch_stream(const PackedArgs& w, const ProductArgs& p, int gshift, const StreamPlan& plan, float* part,
+                         hipStream_t stream);
+
+// One row at a time (awq_fused_gemv.hip): R rows, each with its expert's whole
+// weight; and T tokens' weighted sums.
+hipError_t launch_fused_gemv(const PackedArgs& w, const ProductArgs& p, int gshift, hipStream_t stream);
+hipError_t launch_combine_gemv(const PackedArgs& w, const ProductArgs& p, const CombineArgs& c, int gshift,
+                               hipStream_t stream);
+
+// A few rows (awq_fused_few.hip): tiles of at most 4 or 8 rows; N * K < 2^32.
+hipError_t launch_few(const PackedArgs& w, const ProductArgs& p, int gshift, int rows, float* part, hipStream_t stream);
+
 size_t product_workspace_bytes(int R, int E, int N, int K, bool gated);
 hipError_t launch_product(const PackedArgs& w, const ProductArgs& p, void* workspace, hipStream_t stream);
 
