@@ -494,24 +494,35 @@ def quantize_awq(w: torch.Tensor, x: torch.Tensor, q_group_size: int = 128, zero
     return QuantizedLinear(pack(ws, q_group_size, zero_point), res.scale, res)
 
 
-def _rows2d(t: torch.Tensor, width: int, what: str):
-    """(address, row stride) of a float16 matrix on the GPU whose rows are contiguous and 16-byte aligned."""
-    if t.dtype != torch.float16 or t.dim() != 2 or t.shape[1] != width:
-        raise ValueError(f"{what} must be a 2-D float16 tensor with {width} columns")
+# The calls below serve single tokens, where the kernel takes a few microseconds and the binding counts: one library
+# call each, the checks on attributes only, the stream's handle without its Python object where torch offers that.
+_F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _handle(t: torch.Tensor) -> int:
+    """The handle of the current stream of a GPU tensor's device."""
+    return _raw_stream(t.get_device()) if _raw_stream is not None else _stream(t)
+
+
+def _rows2d(t: torch.Tensor, rows: Optional[int], width: int, what: str):
+    """(address, row stride) of a float16 matrix on the GPU whose rows are contiguous and do not overlap."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not _F16 or len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{what} must be a float16 tensor [{'rows' if rows is None else rows}, {width}]")
     if not t.is_cuda:
         raise ValueError("tensors passed to the AWQ kernels must live on the GPU")
-    ld, inner = t.stride()
-    if t.shape[0] == 1:
-        ld = (width + 7) & ~7
-    if (inner != 1 and width > 1) or ld < width:
+    ld = stride[0] if shape[0] > 1 else width
+    if (stride[1] != 1 and width > 1) or ld < width:
         raise ValueError(f"{what} must have contiguous rows that do not overlap")
     return t.data_ptr(), ld
 
 
 def _flat(t: Optional[torch.Tensor], shape, dtype, what: str) -> Optional[int]:
+    """Address of a contiguous GPU tensor of a given shape and type (None: NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what} must be a {str(dtype).split('.')[-1]} tensor of shape {tuple(shape)}")
     return _ptr(t)
 
@@ -523,13 +534,16 @@ def _activation(name: str) -> int:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}; got {name!r}") from None
 
 
-def _scratch(need: int, t: torch.Tensor, workspace: Optional[torch.Tensor]):
-    """(address, bytes) of the caller's workspace, or of the stream's own."""
-    if workspace is None:
-        if need == 0:
-            return None, 0
-        workspace = gemm_workspace(need, t.device)
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+def _with_workspace(call, need, where: str, workspace: Optional[torch.Tensor], t: torch.Tensor, stream: int) -> None:
+    """``call(address, bytes)`` with the caller's workspace, or else with the one of the current stream: the call says
+    itself when that is too small, and only then is its size (``need()``) asked for."""
+    ws = workspace if workspace is not None else _WORKSPACES.get((t.get_device(), stream))
+    st = call(None, 0) if ws is None else call(_ptr(ws), ws.numel() * ws.element_size())
+    if st == AWQ_ERR_WORKSPACE and workspace is None:
+        ws = gemm_workspace(int(need()), t.device)
+        st = call(ws.data_ptr(), ws.numel())
+    if st != AWQ_OK:
+        raise AwqError(st, where)
 
 
 def linear_fused(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor] = None, activation: str = "none",
@@ -539,27 +553,29 @@ def linear_fused(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor]
     ``pw``'s rows is the gate (``pack_fused([gate, up])``): act(gate) * up, half as many columns.  ``x``,
     ``residual`` and ``y`` may be 2-D views with a row stride (a multiple of 8 elements); ``y`` may be
     ``residual`` itself.  One rounding to fp16."""
-    lib = load_library()
-    x2 = x if x.dim() == 2 else x.reshape(-1, pw.K)
-    M, width = x2.shape[0], pw.N // 2 if gated else pw.N
-    xp, ldx = _rows2d(x2, pw.K, "x")
+    lib = _lib or load_library()
+    qweight, scales, qzeros, N, K, group_size, zero_point = pw
+    x2 = x if x.dim() == 2 else x.reshape(-1, K)
+    M, width = x2.shape[0], N // 2 if gated else N
+    xp, ldx = _rows2d(x2, None, K, "x")
     act = _activation(activation)
     rp, ldr = None, 0
     if residual is not None:
-        residual = residual if residual.dim() == 2 else residual.reshape(-1, width)
-        if residual.shape[0] != M:
-            raise ValueError(f"residual must have x's {M} rows")
-        rp, ldr = _rows2d(residual, width, "residual")
-    out = torch.empty((M, width), dtype=torch.float16, device=x.device) if y is None else y
-    if out.dim() != 2 or out.shape[0] != M:
-        raise ValueError(f"y must be [{M}, {width}]")
-    yp, ldy = _rows2d(out, width, "y")
-    need = lib.awq_linear_fused_workspace_bytes(M, pw.N, pw.K, pw.group_size, int(gated))
-    ws, ws_bytes = _scratch(need, x2, workspace)
-    st = lib.awq_linear_fused(xp, ldx, _ptr(pw.qweight), _ptr(pw.scales), _ptr(pw.qzeros) if pw.zero_point else None,
-                              _flat(bias, (pw.N,), torch.float16, "bias"), act, int(gated), rp, ldr, yp, ldy, M, pw.N,
-                              pw.K, pw.group_size, int(pw.zero_point), ws, ws_bytes, _stream(x2))
-    _check(st, "awq_linear_fused")
+        rp, ldr = _rows2d(residual if residual.dim() == 2 else residual.reshape(-1, width), M, width, "residual")
+    if y is None:
+        out = x2.new_empty((M, width))
+        yp, ldy = out.data_ptr(), width
+    else:
+        out = y
+        yp, ldy = _rows2d(y, M, width, "y")
+    bp = _flat(bias, (N,), _F16, "bias")
+    qp, sp, zp = _ptr(qweight), _ptr(scales), _ptr(qzeros) if zero_point else None
+    stream = _handle(x2)
+    _with_workspace(
+        lambda ws, n: lib.awq_linear_fused(xp, ldx, qp, sp, zp, bp, act, gated, rp, ldr, yp, ldy, M, N, K, group_size,
+                                           zero_point, ws, n, stream),
+        lambda: lib.awq_linear_fused_workspace_bytes(M, N, K, group_size, gated), "awq_linear_fused", workspace, x2,
+        stream)
     return out if y is not None or x.dim() == 2 else out.reshape(*x.shape[:-1], width)
 
 
@@ -582,8 +598,9 @@ def route_experts(logits: torch.Tensor, top_k: int, renormalize: bool = True,
     """The ``top_k`` largest of each token's expert logits (fp16 or fp32 [T, E]; the lower index first among equal
     ones), their softmax weights (over the chosen ones, or over all E without ``renormalize``), and the tokens'
     slots sorted by expert.  Logits of -inf or NaN are masked; a slot left without an expert has id -1."""
-    lib = load_library()
-    if logits.dim() != 2 or logits.dtype not in (torch.float16, torch.float32):
+    lib = _lib or load_library()
+    wide = logits.dtype is _F32
+    if logits.dim() != 2 or not (wide or logits.dtype is _F16):
         raise ValueError("logits must be a 2-D float16 or float32 tensor [T, E]")
     if not logits.is_cuda:
         raise ValueError("tensors passed to the AWQ kernels must live on the GPU")
@@ -595,19 +612,19 @@ def route_experts(logits: torch.Tensor, top_k: int, renormalize: bool = True,
         raise ValueError("logits must have contiguous rows")
     if not 1 <= top_k <= min(E, 64):
         raise AwqError(AWQ_ERR_OPTION, "awq_route_experts")
-    dev, slots = logits.device, T * top_k
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    rows = torch.empty(slots, dtype=torch.int32, device=dev)
-    positions = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    need = lib.awq_route_experts_workspace_bytes(T, E)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws, ws_bytes = _scratch(need, logits, workspace)
-    st = lib.awq_route_experts(logits.data_ptr(), ld, int(logits.dtype == torch.float32), T, E, top_k,
-                               int(renormalize), ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
-                               rows.data_ptr(), positions.data_ptr(), ws, ws_bytes, _stream(logits))
+    shape = (T, top_k)
+    ids = logits.new_empty(shape, dtype=_I32)
+    weights = logits.new_empty(shape, dtype=_F32)
+    offsets = logits.new_empty(E + 1, dtype=_I32)
+    rows = logits.new_empty(T * top_k, dtype=_I32)
+    positions = logits.new_empty(shape, dtype=_I32)
+    need = lib.awq_route_experts_workspace_bytes(T, E) if workspace is None else 0
+    if need:
+        workspace = logits.new_empty(need, dtype=torch.uint8)
+    st = lib.awq_route_experts(logits.data_ptr(), ld, wide, T, E, top_k, renormalize, ids.data_ptr(),
+                               weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), positions.data_ptr(),
+                               _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                               _handle(logits))
     _check(st, "awq_route_experts")
     return ExpertRoute(ids, weights, offsets, rows, positions)
 
@@ -639,37 +656,34 @@ def pack_experts(W, q_group_size: int = 128, zero_point: bool = True) -> PackedE
     return PackedExperts(qweight, scales, qzeros, E, N, K, q_group_size, bool(zero_point))
 
 
-def _check_route(route: ExpertRoute, pe: PackedExperts):
-    T, top_k = route.ids.shape
-    _flat(route.offsets, (pe.E + 1,), torch.int32, "route.offsets")
-    _flat(route.rows, (T * top_k,), torch.int32, "route.rows")
-    return T, top_k
-
-
 def linear_experts(x: torch.Tensor, pe: PackedExperts, route: ExpertRoute, bias: Optional[torch.Tensor] = None,
                    activation: str = "none", gated: bool = False, y: Optional[torch.Tensor] = None,
                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Every routed slot's token (fp16 ``x`` [T, K]) through its expert's layer and epilogue (``bias`` [E, N],
     ``gated`` as in ``linear_fused``): fp16 [T * top_k, N or N / 2], rows sorted by expert as ``route.rows`` says.
     Rows past ``route.offsets[E]`` (slots without an expert) are not written."""
-    lib = load_library()
-    T, top_k = _check_route(route, pe)
-    xp, ldx = _rows2d(x, pe.K, "x")
-    if x.shape[0] != T:
-        raise ValueError(f"x must have the route's {T} tokens")
-    R, width = T * top_k, pe.N // 2 if gated else pe.N
+    lib = _lib or load_library()
+    qweight, scales, qzeros, E, N, K, group_size, zero_point = pe
+    T, top_k = route.ids.shape
+    R, width = T * top_k, N // 2 if gated else N
+    op = _flat(route.offsets, (E + 1,), _I32, "route.offsets")
+    wp = _flat(route.rows, (R,), _I32, "route.rows")
+    xp, ldx = _rows2d(x, T, K, "x")
     act = _activation(activation)
-    out = torch.empty((R, width), dtype=torch.float16, device=x.device) if y is None else y
-    if out.dim() != 2 or out.shape[0] != R:
-        raise ValueError(f"y must be [{R}, {width}]")
-    yp, ldy = _rows2d(out, width, "y")
-    need = lib.awq_linear_experts_workspace_bytes(R, pe.E, pe.N, pe.K, pe.group_size, int(gated))
-    ws, ws_bytes = _scratch(need, x, workspace)
-    st = lib.awq_linear_experts(xp, ldx, T, route.rows.data_ptr(), top_k, route.offsets.data_ptr(), R, pe.E,
-                                _ptr(pe.qweight), _ptr(pe.scales), _ptr(pe.qzeros) if pe.zero_point else None,
-                                _flat(bias, (pe.E, pe.N), torch.float16, "bias"), act, int(gated), yp, ldy, pe.N, pe.K,
-                                pe.group_size, int(pe.zero_point), ws, ws_bytes, _stream(x))
-    _check(st, "awq_linear_experts")
+    if y is None:
+        out = x.new_empty((R, width))
+        yp, ldy = out.data_ptr(), width
+    else:
+        out = y
+        yp, ldy = _rows2d(y, R, width, "y")
+    bp = _flat(bias, (E, N), _F16, "bias")
+    qp, sp, zp = _ptr(qweight), _ptr(scales), _ptr(qzeros) if zero_point else None
+    stream = _handle(x)
+    _with_workspace(
+        lambda ws, n: lib.awq_linear_experts(xp, ldx, T, wp, top_k, op, R, E, qp, sp, zp, bp, act, gated, yp, ldy, N, K,
+                                             group_size, zero_point, ws, n, stream),
+        lambda: lib.awq_linear_experts_workspace_bytes(R, E, N, K, group_size, gated), "awq_linear_experts", workspace,
+        x, stream)
     return out
 
 
@@ -678,30 +692,28 @@ def combine_experts(h: torch.Tensor, pe: PackedExperts, route: ExpertRoute, bias
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The experts' second layer on the sorted rows ``h`` [T * top_k, K] and each token's weighted sum, plus
     ``residual`` [T, N]: fp16 [T, N], one rounding."""
-    lib = load_library()
-    T, top_k = _check_route(route, pe)
-    _flat(route.positions, (T, top_k), torch.int32, "route.positions")
-    _flat(route.weights, (T, top_k), torch.float32, "route.weights")
-    hp, ldh = _rows2d(h, pe.K, "h")
-    if h.shape[0] != T * top_k:
-        raise ValueError(f"h must have the route's {T * top_k} rows")
-    rp, ldr = None, 0
-    if residual is not None:
-        if residual.dim() != 2 or residual.shape[0] != T:
-            raise ValueError(f"residual must be [{T}, {pe.N}]")
-        rp, ldr = _rows2d(residual, pe.N, "residual")
-    out = torch.empty((T, pe.N), dtype=torch.float16, device=h.device) if y is None else y
-    if out.dim() != 2 or out.shape[0] != T:
-        raise ValueError(f"y must be [{T}, {pe.N}]")
-    yp, ldy = _rows2d(out, pe.N, "y")
-    need = lib.awq_combine_experts_workspace_bytes(T, top_k, pe.E, pe.N, pe.K, pe.group_size)
-    ws, ws_bytes = _scratch(need, h, workspace)
-    st = lib.awq_combine_experts(hp, ldh, route.offsets.data_ptr(), route.positions.data_ptr(),
-                                 route.weights.data_ptr(), T, top_k, pe.E, _ptr(pe.qweight), _ptr(pe.scales),
-                                 _ptr(pe.qzeros) if pe.zero_point else None,
-                                 _flat(bias, (pe.E, pe.N), torch.float16, "bias"), rp, ldr, yp, ldy, pe.N, pe.K,
-                                 pe.group_size, int(pe.zero_point), ws, ws_bytes, _stream(h))
-    _check(st, "awq_combine_experts")
+    lib = _lib or load_library()
+    qweight, scales, qzeros, E, N, K, group_size, zero_point = pe
+    T, top_k = shape = route.ids.shape
+    op = _flat(route.offsets, (E + 1,), _I32, "route.offsets")
+    pp = _flat(route.positions, shape, _I32, "route.positions")
+    wp = _flat(route.weights, shape, _F32, "route.weights")
+    hp, ldh = _rows2d(h, T * top_k, K, "h")
+    rp, ldr = (None, 0) if residual is None else _rows2d(residual, T, N, "residual")
+    if y is None:
+        out = h.new_empty((T, N))
+        yp, ldy = out.data_ptr(), N
+    else:
+        out = y
+        yp, ldy = _rows2d(y, T, N, "y")
+    bp = _flat(bias, (E, N), _F16, "bias")
+    qp, sp, zp = _ptr(qweight), _ptr(scales), _ptr(qzeros) if zero_point else None
+    stream = _handle(h)
+    _with_workspace(
+        lambda ws, n: lib.awq_combine_experts(hp, ldh, op, pp, wp, T, top_k, E, qp, sp, zp, bp, rp, ldr, yp, ldy, N, K,
+                                              group_size, zero_point, ws, n, stream),
+        lambda: lib.awq_combine_experts_workspace_bytes(T, top_k, E, N, K, group_size), "awq_combine_experts",
+        workspace, h, stream)
     return out
 
 
