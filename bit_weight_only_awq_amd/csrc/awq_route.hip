@@ -8,130 +8,131 @@
 // in fp32.  A logit of -inf or NaN is never chosen: its slot has id -1,
 // weight 0 and position -1.  With m = +inf the +inf logits share the weight.
 //
-// The sort is a counting sort without atomics on anything but bits: a token
-// chooses an expert at most once, so the choices of 64 tokens for one expert
-// are one 64-bit word with bit t set, and a slot's rank among its expert's
-// slots is a population count.  Blocks of 256 tokens count their slots per
-// expert; with more than one block a second launch adds the counts of the blocks before.
-#include <hip/hip_runtime.h>
-#include <stdint.h>
-
+// Bound: latency for a few tokens (one launch, 3-6 us), the picks for many: per
+// token top_k dependent maxima.  LG lanes hold a token's logits, consecutive
+// ones per lane, so the lowest lane with the maximum also has the lowest index;
+// a maximum over the lanes is log2(LG) register exchanges (DPP).
+//
+// The sort is a counting sort without atomics on anything but bits and integer
+// sums: a token chooses an expert at most once, so the choices of a block's 64
+// tokens for one expert are one 64-bit word, and a slot's rank among its
+// expert's slots is a population count.  Up to 64 tokens one launch does it
+// all; more blocks write their counts (a byte per expert) and a second launch adds up
+// the counts of the blocks before each; past 512 blocks a launch between the two
+// sums the counts along the blocks, so that the work stays linear.
+#include "awq_epilogue.hpp"
 #include "awq_launch_fused.hpp"
 
 namespace awq {
 namespace {
 
-constexpr int kTokens = 256;     // tokens per block
+constexpr int kTokens = 64;       // tokens per block: the bits of a mask
 constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopK = 64;
+constexpr int kSumBlocks = 512;   // blocks whose counts every block adds up for itself
 
-// Largest of v over groups of LG consecutive lanes.
-template <int LG>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int d = 1; d < LG; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
+// Largest of v (sum of v) over groups of LG consecutive lanes, in every lane.
+template <int LG, typename Op>
+__device__ __forceinline__ float group_reduce(float v, Op op) {
+  v = op(v, row_rotate<0x141>(v));                        // row_half_mirror
+  v = op(v, row_rotate<0x4E>(v));                         // quad_perm [2, 3, 0, 1]
+  v = op(v, row_rotate<0xB1>(v));                         // quad_perm [1, 0, 3, 2]
+  if constexpr (LG >= 16) v = op(v, row_rotate<0x128>(v));  // row_ror:8
+  if constexpr (LG >= 32) v = op(v, __shfl_xor(v, 16));
+  if constexpr (LG >= 64) v = op(v, __shfl_xor(v, 32));
   return v;
 }
 template <int LG>
+__device__ __forceinline__ float group_max(float v) {
+  return group_reduce<LG>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int LG>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < LG; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+  return group_reduce<LG>(v, [](float a, float b) { return a + b; });
 }
 
 __device__ __forceinline__ float exp_below(float l, float m) { return l == m ? 1.0f : expf(l - m); }
 
-// LG lanes per token, EPL consecutive logits per lane.
+// What a block keeps of its tokens' choices.
+struct Choices {
+  unsigned long long mask[kMaxExperts];  // bit t: the block's token t chose the expert
+  int id[kTokens * kMaxTopK];
+  float share[kTokens * kMaxTopK];       // exp(l - m)
+};
+
+// The block's tokens' choices: LG lanes per token, EPL consecutive logits per lane.
 template <int LG, int EPL, typename T>
-__device__ void choose(const T* __restrict__ logits, int64_t ld, int tokens, int E, int top_k, bool renormalize,
-                       int* __restrict__ ids, float* __restrict__ weights) {
+__device__ __forceinline__ void choose(const T* __restrict__ logits, int64_t ld, int tokens, int E, int top_k,
+                                       bool renormalize, int* __restrict__ ids, float* __restrict__ weights,
+                                       Choices& c) {
   const int lane = threadIdx.x & 63, l = lane & (LG - 1), base = lane & ~(LG - 1);
   const int per_pass = blockDim.x / LG;
   for (int t0 = 0; t0 < tokens; t0 += per_pass) {
     const int t = t0 + threadIdx.x / LG;
     const bool live = t < tokens;
-    float v[EPL];
+    float v[EPL], mine = -INFINITY;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const int e = l * EPL + i;
       v[i] = live && e < E ? (float)logits[t * ld + e] : -INFINITY;
       if (v[i] != v[i]) v[i] = -INFINITY;
+      mine = fmaxf(mine, v[i]);
     }
-    float all = 0.0f, m = 0.0f, sum = 0.0f;
+    const float m = group_max<LG>(mine);
+    float all = 0.0f;
+    if (!renormalize) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) all += v[i] == -INFINITY ? 0.0f : exp_below(v[i], m);
+      all = group_sum<LG>(all);
+    }
+    float best = m, sum = 0.0f;
     for (int j = 0; j < top_k; ++j) {
-      float mine = v[0];
-#pragma unroll
-      for (int i = 1; i < EPL; ++i) mine = fmaxf(mine, v[i]);
-      const float best = group_max<LG>(mine);
-      if (j == 0) {
-        m = best;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) all += v[i] == -INFINITY ? 0.0f : exp_below(v[i], m);
-        all = group_sum<LG>(all);
-      }
       const bool any = best != -INFINITY;
-      const unsigned long long has = __ballot(mine == best) >> base;
-      const int owner = __builtin_ctzll(has | (1ull << 63));
-      if (any) sum += exp_below(best, m);
-      if (live && (any ? l == owner : l == 0)) {
+      const float share = any ? exp_below(best, m) : 0.0f;
+      sum += share;
+      const int owner = __builtin_ctzll(__ballot(mine == best) >> base);
+      if (l == owner && live) {
         int at = -1;
         if (any) {
+          // the first of the lane's logits that equals it, taken out
+          mine = -INFINITY;
 #pragma unroll
-          for (int i = EPL - 1; i >= 0; --i)
-            if (v[i] == best) at = i;
-#pragma unroll
-          for (int i = 0; i < EPL; ++i)
-            if (i == at) v[i] = -INFINITY;
-          at += l * EPL;
+          for (int i = 0; i < EPL; ++i) {
+            if (at < 0 && v[i] == best) {
+              at = l * EPL + i;
+              v[i] = -INFINITY;
+            }
+            mine = fmaxf(mine, v[i]);
+          }
+          atomicOr(&c.mask[at], 1ull << t);
         }
-        ids[(int64_t)t * top_k + j] = at;
-        weights[(int64_t)t * top_k + j] = any ? exp_below(best, m) : 0.0f;
+        c.id[t * top_k + j] = at;
+        c.share[t * top_k + j] = share;
       }
+      best = group_max<LG>(mine);
     }
-    if (live) {
-      const float total = renormalize ? sum : all;
-      __threadfence_block();
+    // (written and read within one wave, in order)
+    const float total = renormalize ? sum : all;
+    if (live)
       for (int j = l; j < top_k; j += LG) {
-        const int64_t s = (int64_t)t * top_k + j;
-        weights[s] = total > 0.0f ? weights[s] / total : 0.0f;
+        const int s = t * top_k + j;
+        ids[s] = c.id[s];
+        weights[s] = total > 0.0f ? c.share[s] / total : 0.0f;
       }
-    }
   }
-}
-
-// The block's choices as bits: mask[e][w] bit b = token 64 w + b chose expert e.
-__device__ void mark(const int* ids, int tokens, int E, int top_k, unsigned long long (*mask)[kTokens / 64]) {
-  for (int i = threadIdx.x; i < E * (kTokens / 64); i += blockDim.x) (&mask[0][0])[i] = 0;
-  __syncthreads();
-  for (int s = threadIdx.x; s < tokens * top_k; s += blockDim.x) {
-    const int e = ids[s], t = s / top_k;
-    if (e >= 0) atomicOr(&mask[e][t >> 6], 1ull << (t & 63));
-  }
-  __syncthreads();
-}
-
-__device__ int count_of(const unsigned long long* m) {
-  int n = 0;
-#pragma unroll
-  for (int w = 0; w < kTokens / 64; ++w) n += __popcll(m[w]);
-  return n;
 }
 
 // start[e] (LDS) holds expert e's slots in all blocks: replaced by the sum over
 // the experts below; start[E] the total.  One wave.
-__device__ void scan_experts(int* start, int E) {
+__device__ __forceinline__ void scan_experts(int* start, int E) {
   if (threadIdx.x < 64) {
     int seen = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
       const int e = e0 + threadIdx.x;
       const int n = e < E ? start[e] : 0;
-      int sum = n;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int up = __shfl_up(sum, d);
-        if ((int)threadIdx.x >= d) sum += up;
-      }
+      const int sum = prefix_sum(n);
       if (e < E) start[e] = seen + sum - n;
-      seen += __shfl(sum, 63);
+      seen += __builtin_amdgcn_readlane(sum, 63);
     }
     if (threadIdx.x == 0) start[E] = seen;
   }
@@ -140,72 +141,136 @@ __device__ void scan_experts(int* start, int E) {
 
 // Positions and rows of the block's slots, from the masks and the place of
 // the block's first slot of each expert.
-__device__ void place(const int* ids, int t0, int tokens, int top_k, const unsigned long long (*mask)[kTokens / 64],
-                      const int* first, int* __restrict__ positions, int* __restrict__ rows) {
+__device__ __forceinline__ void place(const int* id, int t0, int tokens, int top_k, const unsigned long long* mask,
+                                      const int* first, int* __restrict__ positions, int* __restrict__ rows) {
   for (int s = threadIdx.x; s < tokens * top_k; s += blockDim.x) {
-    const int e = ids[s], t = s / top_k;
+    const int e = id[s], t = s / top_k;
     int at = -1;
     if (e >= 0) {
-      at = first[e];
-      for (int w = 0; w < (t >> 6); ++w) at += __popcll(mask[e][w]);
-      at += __popcll(mask[e][t >> 6] & ((1ull << (t & 63)) - 1));
+      at = first[e] + __popcll(mask[e] & ((1ull << t) - 1));
       rows[at] = t0 * top_k + s;
     }
     positions[(int64_t)t0 * top_k + s] = at;
   }
 }
 
-// One block: choices of kTokens tokens, and either the whole sort (one block
-// in the grid) or the block's counts per expert.
+// One block: the choices of kTokens tokens, and either the whole sort (one
+// block in the grid) or the block's counts per expert, a byte each.
 template <int LG, int EPL, typename T>
 __global__ __launch_bounds__(1024) void route_kernel(const T* __restrict__ logits, int ld, int tokens, int E, int top_k,
                                                      int renormalize, int* __restrict__ ids,
                                                      float* __restrict__ weights, int* __restrict__ offsets,
                                                      int* __restrict__ rows, int* __restrict__ positions,
-                                                     int* __restrict__ counts) {
-  __shared__ unsigned long long mask[kMaxExperts][kTokens / 64];
+                                                     uint8_t* __restrict__ counts) {
+  __shared__ Choices c;
   __shared__ int start[kMaxExperts + 1];
   const int t0 = blockIdx.x * kTokens, here = min(kTokens, tokens - t0);
-  int* my_ids = ids + (int64_t)t0 * top_k;
-  choose<LG, EPL, T>(logits + (int64_t)t0 * ld, ld, here, E, top_k, renormalize != 0, my_ids,
-                     weights + (int64_t)t0 * top_k);
+  for (int e = threadIdx.x; e < E; e += blockDim.x) c.mask[e] = 0;
   __syncthreads();
-  mark(my_ids, here, E, top_k, mask);
+  choose<LG, EPL, T>(logits + (int64_t)t0 * ld, ld, here, E, top_k, renormalize != 0, ids + (int64_t)t0 * top_k,
+                     weights + (int64_t)t0 * top_k, c);
+  __syncthreads();
   if (gridDim.x > 1) {
-    for (int e = threadIdx.x; e < E; e += blockDim.x) counts[blockIdx.x * E + e] = count_of(mask[e]);
+    const int pitch = (E + 3) & ~3;
+    for (int e = threadIdx.x; e < pitch; e += blockDim.x)
+      counts[(int64_t)blockIdx.x * pitch + e] = e < E ? (uint8_t)__popcll(c.mask[e]) : 0;
     return;
   }
-  for (int e = threadIdx.x; e < E; e += blockDim.x) start[e] = count_of(mask[e]);
+  for (int e = threadIdx.x; e < E; e += blockDim.x) start[e] = __popcll(c.mask[e]);
   __syncthreads();
   scan_experts(start, E);
   for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = start[e];
-  place(my_ids, 0, here, top_k, mask, start, positions, rows);
+  place(c.id, 0, here, top_k, c.mask, start, positions, rows);
   for (int i = start[E] + threadIdx.x; i < tokens * top_k; i += blockDim.x) rows[i] = -1;
 }
 
-__global__ __launch_bounds__(1024) void route_place_kernel(const int* __restrict__ ids, int tokens, int E, int top_k,
-                                                           const int* __restrict__ counts, int* __restrict__ offsets,
-                                                           int* __restrict__ rows, int* __restrict__ positions) {
-  __shared__ unsigned long long mask[kMaxExperts][kTokens / 64];
-  __shared__ int start[kMaxExperts + 1], before[kMaxExperts];
-  const int t0 = blockIdx.x * kTokens, here = min(kTokens, tokens - t0);
-  const int* my_ids = ids + (int64_t)t0 * top_k;
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    int sum = 0, mine = 0;
-    for (int b = 0; b < (int)gridDim.x; ++b) {
-      if (b == (int)blockIdx.x) mine = sum;
-      sum += counts[b * E + e];
-    }
-    start[e] = sum;
-    before[e] = mine;
+// Sums along the blocks for 4 experts: base[b][e] = the slots of expert e in the
+// blocks before b, base[blocks][e] in all.
+__global__ __launch_bounds__(1024) void route_sum_kernel(const uint32_t* __restrict__ counts, int blocks, int words,
+                                                         int* __restrict__ base) {
+  __shared__ int part[16][4];
+  const int w = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per = (blocks + 1023) / 1024, b0 = threadIdx.x * per, b1 = min(blocks, b0 + per);
+  int sum[4] = {0, 0, 0, 0}, first[4];
+  for (int b = b0; b < b1; ++b) {
+    const uint32_t v = counts[(int64_t)b * words + w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] += (v >> (8 * i)) & 255u;
   }
-  mark(my_ids, here, E, top_k, mask);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int upto = prefix_sum(sum[i]);
+    first[i] = upto - sum[i];
+    if (lane == 63) part[wave][i] = upto;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    for (int v = 0; v < wave; ++v) first[i] += part[v][i];
+  for (int b = b0; b < b1; ++b) {
+    const uint32_t v = counts[(int64_t)b * words + w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      base[((int64_t)b * words + w) * 4 + i] = first[i];
+      first[i] += (v >> (8 * i)) & 255u;
+    }
+  }
+  if (threadIdx.x == 1023)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) base[((int64_t)blocks * words + w) * 4 + i] = first[i];
+}
+
+// Offsets, and the positions and rows of one block's slots; `base` from
+// route_sum_kernel, or NULL: the block adds up the counts itself.
+__global__ __launch_bounds__(1024) void route_place_kernel(const int* __restrict__ ids, int tokens, int E, int top_k,
+                                                           const uint32_t* __restrict__ counts,
+                                                           const int* __restrict__ base, int* __restrict__ offsets,
+                                                           int* __restrict__ rows, int* __restrict__ positions) {
+  __shared__ unsigned long long mask[kMaxExperts];
+  __shared__ int start[kMaxExperts + 1], before[kMaxExperts], id[kTokens * kMaxTopK];
+  const int b = blockIdx.x, blocks = gridDim.x, t0 = b * kTokens, here = min(kTokens, tokens - t0);
+  const int words = (E + 3) >> 2;
+  for (int e = threadIdx.x; e < 4 * words; e += blockDim.x) {
+    mask[e] = 0;
+    before[e] = base ? base[(int64_t)b * words * 4 + e] : 0;
+    start[e] = base ? base[(int64_t)blocks * words * 4 + e] : 0;
+  }
+  __syncthreads();
+  for (int s = threadIdx.x; s < here * top_k; s += blockDim.x) {
+    const int e = ids[(int64_t)t0 * top_k + s];
+    id[s] = e;
+    if (e >= 0) atomicOr(&mask[e], 1ull << (s / top_k));
+  }
+  if (!base) {
+    // four experts per word, two 16-bit sums per register (at most 512 blocks of 64)
+    const int sets = blockDim.x / words, w = threadIdx.x % words, set = threadIdx.x / words;
+    if (set < sets) {
+      uint32_t lo = 0, hi = 0, lo_before = 0, hi_before = 0;
+#pragma unroll 4
+      for (int r = set; r < blocks; r += sets) {
+        const uint32_t v = counts[(int64_t)r * words + w], even = v & 0x00FF00FFu, odd = (v >> 8) & 0x00FF00FFu;
+        lo += even;
+        hi += odd;
+        lo_before += r < b ? even : 0u;
+        hi_before += r < b ? odd : 0u;
+      }
+      atomicAdd(&start[4 * w], (int)(lo & 0xFFFFu));
+      atomicAdd(&start[4 * w + 1], (int)(hi & 0xFFFFu));
+      atomicAdd(&start[4 * w + 2], (int)(lo >> 16));
+      atomicAdd(&start[4 * w + 3], (int)(hi >> 16));
+      atomicAdd(&before[4 * w], (int)(lo_before & 0xFFFFu));
+      atomicAdd(&before[4 * w + 1], (int)(hi_before & 0xFFFFu));
+      atomicAdd(&before[4 * w + 2], (int)(lo_before >> 16));
+      atomicAdd(&before[4 * w + 3], (int)(hi_before >> 16));
+    }
+  }
+  __syncthreads();
   scan_experts(start, E);
-  if (blockIdx.x == 0)
+  if (b == 0)
     for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = start[e];
   for (int e = threadIdx.x; e < E; e += blockDim.x) before[e] += start[e];
   __syncthreads();
-  place(my_ids, t0, here, top_k, mask, before, positions, rows);
+  place(id, t0, here, top_k, mask, before, positions, rows);
   // this block's share of the rows that no slot takes
   const int64_t lo = (int64_t)t0 * top_k, hi = lo + (int64_t)here * top_k;
   for (int64_t i = (lo > start[E] ? lo : start[E]) + threadIdx.x; i < hi; i += blockDim.x) rows[i] = -1;
@@ -213,27 +278,33 @@ __global__ __launch_bounds__(1024) void route_place_kernel(const int* __restrict
 
 template <int LG, int EPL>
 void launch_choose(const void* logits, int ld, bool fp32, int T, int E, int top_k, bool renormalize, int* ids,
-                   float* weights, int* offsets, int* rows, int* positions, int* counts, hipStream_t stream) {
+                   float* weights, int* offsets, int* rows, int* positions, uint8_t* counts, hipStream_t stream) {
   const dim3 grid((T + kTokens - 1) / kTokens);
+  const int tokens = T < kTokens ? T : kTokens, threads = (tokens * LG + 63) / 64 * 64;
+  const dim3 block(threads < 1024 ? threads : 1024);
   if (fp32)
-    hipLaunchKernelGGL((route_kernel<LG, EPL, float>), grid, dim3(1024), 0, stream, static_cast<const float*>(logits),
-                       ld, T, E, top_k, (int)renormalize, ids, weights, offsets, rows, positions, counts);
+    hipLaunchKernelGGL((route_kernel<LG, EPL, float>), grid, block, 0, stream, static_cast<const float*>(logits), ld, T,
+                       E, top_k, (int)renormalize, ids, weights, offsets, rows, positions, counts);
   else
-    hipLaunchKernelGGL((route_kernel<LG, EPL, _Float16>), grid, dim3(1024), 0, stream,
-                       static_cast<const _Float16*>(logits), ld, T, E, top_k, (int)renormalize, ids, weights, offsets,
-                       rows, positions, counts);
+    hipLaunchKernelGGL((route_kernel<LG, EPL, _Float16>), grid, block, 0, stream, static_cast<const _Float16*>(logits),
+                       ld, T, E, top_k, (int)renormalize, ids, weights, offsets, rows, positions, counts);
 }
+
+int blocks_of(int T) { return (T + kTokens - 1) / kTokens; }
+
+size_t count_bytes(int T, int E) { return ((size_t)blocks_of(T) * ((E + 3) & ~3) + 15) & ~(size_t)15; }
 
 }  // namespace
 
 size_t route_workspace_bytes(int T, int E) {
-  const size_t blocks = ((size_t)T + kTokens - 1) / kTokens;
-  return blocks > 1 ? blocks * E * 4 : 0;
+  const int blocks = blocks_of(T);
+  if (blocks <= 1) return 0;
+  return count_bytes(T, E) + (blocks > kSumBlocks ? (size_t)(blocks + 1) * ((E + 3) & ~3) * 4 : 0);
 }
 
 hipError_t launch_route(const void* logits, int ld, bool fp32, int T, int E, int top_k, bool renormalize, int* ids,
                         float* weights, int* offsets, int* rows, int* positions, void* workspace, hipStream_t stream) {
-  int* counts = static_cast<int*>(workspace);
+  uint8_t* counts = static_cast<uint8_t*>(workspace);
 #define AWQ_ROUTE(LG, EPL) \
   launch_choose<LG, EPL>(logits, ld, fp32, T, E, top_k, renormalize, ids, weights, offsets, rows, positions, counts, stream)
   if (E <= 8) AWQ_ROUTE(8, 1);
@@ -245,9 +316,18 @@ hipError_t launch_route(const void* logits, int ld, bool fp32, int T, int E, int
   else if (E <= 512) AWQ_ROUTE(32, 16);
   else AWQ_ROUTE(64, 16);
 #undef AWQ_ROUTE
-  if (T > kTokens)
-    hipLaunchKernelGGL(route_place_kernel, dim3((T + kTokens - 1) / kTokens), dim3(1024), 0, stream, ids, T, E, top_k,
-                       counts, offsets, rows, positions);
+  const int blocks = blocks_of(T);
+  if (blocks > 1) {
+    int* base = nullptr;
+    const int words = (E + 3) / 4;
+    const uint32_t* four = reinterpret_cast<const uint32_t*>(counts);
+    if (blocks > kSumBlocks) {
+      base = reinterpret_cast<int*>(counts + count_bytes(T, E));
+      hipLaunchKernelGGL(route_sum_kernel, dim3(words), dim3(1024), 0, stream, four, blocks, words, base);
+    }
+    hipLaunchKernelGGL(route_place_kernel, dim3(blocks), dim3(words > 32 ? 1024 : 256), 0, stream, ids, T, E, top_k,
+                       four, base, offsets, rows, positions);
+  }
   return hipGetLastError();
 }
 

@@ -50,6 +50,11 @@ def test_token_counts(T):
     check(logits_of(T, 60, 3, np.float16), 4, False)
 
 
+@pytest.mark.parametrize("T,E,k,dtype", [(33000, 6, 1, np.float16), (40001, 10, 2, np.float32)])
+def test_more_blocks_than_one_block_adds_up(T, E, k, dtype):
+    check(logits_of(T, E, 5, dtype), k, True)
+
+
 @pytest.mark.parametrize("E,k", [(8, 8), (64, 64), (100, 64), (1024, 64)])
 def test_many_choices(E, k):
     check(logits_of(40, E, 4), k, True)
