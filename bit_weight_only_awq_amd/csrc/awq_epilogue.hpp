@@ -84,7 +84,7 @@ __device__ __forceinline__ int prefix_sum(int v) {
 
 // 64 experts' row ranges and tiles, one expert per lane.
 struct ExpertLanes {
-  int lo, n, tiles, sum;  // first row, rows, tiles, tiles of the lanes up to this one
+  int lo, n, tiles, sum;  // first row, rows, tiles, one past the number of the last of them
 };
 __device__ __forceinline__ ExpertLanes expert_lanes(const int* __restrict__ offsets, int E, int R, int tile, int e0) {
   const int e = e0 + __lane_id();
@@ -99,12 +99,12 @@ __device__ __forceinline__ ExpertLanes expert_lanes(const int* __restrict__ offs
 }
 
 // The rows sorted by expert (expert e: offsets[e] .. offsets[e + 1] - 1), cut into
-// tiles of at most `tile` rows of one expert each, an expert's rows shared
-// evenly among its tiles (in multiples of `unit` rows).  The counts live on
+// tiles of at most `tile` rows of one expert each, an expert's units of `unit`
+// rows shared evenly among its tiles (`tile` a multiple of `unit`).  The counts live on
 // the device only, so the host launches for row_tiles(R, E, tile) tiles and
 // each wave finds its own here, 64 experts at a time: lane l counts expert l's
-// tiles, a prefix sum over the lanes places them, and the first lane whose sum
-// passes the wanted tile is the expert.  Offsets are clamped into [0, R], so no
+// tiles, a prefix sum over the lanes numbers them, and the lane whose numbers
+// hold the wanted tile is the expert.  Offsets are clamped into [0, R], so no
 // wrong value leads outside the buffers.  With `offsets` NULL one expert holds
 // all R rows.
 struct RowTiles {
@@ -126,8 +126,22 @@ struct RowTiles {
 
   __device__ __forceinline__ RowTile cut(int expert, int lo, int n, int tiles, int nth) const {
     if (tiles == 1) return RowTile{expert, lo, n};
-    const int each = ((n + tiles - 1) / tiles + unit - 1) / unit * unit;
-    return RowTile{expert, lo + nth * each, min(each, n - nth * each)};
+    const int units = (n + unit - 1) / unit, each = units / tiles, more = units - each * tiles;
+    const int from = unit * (nth * each + min(nth, more));
+    return RowTile{expert, lo + from, min(unit * (each + (nth < more)), n - from)};
+  }
+
+  // Numbers the tiles of up to 64 experts by height: the experts with the
+  // tallest tiles first.
+  __device__ __forceinline__ void tallest_first() {
+    if (offsets == nullptr || E > 64) return;
+    const int units = (first.n + unit - 1) / unit, height = first.tiles ? (units + first.tiles - 1) / first.tiles : 0;
+    int before = 0;
+    for (int e = 0; e < E; ++e) {
+      const int h = __builtin_amdgcn_readlane(height, e), tiles = __builtin_amdgcn_readlane(first.tiles, e);
+      before += h > height || (h == height && e < (int)__lane_id()) ? tiles : 0;
+    }
+    first.sum = before + first.tiles;
   }
 
   // 0 <= slot < total
@@ -136,9 +150,9 @@ struct RowTiles {
     int seen = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
       const ExpertLanes x = e0 == 0 ? first : expert_lanes(offsets, E, R, tile, e0);
-      const unsigned long long past = __ballot(seen + x.sum > slot);
-      if (past != 0) {
-        const int l = __builtin_ctzll(past);
+      const unsigned long long owner = __ballot(seen + x.sum > slot && seen + x.sum - x.tiles <= slot);
+      if (owner != 0) {
+        const int l = __builtin_ctzll(owner);
         const int tiles = __builtin_amdgcn_readlane(x.tiles, l);
         return cut(e0 + l, __builtin_amdgcn_readlane(x.lo, l), __builtin_amdgcn_readlane(x.n, l), tiles,
                    slot - (seen + __builtin_amdgcn_readlane(x.sum, l) - tiles));
