@@ -90,6 +90,10 @@ def test_all_tokens_masked():
     run_case(np.full((5, 6), -np.inf, np.float32), 2, 48, 64, 32, True, "none", True, False, True, seed=3)
 
 
+def test_more_tokens_than_a_grid_has_rows():
+    run_case(logits_of(33000, 4, 5), 2, 16, 32, 32, True, "silu", True, True, True, seed=4)
+
+
 @pytest.mark.parametrize("T,E,k,N,K,gated", [(1, 8, 2, 22016, 4096, True), (1, 8, 2, 4096, 11008, False),
                                              (48, 64, 6, 2816, 2048, True), (300, 8, 2, 4096, 11008, False),
                                              (900, 8, 2, 4096, 4096, True)])
