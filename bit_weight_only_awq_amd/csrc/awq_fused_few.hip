@@ -26,25 +26,30 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, ui
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
 }
 
+// (What the loads need comes first, as plain arguments: the leading 16 words of
+// the arguments are in registers when a wave starts.)
 // TS: sets of 4 tokens; S: sub-chunks per wave and round; MULTI: K takes more
 // than one round (a loop around the loads makes the compiler stage them less
 // aggressively, so a single round is an instance of its own).
 template <int TS, int S, int MAXW, bool ZP, bool MULTI, bool GROUPED>
-__global__ __launch_bounds__(MAXW * 64) void few_kernel(PackedArgs w, ProductArgs p, int gshift, int groups, int rounds,
-                                                        float* __restrict__ part) {
+__global__ __launch_bounds__(MAXW * 64) void few_kernel(const uint32_t* __restrict__ qweight,
+                                                        const uint16_t* __restrict__ scales,
+                                                        const uint32_t* __restrict__ qzeros,
+                                                        const _Float16* __restrict__ xs, int N, int K, int ldx, int R,
+                                                        int gshift, int gated, int groups, int rounds, int E,
+                                                        ProductArgs p, float* __restrict__ part) {
   constexpr int RS = kRows / 4;
   __shared__ float red[MAXW][kRows][TS * 4];
   const int nw = blockDim.x >> 6;
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int b = lane >> 2, q = lane & 3;
-  const int K = w.K, G = K >> gshift;
-  const bool gated = p.gated;
-  const int width = gated ? w.N >> 1 : w.N;
+  const int G = K >> gshift;
+  const int width = gated ? N >> 1 : N;
   int grp = blockIdx.x;
-  RowTile rt{0, 0, p.R};
+  RowTile rt{0, 0, R};
   if constexpr (GROUPED) {
     // (the row tiles of an expert next to each other: its weights come from HBM once)
-    const RowTiles tiles(p.offsets, w.E, p.R, TS * 4, 1);
+    const RowTiles tiles(p.offsets, E, R, TS * 4, 1);
     grp = blockIdx.x / max(tiles.total, 1);
     if (grp >= groups || tiles.total == 0) return;
     rt = tiles[blockIdx.x - grp * tiles.total];
@@ -52,13 +57,13 @@ __global__ __launch_bounds__(MAXW * 64) void few_kernel(PackedArgs w, ProductArg
   const int n0 = grp * (gated ? 8 : kRows);  // first output column
   const size_t e = rt.expert;
   const DecodeConsts kc;
-  const __amdgpu_buffer_rsrc_t rw = make_rsrc(w.qweight + e * w.N * (K >> 3), (uint32_t)w.N * (K >> 1));
-  const __amdgpu_buffer_rsrc_t rs = make_rsrc(w.scales + e * w.N * G, (uint32_t)w.N * G * 2);
-  const __amdgpu_buffer_rsrc_t rz = make_rsrc(ZP ? w.qzeros + e * (w.N >> 3) * G : w.qweight,
-                                              ZP ? (uint32_t)(w.N >> 3) * G * 4 : 0u);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(qweight + e * N * (K >> 3), (uint32_t)N * (K >> 1));
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(scales + e * N * G, (uint32_t)N * G * 2);
+  const __amdgpu_buffer_rsrc_t rz = make_rsrc(ZP ? qzeros + e * (N >> 3) * G : qweight,
+                                              ZP ? (uint32_t)(N >> 3) * G * 4 : 0u);
   const __amdgpu_buffer_rsrc_t rx =
-      GROUPED && p.rows ? make_rsrc(p.x, (uint32_t)((p.x_rows - 1) * p.ldx + K) * 2)
-                        : make_rsrc(p.x + rt.row0 * p.ldx, (uint32_t)((rt.count - 1) * (int)p.ldx + K) * 2);
+      GROUPED && p.rows ? make_rsrc(xs, (uint32_t)((p.x_rows - 1) * ldx + K) * 2)
+                        : make_rsrc(xs + rt.row0 * (int64_t)ldx, (uint32_t)((rt.count - 1) * ldx + K) * 2);
   // the two octets; one past N lies past the resources and reads as 0
   uint32_t octet[2];
   octet[0] = n0 >> 3;
@@ -69,7 +74,7 @@ __global__ __launch_bounds__(MAXW * 64) void few_kernel(PackedArgs w, ProductArg
     const int m = 4 * ts + q;
     int r = min(m, rt.count - 1);
     if (GROUPED && p.rows) r = min(max(p.rows[rt.row0 + r] / p.slots_per_row, 0), p.x_rows - 1);
-    xrow[ts] = m < rt.count ? (uint32_t)(r * (int)p.ldx) * 2 : kOutOfRange;
+    xrow[ts] = m < rt.count ? (uint32_t)(r * ldx) * 2 : kOutOfRange;
   }
 
   float4_t acc[RS][TS];
@@ -91,7 +96,7 @@ __global__ __launch_bounds__(MAXW * 64) void few_kernel(PackedArgs w, ProductArg
         const uint32_t row = octet[r >> 1] * 8 + 4 * (r & 1) + q;
         wv[s][r] = __builtin_bit_cast(
             u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                       rw, kin && row < (uint32_t)w.N ? row * (K >> 1) + (k0 >> 1) : kOutOfRange, 0, 0));
+                       rw, kin && row < (uint32_t)N ? row * (K >> 1) + (k0 >> 1) : kOutOfRange, 0, 0));
       }
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
@@ -173,15 +178,15 @@ __global__ __launch_bounds__(MAXW * 64) void few_kernel(PackedArgs w, ProductArg
     const int64_t r = rt.row0 + m;
     const int n = gated && row >= 8 ? width + col : col;
     float v = total(row, m);
-    if (p.bias) v += (float)p.bias[e * w.N + n];
+    if (p.bias) v += (float)p.bias[e * N + n];
     if (part) {  // raw sums, part[row][N]
-      part[r * w.N + n] = v;
+      part[r * N + n] = v;
       continue;
     }
     v = activate(v, p.activation);
     if (gated) {
       float u = total(row + 8, m);
-      if (p.bias) u += (float)p.bias[e * w.N + width + n];
+      if (p.bias) u += (float)p.bias[e * N + width + n];
       v *= u;
     }
     if (p.residual) v += (float)p.residual[r * p.ldr + col];
@@ -199,7 +204,8 @@ hipError_t launch_few_as(const PackedArgs& w, const ProductArgs& p, int gs, int 
                                                : few_kernel<TS, S, MAXW, ZP, true, true>)
                                 : (rounds == 1 ? few_kernel<TS, S, MAXW, ZP, false, false>
                                                : few_kernel<TS, S, MAXW, ZP, true, false>);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(groups * slots)), dim3(nw * 64), 0, stream, w, p, gs, groups, rounds, part);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(groups * slots)), dim3(nw * 64), 0, stream, w.qweight, w.scales, w.qzeros, p.x,
+                     w.N, w.K, (int)p.ldx, p.R, gs, (int)p.gated, groups, rounds, w.E, p, part);
   return hipGetLastError();
 }
 
