@@ -13,6 +13,9 @@
 // sub-chunks of 512 channels a round, with every load of a round in flight
 // before any decoding.  The slices are summed across lanes in registers and the
 // waves in LDS, in a fixed order; the last few threads apply the epilogue.
+//
+// Measured (us): 4 / 8 x 4096 -> 4096: 5.4 / 6.2; -> 11008: 9.6 / 12.2; -> 22016
+// gated: 16.0 / 20.9 (2.9 / 2.3 TB/s); 8 tokens x 2 of 8 -> 22016 gated: 78 (4.3 TB/s).
 #include "awq_epilogue.hpp"
 #include "awq_launch_fused.hpp"
 

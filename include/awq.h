@@ -313,15 +313,19 @@ size_t awq_clip_search_workspace_bytes(int32_t count, int32_t M, int32_t N, int3
  * ("AI-Research-SKILLs AWQ 高级使用指南", section 层融合: gate and up fused; the
  * MLP's activation, the bias and the residual stream are what a decoder
  * block puts around the layer.)  Sums, bias, activation, product and residual
- * are fp32; the output is rounded once to fp16.  Weights are exact (q - z
- * times the group scale on fp32 sums) up to 8 tokens and rounded once to fp16
- * above, as awq_gemm's.
+ * are fp32; the output is rounded once to fp16.  Up to 8 tokens, and up to 256
+ * with groups of 64 and more (N K < 2^32), no weight is rounded (exact q - z, the
+ * group scale on their fp32 sums); 9 to 256 tokens with groups of 32, and all
+ * larger products, take fp16((q - z) s), one rounding per weight, as awq_gemm's.
+ * A row that holds infinities or NaN gives NaN or infinities in its own outputs
+ * only.  Deterministic: the same bits again for the same call.
  * x         in   fp16, row m at x + m * ldx; bias fp16 [N] or NULL.
  * residual  in   fp16, row m at residual + m * ldr, or NULL.
  * y         out  fp16, row m at y + m * ldy; must not overlap an input, except
  *                that it may be the residual itself (same address and stride).
- * Strides are in elements, multiples of 8 and at least the row.  N a multiple
- * of 8 (gated: of 16); M <= 2^24.
+ * Strides are in elements, multiples of 8, at least the row and at most 2^21.
+ * N a multiple of 8 (gated: of 16); M <= 2^24.  Other checks as awq_gemm's
+ * (device pointers 16-byte aligned); AWQ_ERR_OPTION for an unknown activation.
  * workspace: awq_linear_fused_workspace_bytes() bytes (NULL when 0), under the
  * contract of awq_gemm's workspace: its first 512 KiB are zero at first use and
  * every call leaves them zero, so both share one buffer in stream order.
@@ -371,7 +375,9 @@ size_t awq_route_experts_workspace_bytes(int32_t T, int32_t E);
  *               clamped to [0, R], rows to x's x_rows rows, so that wrong ones
  *               give wrong results but never lead outside the buffers.
  * y        out  fp16, row r at y + r * ldy, r < offsets[E]; rows past it are left as they are.
- * R rows at most (R = T * top_k after a router), 1 <= R <= 2^24, E <= 1024; the rest
+ * R rows at most (R = T * top_k after a router), 1 <= R <= 2^24, E <= 1024; with
+ * `rows`, x_rows * ldx < 2^30.  Weights are exact as above while R is at most
+ * 2 rows per expert, or 64 with groups of 64 and more, and rounded past that; the rest
  * as in awq_linear_fused; workspace likewise, awq_linear_experts_workspace_bytes().
  */
 int awq_linear_experts(const void* x, int32_t ldx, int32_t x_rows, const int32_t* rows, int32_t slots_per_row,
