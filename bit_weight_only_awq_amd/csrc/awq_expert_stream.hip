@@ -24,8 +24,8 @@
 // workgroup per compute unit a stage's decoding and products take about as long
 // as its loads.
 //
-// Measured: 48 tokens x 6 of 64, 2048 -> 2816 gated: 46.8 us, 4.1 TB/s of the
-// packed weights (floor 37.0); 24 tokens 39.2 us, 4.4 TB/s; 16 x 4096 -> 4096:
+// Measured: 48 tokens x 6 of 64, 2048 -> 2816 gated: 46.2 us, 4.1 TB/s of the
+// packed weights (floor 37.0); 24 tokens 40.0 us, 4.4 TB/s; 16 x 4096 -> 4096:
 // 9.3 us; 13 x 11008 -> 4096: 15.0; 61 x 4096 -> 11008, groups of 64: 17.9 (5.0).
 #include "awq_epilogue.hpp"
 #include "awq_launch_fused.hpp"
@@ -339,7 +339,6 @@ template <bool ZP, int GROUP>
 hipError_t launch_stream_zg(const PackedArgs& w, const ProductArgs& p, int gs, const StreamPlan& plan, float* part,
                             hipStream_t stream) {
   switch (plan.rows * 100 + plan.cw * 10 + plan.kw) {
-    case 1641: return launch_stream_as<ZP, GROUP, 16, 4, 1, 3, 256>(w, p, gs, plan, part, stream);
     case 1622: return launch_stream_as<ZP, GROUP, 16, 2, 2, 2, 256>(w, p, gs, plan, part, stream);
     case 1624: return launch_stream_as<ZP, GROUP, 16, 2, 4, 2, 256>(w, p, gs, plan, part, stream);
     case 3241: return launch_stream_as<ZP, GROUP, 32, 4, 1, 2, 256>(w, p, gs, plan, part, stream);

@@ -124,7 +124,11 @@ TilePlan plan_tiles(int R, int experts, int N, int K) {
 // the variant chosen / the one on the other side of the rule:
 //   13 x 11008 -> 4096: 2 x 2 waves, K in 4: 14.9 / 2 x 4 waves, no split: 23.0
 //   16 x 4096 -> 4096: 2 x 4: 9.1 / 4 x 1: 16.8;  16 x 4096 -> 11008: 11.6 / 17.9
-//   48 tokens x 6 of 64, 2048 -> 2816: 4 x 1: 44.9 / 2 x 2: 53.5
+//   16 x 4096 -> 32768: 2 x 2: 21.7 / 4 x 1 with 32 rows: 22.9 (with 16 rows: 22.3)
+//   16 tokens x 2 of 8, 11008 -> 4096: 2 x 2: 47.2 / 4 x 1 with 32 rows: 54.4
+//   48 tokens x 6 of 64, 2048 -> 2816: 4 x 1 with 32 rows: 46.1 / 2 x 2: 54.0
+// (4 x 1 waves take tiles of 32 rows however few there are: an expert with 17 is
+// then read once, and 96 tokens x 6 of 64 take 51.6 us against 57.0 with 16.)
 //   61 x 4096 -> 11008 (32-row tiles): 4 x 2: 17.9 / 4 x 1: 20.8; 64 rows: 22.2
 //   100 x 4096 -> 4096: 4 x 2, K in 2: 14.0 / 4 x 1: 27
 //   200 x 4096 -> 11008: 4 x 1: 42.5 / 4 x 2: 46.5
@@ -141,7 +145,7 @@ StreamPlan plan_stream(int R, int experts, int N, int K) {
   const int c64 = experts * ((N + 63) / 64);
   if (each <= (experts == 1 ? 16 : 10) || (experts == 1 && R <= 32 && K <= 6144 && 2 * c64 <= 160)) {
     const int c = each <= 16 ? c64 : 2 * c64;
-    if (c >= 512) return plan(16, 4, 1, 1);
+    if (c >= 768) return plan(32, 4, 1, 1);
     if (c >= 224) return plan(16, 2, 2, 1);
     if (c >= 96 || K <= 6144) return plan(16, 2, 4, 1);
     return plan(16, 2, 2, c >= 64 ? 4 : 8);
