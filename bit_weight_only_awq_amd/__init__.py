@@ -661,7 +661,8 @@ def linear_experts(x: torch.Tensor, pe: PackedExperts, route: ExpertRoute, bias:
                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Every routed slot's token (fp16 ``x`` [T, K]) through its expert's layer and epilogue (``bias`` [E, N],
     ``gated`` as in ``linear_fused``): fp16 [T * top_k, N or N / 2], rows sorted by expert as ``route.rows`` says.
-    Rows past ``route.offsets[E]`` (slots without an expert) are not written."""
+    Rows before ``route.offsets[0]`` or past ``route.offsets[E]`` (slots without an expert, or with one outside the
+    slice of a route's experts that ``route.offsets[e0:e1 + 1]`` names) are not written."""
     lib = _lib or load_library()
     qweight, scales, qzeros, E, N, K, group_size, zero_point = pe
     T, top_k = route.ids.shape
@@ -691,7 +692,7 @@ def combine_experts(h: torch.Tensor, pe: PackedExperts, route: ExpertRoute, bias
                     residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The experts' second layer on the sorted rows ``h`` [T * top_k, K] and each token's weighted sum, plus
-    ``residual`` [T, N]: fp16 [T, N], one rounding."""
+    ``residual`` [T, N]: fp16 [T, N], one rounding.  With a slice of the route's offsets, the sum over the slice."""
     lib = _lib or load_library()
     qweight, scales, qzeros, E, N, K, group_size, zero_point = pe
     T, top_k = shape = route.ids.shape

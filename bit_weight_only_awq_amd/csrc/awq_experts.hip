@@ -34,13 +34,17 @@ __device__ __forceinline__ float4_t slices_sum(const float* __restrict__ part, i
   return v;
 }
 
+// The rows that the experts' ranges hold: only their sums were written.
+__device__ __forceinline__ int first_row(const ProductArgs& p) { return p.offsets ? max(p.offsets[0], 0) : 0; }
+__device__ __forceinline__ int end_row(const ProductArgs& p, int E) { return p.offsets ? min(p.offsets[E], p.R) : p.R; }
+
 // The epilogue of a product whose K was split.
 __global__ __launch_bounds__(kFinish) void finish_kernel(const float* __restrict__ part, int splits, PackedArgs w,
                                                          ProductArgs p) {
   const int width = p.gated ? w.N >> 1 : w.N, n = (blockIdx.x * kFinish + threadIdx.x) * 4;
   if (n >= width) return;
-  const int rows = p.offsets ? min(p.offsets[w.E], p.R) : p.R;
-  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+  const int rows = end_row(p, w.E);
+  for (int row = first_row(p) + blockIdx.y; row < rows; row += gridDim.y) {
     float4_t v = slices_sum(part, splits, p.R, w.N, row, n);
     float4_t up = {1.f, 1.f, 1.f, 1.f};
     if (p.gated) up = slices_sum(part, splits, p.R, w.N, row, width + n);
@@ -57,17 +61,18 @@ __global__ __launch_bounds__(kFinish) void finish_kernel(const float* __restrict
 }
 
 // y[t] = sum over the slots j, in order, of weights[t][j] * part[positions[t][j]]
-// + residual[t].
-__global__ __launch_bounds__(kFinish) void combine_kernel(const float* __restrict__ part, int splits, CombineArgs c,
-                                                          int R, int N) {
-  const int n = (blockIdx.x * kFinish + threadIdx.x) * 4;
+// + residual[t], over the slots whose rows the experts' ranges hold.
+__global__ __launch_bounds__(kFinish) void combine_kernel(const float* __restrict__ part, int splits, PackedArgs w,
+                                                          ProductArgs p, CombineArgs c) {
+  const int n = (blockIdx.x * kFinish + threadIdx.x) * 4, N = w.N;
   if (n >= N) return;
+  const int first = first_row(p), end = end_row(p, w.E);
   for (int t = blockIdx.y; t < c.T; t += gridDim.y) {
     float4_t sum = {0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < c.top_k; ++j) {
       const int at = c.positions[(int64_t)t * c.top_k + j];
-      if (at < 0 || at >= R) continue;
-      sum += c.weights[(int64_t)t * c.top_k + j] * slices_sum(part, splits, R, N, at, n);
+      if (at < first || at >= end) continue;
+      sum += c.weights[(int64_t)t * c.top_k + j] * slices_sum(part, splits, p.R, N, at, n);
     }
     half4_t out;
 #pragma unroll
@@ -219,7 +224,7 @@ hipError_t launch_combine(const PackedArgs& w, const ProductArgs& p, const Combi
   const hipError_t e = launch_planned(w, p, plan, part, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(combine_kernel, finish_grid(w.N, c.T), dim3(kFinish), 0, stream, part,
-                     plan.splits(), c, p.R, w.N);
+                     plan.splits(), w, p, c);
   return hipGetLastError();
 }
 

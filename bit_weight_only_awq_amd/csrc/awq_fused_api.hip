@@ -11,6 +11,7 @@
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }  // offsets: read one by one
 
 constexpr int32_t kMaxDim = 1 << 21;
 constexpr int32_t kMaxRows = 1 << 24;     // tokens, slots: keeps launch grids and row tiles in 32 bits
@@ -129,7 +130,7 @@ int awq_linear_experts(const void* x, int32_t ldx, int32_t x_rows, const int32_t
     return AWQ_ERR_SHAPE;
   if (rows && slots_per_row < 1) return AWQ_ERR_OPTION;
   if (!offsets) return AWQ_ERR_NULL;
-  if (!aligned16(offsets) || !aligned16(rows)) return AWQ_ERR_ALIGN;
+  if (!aligned4(offsets) || !aligned16(rows)) return AWQ_ERR_ALIGN;
   st = check_workspace(workspace, workspace_bytes,
                        awq_linear_experts_workspace_bytes(R, E, N, K, group_size, gated));
   if (st != AWQ_OK) return st;
@@ -159,7 +160,7 @@ int awq_combine_experts(const void* x, int32_t ldx, const int32_t* offsets, cons
   if (top_k < 1 || top_k > E || top_k > kMaxTopK) return AWQ_ERR_OPTION;
   if ((int64_t)T * top_k > kMaxRows) return AWQ_ERR_SHAPE;
   if (!offsets || !positions || !weights) return AWQ_ERR_NULL;
-  if (!aligned16(offsets) || !aligned16(positions) || !aligned16(weights)) return AWQ_ERR_ALIGN;
+  if (!aligned4(offsets) || !aligned16(positions) || !aligned16(weights)) return AWQ_ERR_ALIGN;
   st = check_workspace(workspace, workspace_bytes,
                        awq_combine_experts_workspace_bytes(T, top_k, E, N, K, group_size));
   if (st != AWQ_OK) return st;

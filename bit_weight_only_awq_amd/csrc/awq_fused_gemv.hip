@@ -26,12 +26,14 @@ namespace awq {
 namespace {
 
 // Row `r` of the sorted order: the expert whose range holds it, or -1.  `ends`:
-// the ends of the first 64 experts' ranges, one per lane (loaded early).
+// the ends of the first 64 experts' ranges, one per lane, and `first`, where the
+// first of them begins (loaded early).
 __device__ __forceinline__ int range_ends(const int* __restrict__ offsets, int E, int e0) {
   const int e = e0 + __lane_id();
   return e < E ? offsets[e + 1] : 0;
 }
-__device__ __forceinline__ int expert_of_row(const int* __restrict__ offsets, int E, int ends, int r) {
+__device__ __forceinline__ int expert_of_row(const int* __restrict__ offsets, int E, int first, int ends, int r) {
+  if (r < first) return -1;
   for (int e0 = 0; e0 < E; e0 += 64) {
     const unsigned long long past = __ballot((e0 == 0 ? ends : range_ends(offsets, E, e0)) > r);
     if (past != 0) return e0 + __builtin_ctzll(past);
@@ -155,10 +157,10 @@ __global__ __launch_bounds__(NW * QPW * 64) void fused_gemv_kernel(
   const _Float16* xr = x;
   if constexpr (GROUPED) {
     // (the source row is looked up beside the expert)
-    const int ends = range_ends(p.offsets, E, 0);
+    const int ends = range_ends(p.offsets, E, 0), first = p.offsets[0];
     int r = slot;
     if (p.rows) r = min(max(p.rows[slot] / p.slots_per_row, 0), p.x_rows - 1);
-    const int e = expert_of_row(p.offsets, E, ends, slot);
+    const int e = expert_of_row(p.offsets, E, first, ends, slot);
     if (e < 0) return;
     expert = e;
     xr = x + r * p.ldx;
@@ -212,7 +214,7 @@ __global__ __launch_bounds__(NW * 64) void combine_gemv_kernel(
   const int chunks = K >> 5, G = K >> gshift;
   // waves to slots: `side` of them share a slot's chunks, `sets` slots at a time
   const int side = c.top_k >= NW ? 1 : NW / c.top_k, sets = NW / side;
-  const int ends = range_ends(p.offsets, E, 0);
+  const int ends = range_ends(p.offsets, E, 0), first = p.offsets[0];
   const int rows = lane < c.top_k ? c.positions[(int64_t)t * c.top_k + lane] : -1;
   const float weights = lane < c.top_k ? c.weights[(int64_t)t * c.top_k + lane] : 0.0f;
   const DecodeConsts kc;
@@ -222,7 +224,7 @@ __global__ __launch_bounds__(NW * 64) void combine_gemv_kernel(
   for (int j = wave / side; j < c.top_k && wave < side * sets; j += sets) {
     const int row = __builtin_amdgcn_readlane(rows, j);
     const float weight = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weights), j));
-    const int e = row < 0 || row >= p.R ? -1 : expert_of_row(p.offsets, E, ends, row);
+    const int e = row < 0 || row >= p.R ? -1 : expert_of_row(p.offsets, E, first, ends, row);
     if (wave % side == 0 && lane == 0) {
       slot_expert[j] = e;
       slot_weight[j] = weight;

@@ -371,10 +371,13 @@ size_t awq_route_experts_workspace_bytes(int32_t T, int32_t E);
  * slots_per_row = top_k: the slot's token), or r with rows NULL.
  * qweight, scales, qzeros  in  [E] packed weights of one shape, one after the other.
  * bias     in   fp16 [E][N] or NULL.
- * offsets  in   int32 [E + 1] (device), ascending, offsets[E] <= R; values are
- *               clamped to [0, R], rows to x's x_rows rows, so that wrong ones
- *               give wrong results but never lead outside the buffers.
- * y        out  fp16, row r at y + r * ldy, r < offsets[E]; rows past it are left as they are.
+ * offsets  in   int32 [E + 1] (device, 4-byte aligned), ascending, offsets[E] <= R.
+ *               offsets[0] may be above 0: offsets + e0 of a route over more experts
+ *               names a slice of them.  Values are clamped to [0, R], rows to x's
+ *               x_rows rows, so that wrong ones give wrong results but never lead
+ *               outside the buffers.
+ * y        out  fp16, row r at y + r * ldy, offsets[0] <= r < offsets[E]; the rows
+ *               before and past them are left as they are.
  * R rows at most (R = T * top_k after a router), 1 <= R <= 2^24, E <= 1024; with
  * `rows`, x_rows * ldx < 2^30.  Weights are exact as above while R is at most
  * 2 rows per expert, or 64 with groups of 64 and more, and rounded past that; the rest
@@ -392,10 +395,11 @@ size_t awq_linear_experts_workspace_bytes(int32_t R, int32_t E, int32_t N, int32
  * awq_combine_experts - the experts' second layer and the weighted sum per token:
  *   y[t] = sum_j weights[t][j] (x[positions[t][j]] . W'_e^T + bias_e) + residual[t]
  * x holds the T * top_k rows sorted by expert (awq_linear_experts' output), e
- * the expert whose range of offsets holds the row.  Slots with a negative
- * position add nothing (a token without any: y = residual, or 0).  The sum
+ * the expert whose range of offsets holds the row.  Slots whose position is
+ * negative or in no expert's range (a slice of the experts, as above) add
+ * nothing (a token without any: y = residual, or 0).  The sum
  * runs over j in order, in fp32, on unrounded products; one rounding to fp16.
- * positions, weights  in  int32, fp32 [T][top_k]; the other arguments as above.
+ * positions, weights  in  int32, fp32 [T][top_k], top_k <= min(E, 64); the other arguments as above.
  * workspace: awq_combine_experts_workspace_bytes() bytes, under the contract
  * of awq_gemm's workspace.
  */
