@@ -534,13 +534,14 @@ def _activation(name: str) -> int:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}; got {name!r}") from None
 
 
-def _with_workspace(call, need, where: str, workspace: Optional[torch.Tensor], t: torch.Tensor, stream: int) -> None:
-    """``call(address, bytes)`` with the caller's workspace, or else with the one of the current stream: the call says
-    itself when that is too small, and only then is its size (``need()``) asked for."""
-    ws = workspace if workspace is not None else _WORKSPACES.get((t.get_device(), stream))
-    st = call(None, 0) if ws is None else call(_ptr(ws), ws.numel() * ws.element_size())
+def _with_workspace(call, need, where: str, workspace: Optional[torch.Tensor], t: torch.Tensor) -> None:
+    """``call(address, bytes)`` with the caller's workspace, or else without one: the call says itself when it needs one,
+    and then gets ``need()`` bytes beside ``t`` for this call only.  (Its two launches hand partial sums on in them, so
+    calls of several host threads on one stream must not share them; and a buffer kept for the stream would grow
+    with the largest batch and stay.  Under graph capture the bytes come from the graph's own memory.)"""
+    st = call(_ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
     if st == AWQ_ERR_WORKSPACE and workspace is None:
-        ws = gemm_workspace(int(need()), t.device)
+        ws = t.new_empty(need(), dtype=torch.uint8)
         st = call(ws.data_ptr(), ws.numel())
     if st != AWQ_OK:
         raise AwqError(st, where)
@@ -574,8 +575,7 @@ def linear_fused(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor]
     _with_workspace(
         lambda ws, n: lib.awq_linear_fused(xp, ldx, qp, sp, zp, bp, act, gated, rp, ldr, yp, ldy, M, N, K, group_size,
                                            zero_point, ws, n, stream),
-        lambda: lib.awq_linear_fused_workspace_bytes(M, N, K, group_size, gated), "awq_linear_fused", workspace, x2,
-        stream)
+        lambda: lib.awq_linear_fused_workspace_bytes(M, N, K, group_size, gated), "awq_linear_fused", workspace, x2)
     return out if y is not None or x.dim() == 2 else out.reshape(*x.shape[:-1], width)
 
 
@@ -684,7 +684,7 @@ def linear_experts(x: torch.Tensor, pe: PackedExperts, route: ExpertRoute, bias:
         lambda ws, n: lib.awq_linear_experts(xp, ldx, T, wp, top_k, op, R, E, qp, sp, zp, bp, act, gated, yp, ldy, N, K,
                                              group_size, zero_point, ws, n, stream),
         lambda: lib.awq_linear_experts_workspace_bytes(R, E, N, K, group_size, gated), "awq_linear_experts", workspace,
-        x, stream)
+        x)
     return out
 
 
@@ -714,7 +714,7 @@ def combine_experts(h: torch.Tensor, pe: PackedExperts, route: ExpertRoute, bias
         lambda ws, n: lib.awq_combine_experts(hp, ldh, op, pp, wp, T, top_k, E, qp, sp, zp, bp, rp, ldr, yp, ldy, N, K,
                                               group_size, zero_point, ws, n, stream),
         lambda: lib.awq_combine_experts_workspace_bytes(T, top_k, E, N, K, group_size), "awq_combine_experts",
-        workspace, h, stream)
+        workspace, h)
     return out
 
 

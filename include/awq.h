@@ -326,9 +326,12 @@ size_t awq_clip_search_workspace_bytes(int32_t count, int32_t M, int32_t N, int3
  * Strides are in elements, multiples of 8, at least the row and at most 2^21.
  * N a multiple of 8 (gated: of 16); M <= 2^24.  Other checks as awq_gemm's
  * (device pointers 16-byte aligned); AWQ_ERR_OPTION for an unknown activation.
- * workspace: awq_linear_fused_workspace_bytes() bytes (NULL when 0), under the
- * contract of awq_gemm's workspace: its first 512 KiB are zero at first use and
- * every call leaves them zero, so both share one buffer in stream order.
+ * workspace: awq_linear_fused_workspace_bytes() bytes (NULL when 0), contents
+ * not needed before or after; the first 512 KiB are not touched, so awq_gemm's
+ * workspace serves in stream order.  A call that needs one enqueues two kernels,
+ * the second of which reads what the first wrote there: calls whose launches
+ * may interleave (several streams, or several host threads on one stream) need
+ * a workspace each.
  */
 int awq_linear_fused(const void* x, int32_t ldx, const uint32_t* qweight, const void* scales, const uint32_t* qzeros,
                      const void* bias, int32_t activation, int32_t gated, const void* residual, int32_t ldr, void* y,
@@ -353,8 +356,8 @@ size_t awq_linear_fused_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t
  * rows       out  int32 [T * top_k]: the slot at each place of that order, -1 past offsets[E].
  * positions  out  int32 [T][top_k]: each slot's place in that order.
  * 1 <= E <= 1024, top_k <= min(E, 64), T * top_k <= 2^24.  Deterministic.
- * workspace: awq_route_experts_workspace_bytes() bytes, contents not needed
- * before or after (NULL when 0).
+ * workspace: awq_route_experts_workspace_bytes() bytes (NULL when 0), contents
+ * not needed before or after; shared as awq_linear_fused's.
  */
 int awq_route_experts(const void* logits, int32_t ld, int32_t fp32_logits, int32_t T, int32_t E, int32_t top_k,
                       int32_t renormalize, int32_t* ids, float* weights, int32_t* offsets, int32_t* rows,
@@ -400,8 +403,8 @@ size_t awq_linear_experts_workspace_bytes(int32_t R, int32_t E, int32_t N, int32
  * nothing (a token without any: y = residual, or 0).  The sum
  * runs over j in order, in fp32, on unrounded products; one rounding to fp16.
  * positions, weights  in  int32, fp32 [T][top_k], top_k <= min(E, 64); the other arguments as above.
- * workspace: awq_combine_experts_workspace_bytes() bytes, under the contract
- * of awq_gemm's workspace.
+ * workspace: awq_combine_experts_workspace_bytes() bytes (the fp32 products of
+ * all T * top_k rows, past a few rows), as awq_linear_fused's.
  */
 int awq_combine_experts(const void* x, int32_t ldx, const int32_t* offsets, const int32_t* positions,
                         const float* weights, int32_t T, int32_t top_k, int32_t E, const uint32_t* qweight,
