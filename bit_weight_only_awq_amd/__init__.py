@@ -640,19 +640,32 @@ class PackedExperts(NamedTuple):
     zero_point: bool
 
 
+_PACK_ROWS = 1 << 21  # most rows of one awq_pack call
+
+
 def pack_experts(W, q_group_size: int = 128, zero_point: bool = True) -> PackedExperts:
     """Quantize the experts' weights [E, out, in] (a tensor, or a list of [out, in]).  Expert by expert the same
-    bits as ``pack``: the rows of all experts are one tall weight to ``awq_pack``."""
+    bits as ``pack``: rows are independent and octets of them do not cross experts, so the rows of as many experts
+    as one call takes are one tall weight to ``awq_pack``."""
     W = W if isinstance(W, torch.Tensor) else torch.stack(list(W))
     if W.dtype != torch.float16 or W.dim() != 3:
         raise ValueError("W must be a 3-D float16 tensor [E, N, K]")
     E, N, K = W.shape
+    if N % 8:
+        raise AwqError(AWQ_ERR_SHAPE, "awq_pack")
     G = K // q_group_size if q_group_size > 0 else 0
     qweight = torch.empty((E, N, K // 8), dtype=torch.int32, device=W.device)
     scales = torch.empty((E, N // 8, G, 8), dtype=torch.float16, device=W.device)
     qzeros = torch.empty((E, N // 8, G), dtype=torch.int32, device=W.device) if zero_point else None
-    for e in range(E):
-        awq_pack(W[e], q_group_size, zero_point, qweight[e], scales[e], qzeros[e] if zero_point else None)
+    step = max(1, _PACK_ROWS // max(N, 1))
+    for e in range(0, E, step):
+        part = slice(e, min(e + step, E))
+        own = qzeros[part] if zero_point else None
+        if zero_point and own.data_ptr() % 16:  # awq_pack writes whole aligned buffers: through one, then in place
+            own = torch.empty_like(own)
+        awq_pack(W[part].flatten(0, 1), q_group_size, zero_point, qweight[part], scales[part], own)
+        if zero_point and own.data_ptr() != qzeros[part].data_ptr():
+            qzeros[part] = own
     return PackedExperts(qweight, scales, qzeros, E, N, K, q_group_size, bool(zero_point))
 
 
