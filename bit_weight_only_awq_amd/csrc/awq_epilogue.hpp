@@ -12,13 +12,15 @@ namespace awq {
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 
 // v = act(v) in fp32.  Each form passes NaN on; silu and the two gelus are
-// written with one exponential (or erf) of the argument.
+// written with one exponential (or erfc) of the argument, and no form adds numbers
+// that cancel: the small values below zero keep their relative accuracy, which a
+// gate's other factor carries back into fp16's range.
 __device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
     case 1: return v < 0.0f ? 0.0f : v;
     case 2: return v * sigmoid(v);
-    case 3: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case 3: return 0.5f * v * erfcf(v * -0.70710678118654752f);
     // 0.5 v (1 + tanh u) = v sigmoid(2 u), u = sqrt(2 / pi) (v + 0.044715 v^3)
     case 4: return v * sigmoid(1.5957691216057308f * (v + 0.044715f * v * v * v));
     default: return v;

@@ -70,7 +70,7 @@ enum awq_activation {
   AWQ_ACT_NONE = 0,
   AWQ_ACT_RELU = 1,
   AWQ_ACT_SILU = 2,     /* v / (1 + exp(-v))                                         */
-  AWQ_ACT_GELU = 3,     /* v (1 + erf(v / sqrt 2)) / 2                               */
+  AWQ_ACT_GELU = 3,     /* v (1 + erf(v / sqrt 2)) / 2 = v erfc(-v / sqrt 2) / 2     */
   AWQ_ACT_GELU_TANH = 4 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2         */
 };
 
