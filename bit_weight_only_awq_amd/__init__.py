@@ -612,6 +612,9 @@ def route_experts(logits: torch.Tensor, top_k: int, renormalize: bool = True,
         raise ValueError("logits must have contiguous rows")
     if not 1 <= top_k <= min(E, 64):
         raise AwqError(AWQ_ERR_OPTION, "awq_route_experts")
+    if logits.data_ptr() % 16:  # a view that begins inside a 16-byte unit: the library takes aligned buffers
+        logits = logits.clone(memory_format=torch.contiguous_format)
+        ld = E
     shape = (T, top_k)
     ids = logits.new_empty(shape, dtype=_I32)
     weights = logits.new_empty(shape, dtype=_F32)

@@ -349,7 +349,8 @@ size_t awq_linear_fused_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t
  * a slot left without an expert (a token with fewer than top_k logits that are
  * not masked, all of them for a token to skip) has id -1, weight 0 and
  * position -1.  Logits of +inf share the weight equally.
- * logits     in   fp16 or (fp32_logits != 0) fp32, row t at logits + t * ld elements, ld >= E.
+ * logits     in   fp16 or (fp32_logits != 0) fp32, row t at logits + t * ld elements, ld >= E
+ *                 (any such ld; the first row 16-byte aligned, as all buffers here).
  * ids        out  int32 [T][top_k];  weights out fp32 [T][top_k].
  * offsets    out  int32 [E + 1]: the routed slots sorted by expert, and by slot
  *                 within one, put expert e's at offsets[e] .. offsets[e + 1] - 1.
