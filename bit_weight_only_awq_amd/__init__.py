@@ -562,7 +562,8 @@ def linear_fused(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor]
     act = _activation(activation)
     rp, ldr = None, 0
     if residual is not None:
-        rp, ldr = _rows2d(residual if residual.dim() == 2 else residual.reshape(-1, width), M, width, "residual")
+        r2 = residual if residual.dim() == 2 else residual.reshape(-1, width)  # (a copy lives until the call returns)
+        rp, ldr = _rows2d(r2, M, width, "residual")
     if y is None:
         out = x2.new_empty((M, width))
         yp, ldy = out.data_ptr(), width
