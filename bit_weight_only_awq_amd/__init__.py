@@ -556,13 +556,19 @@ def linear_fused(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor]
     ``residual`` itself.  One rounding to fp16."""
     lib = _lib or load_library()
     qweight, scales, qzeros, N, K, group_size, zero_point = pw
+    if x.dim() != 2 and x.shape[-1:] != (K,):
+        raise ValueError(f"x must be a float16 tensor [..., {K}]")
     x2 = x if x.dim() == 2 else x.reshape(-1, K)
     M, width = x2.shape[0], N // 2 if gated else N
     xp, ldx = _rows2d(x2, None, K, "x")
     act = _activation(activation)
     rp, ldr = None, 0
     if residual is not None:
-        r2 = residual if residual.dim() == 2 else residual.reshape(-1, width)  # (a copy lives until the call returns)
+        r2 = residual
+        if residual.dim() != 2:
+            if residual.shape != (*x.shape[:-1], width):
+                raise ValueError(f"residual must be a float16 tensor {[*x.shape[:-1], width]}")
+            r2 = residual.reshape(-1, width)
         rp, ldr = _rows2d(r2, M, width, "residual")
     if y is None:
         out = x2.new_empty((M, width))
