@@ -553,7 +553,7 @@ def linear_fused(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor]
     """act(x . W'^T + bias) + residual for fp16 ``x`` [..., K], in one call.  With ``gated`` the first half of
     ``pw``'s rows is the gate (``pack_fused([gate, up])``): act(gate) * up, half as many columns.  ``x``,
     ``residual`` and ``y`` may be 2-D views with a row stride (a multiple of 8 elements); ``y`` may be
-    ``residual`` itself.  One rounding to fp16."""
+    ``residual`` itself.  One rounding to fp16.  No tokens give an empty result, here and in the calls below."""
     lib = _lib or load_library()
     qweight, scales, qzeros, N, K, group_size, zero_point = pw
     if x.dim() != 2 and x.shape[-1:] != (K,):
@@ -579,10 +579,11 @@ def linear_fused(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor]
     bp = _flat(bias, (N,), _F16, "bias")
     qp, sp, zp = _ptr(qweight), _ptr(scales), _ptr(qzeros) if zero_point else None
     stream = _handle(x2)
-    _with_workspace(
-        lambda ws, n: lib.awq_linear_fused(xp, ldx, qp, sp, zp, bp, act, gated, rp, ldr, yp, ldy, M, N, K, group_size,
-                                           zero_point, ws, n, stream),
-        lambda: lib.awq_linear_fused_workspace_bytes(M, N, K, group_size, gated), "awq_linear_fused", workspace, x2)
+    if M > 0:
+        _with_workspace(
+            lambda ws, n: lib.awq_linear_fused(xp, ldx, qp, sp, zp, bp, act, gated, rp, ldr, yp, ldy, M, N, K,
+                                               group_size, zero_point, ws, n, stream),
+            lambda: lib.awq_linear_fused_workspace_bytes(M, N, K, group_size, gated), "awq_linear_fused", workspace, x2)
     return out if y is not None or x.dim() == 2 else out.reshape(*x.shape[:-1], width)
 
 
@@ -628,6 +629,8 @@ def route_experts(logits: torch.Tensor, top_k: int, renormalize: bool = True,
     offsets = logits.new_empty(E + 1, dtype=_I32)
     rows = logits.new_empty(T * top_k, dtype=_I32)
     positions = logits.new_empty(shape, dtype=_I32)
+    if T == 0:
+        return ExpertRoute(ids, weights, offsets.zero_(), rows, positions)
     need = lib.awq_route_experts_workspace_bytes(T, E) if workspace is None else 0
     if need:
         workspace = logits.new_empty(need, dtype=torch.uint8)
@@ -703,11 +706,12 @@ def linear_experts(x: torch.Tensor, pe: PackedExperts, route: ExpertRoute, bias:
     bp = _flat(bias, (E, N), _F16, "bias")
     qp, sp, zp = _ptr(qweight), _ptr(scales), _ptr(qzeros) if zero_point else None
     stream = _handle(x)
-    _with_workspace(
-        lambda ws, n: lib.awq_linear_experts(xp, ldx, T, wp, top_k, op, R, E, qp, sp, zp, bp, act, gated, yp, ldy, N, K,
-                                             group_size, zero_point, ws, n, stream),
-        lambda: lib.awq_linear_experts_workspace_bytes(R, E, N, K, group_size, gated), "awq_linear_experts", workspace,
-        x)
+    if R > 0:
+        _with_workspace(
+            lambda ws, n: lib.awq_linear_experts(xp, ldx, T, wp, top_k, op, R, E, qp, sp, zp, bp, act, gated, yp, ldy, N,
+                                                 K, group_size, zero_point, ws, n, stream),
+            lambda: lib.awq_linear_experts_workspace_bytes(R, E, N, K, group_size, gated), "awq_linear_experts",
+            workspace, x)
     return out
 
 
@@ -733,11 +737,12 @@ def combine_experts(h: torch.Tensor, pe: PackedExperts, route: ExpertRoute, bias
     bp = _flat(bias, (E, N), _F16, "bias")
     qp, sp, zp = _ptr(qweight), _ptr(scales), _ptr(qzeros) if zero_point else None
     stream = _handle(h)
-    _with_workspace(
-        lambda ws, n: lib.awq_combine_experts(hp, ldh, op, pp, wp, T, top_k, E, qp, sp, zp, bp, rp, ldr, yp, ldy, N, K,
-                                              group_size, zero_point, ws, n, stream),
-        lambda: lib.awq_combine_experts_workspace_bytes(T, top_k, E, N, K, group_size), "awq_combine_experts",
-        workspace, h)
+    if T > 0:
+        _with_workspace(
+            lambda ws, n: lib.awq_combine_experts(hp, ldh, op, pp, wp, T, top_k, E, qp, sp, zp, bp, rp, ldr, yp, ldy, N,
+                                                  K, group_size, zero_point, ws, n, stream),
+            lambda: lib.awq_combine_experts_workspace_bytes(T, top_k, E, N, K, group_size), "awq_combine_experts",
+            workspace, h)
     return out
 
 
