@@ -2,13 +2,12 @@
 // up to XR rows x 32 CW weight rows, with every operand flowing through a ring
 // of LDS stages.
 //
-// Mathematics: awq_experts.hip's.  For groups of 64 channels and more the
-// matrix cores multiply the exact integers q - z, and the group's scale
-// multiplies the fp32 sum once per group and output (16 multiply-adds per 32 x 32
-// tile in place of four packed multiplies per packed word): no weight is
-// rounded.  With groups of 32 the two lane halves of a matrix instruction
-// lie in different groups, and the weights are decoded to fp16((q - z) s), one
-// rounding each (relative 2^-11).
+// Mathematics: awq_experts.hip's.  The matrix cores multiply the exact integers
+// q - z, and the group's scale multiplies the fp32 sum once per group and output
+// (16 multiply-adds per 32 x 32 tile in place of four packed multiplies per
+// packed word): no weight is rounded.  A lane holds 32 channels of a 64-channel
+// block; with groups of 32 the lane halves, whose channels then lie in different
+// groups, exchange every other word first.
 //
 // Bound: HBM, the packed weights once, and what a compute unit takes in: a load
 // whose 64 lanes touch 32 rows of 32 bytes runs at 37 bytes/ns per compute
@@ -26,7 +25,8 @@
 //
 // Measured: 48 tokens x 6 of 64, 2048 -> 2816 gated: 46.2 us, 4.1 TB/s of the
 // packed weights (floor 37.0); 24 tokens 40.0 us, 4.4 TB/s; 16 x 4096 -> 4096:
-// 9.3 us; 13 x 11008 -> 4096: 15.0; 61 x 4096 -> 11008, groups of 64: 17.9 (5.0).
+// 9.3 us; 13 x 11008 -> 4096: 15.0; 61 x 4096 -> 11008, groups of 64: 18.2 (5.0),
+// of 32: 22.3.
 #include "awq_epilogue.hpp"
 #include "awq_launch_fused.hpp"
 
@@ -168,6 +168,8 @@ __global__ __launch_bounds__(CW* KW * 64) void stream_kernel(PackedArgs w, Produ
   // scale is applied while the next group multiplies.
   u32x4 wv[NBLK];
   half8_t af[2][4][RT];
+  // slice j's chunk of 8 channels within the block, for X and W alike
+  auto chunk_of = [&](int j) __attribute__((always_inline)) { return GROUP == 0 ? 2 * j + fh : 4 * fh + j; };
   auto read_block = [&](int c, int b) __attribute__((always_inline)) {
     const char* xs = ring(c) + kw * XR * XROW;
 #pragma unroll
@@ -175,7 +177,7 @@ __global__ __launch_bounds__(CW* KW * 64) void stream_kernel(PackedArgs w, Produ
 #pragma unroll
       for (int a = 0; a < RT; ++a)
         af[b & 1][j][a] = *reinterpret_cast<const half8_t*>(xs + (32 * a + (fi & (XT - 1))) * XROW +
-                                                            16 * ((8 * b + 4 * fh + j) ^ (fi & 15)));
+                                                            16 * ((8 * b + chunk_of(j)) ^ (fi & 15)));
   };
   auto begin = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
@@ -188,52 +190,68 @@ __global__ __launch_bounds__(CW* KW * 64) void stream_kernel(PackedArgs w, Produ
   // half of a matrix instruction's result unused, the compiler let another's
   // overlap that half, and sums came out wrong.)
   float16_t tmp[2][RT];
-  auto apply = [&](int g, const Groups& x) __attribute__((always_inline)) {
-    const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)x.s[g]);
+  auto apply = [&](int g, float s) __attribute__((always_inline)) {
 #pragma unroll
     for (int a = 0; a < RT; ++a)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[a][r] = __builtin_fmaf(tmp[g & 1][a][r], s, acc[a][r]);
   };
+  auto scale_of = [&](uint32_t bits) __attribute__((always_inline)) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+  };
   auto compute = [&](int c, const Groups& x) __attribute__((always_inline)) {
+    ZeroBias zb;
+    float scale[2];  // of the last two groups
 #pragma unroll
     for (int b = 0; b < NBLK; ++b) {
-      const int g = GROUP == 2 ? b / 2 : b;
       if (b + 1 < NBLK) read_block(c, b + 1);
       __builtin_amdgcn_sched_barrier(0);
-      const ZeroBias zb = zero_bias(ZP ? (x.z[g] >> zshift) & 15u : 8u);
-      const _Float16 sh = __builtin_bit_cast(_Float16, (uint16_t)x.s[g]);
-      const bool first = GROUP == 1 || b % 2 == 0;
+      uint32_t z[2], sb[2], w[4];  // the block's two groups (groups of 32), or its one in [0]
+      {
+        const int g = GROUP == 2 ? b / 2 : b;
+        z[0] = ZP ? (x.z[g] >> zshift) & 15u : 8u;
+        sb[0] = x.s[g];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = wv[b][j];
+      }
+      if constexpr (GROUP == 0) {
+        // (words 4 h .. 4 h + 3 of lane half h: after the exchange 2 j + h in place j)
+        const auto w01 = __builtin_amdgcn_permlane32_swap(w[0], w[1], false, false);
+        const auto w23 = __builtin_amdgcn_permlane32_swap(w[2], w[3], false, false);
+        const auto zz = __builtin_amdgcn_permlane32_swap(z[0], z[0], false, false);
+        const auto ss = __builtin_amdgcn_permlane32_swap(sb[0], sb[0], false, false);
+        const uint32_t w0 = w01[0], w2 = w01[1], w1 = w23[0], w3 = w23[1];
+        const uint32_t z0 = zz[0], z1 = zz[1], s0 = ss[0], s1 = ss[1];
+        w[0] = w0, w[1] = w1, w[2] = w2, w[3] = w3;
+        z[0] = z0, z[1] = z1, sb[0] = s0, sb[1] = s1;
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        half8_t bf;
-        if constexpr (GROUP == 0) {
-          bf = decode_word_scaled(wv[b][j], zb, kc, splat2(sh));
-        } else {
-          half2_t d[4];
-          decode_pairs(wv[b][j], zb, kc, d);
-          bf = half8_t{d[0][0], d[0][1], d[1][0], d[1][1], d[2][0], d[2][1], d[3][0], d[3][1]};
-        }
+        const int half = GROUP == 0 ? j / 2 : 0, g = GROUP == 0 ? 2 * b + half : GROUP == 2 ? b / 2 : b;
+        const bool first = GROUP == 0 ? j % 2 == 0 : j == 0 && (GROUP == 1 || b % 2 == 0);
+        if (j == 2 * half) zb = zero_bias(z[half]);
+        if (first) scale[g & 1] = scale_of(sb[half]);
+        half2_t d[4];
+        decode_pairs(w[j], zb, kc, d);
+        const half8_t bf = half8_t{d[0][0], d[0][1], d[1][0], d[1][1], d[2][0], d[2][1], d[3][0], d[3][1]};
 #pragma unroll
-        for (int a = 0; a < RT; ++a) {
-          if constexpr (GROUP == 0)
-            acc[a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[b & 1][j][a], bf, acc[a], 0, 0, 0);
-          else
-            tmp[g & 1][a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                af[b & 1][j][a], bf, j == 0 && first ? float16_t(0.0f) : tmp[g & 1][a], 0, 0, 0);
-        }
+        for (int a = 0; a < RT; ++a)
+          tmp[g & 1][a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+              af[b & 1][j][a], bf, first ? float16_t(0.0f) : tmp[g & 1][a], 0, 0, 0);
         // With a constant zero as its addend, the compiler may give a matrix
         // instruction a destination that overlaps its operands, which this one
         // (8 passes) writes before it has read them all: they stay alive past it.
-        if (GROUP != 0 && j == 0 && first) {
+        if (first) {
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int a = 0; a < RT; ++a) asm volatile("" ::"v"(af[b & 1][j][a]), "v"(bf));
         }
-        if (GROUP != 0 && j == 1 && first && b > 0) apply(g - 1, x);
+        const bool second = GROUP == 0 ? j % 2 == 1 : j == 1 && (GROUP == 1 || b % 2 == 0);
+        if (second && g > 0) apply(g - 1, scale[(g - 1) & 1]);
       }
     }
-    if constexpr (GROUP != 0) apply(NS - 1, x);
+    constexpr int LAST = GROUP == 0 ? 2 * NBLK - 1 : NS - 1;
+    apply(LAST, scale[LAST & 1]);
   };
 
   // stage s has landed once at most the loads of the D - 2 stages after it are

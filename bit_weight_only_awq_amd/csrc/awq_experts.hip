@@ -98,25 +98,37 @@ struct Plan {
 // two are rare (their weights are then read twice, the second time from L2).
 bool one_row_each(int R, int E) { return R == 1 || 2 * R <= E; }
 
-// Tile height and K split of the matrix-core tiles, from a time model: rounds of
-// workgroups over the compute units, each a tile's steps (a 64-channel step of
-// 256 rows 1.75 us, of 128 rows 1.0, of 64 rows 0.66: 0.29 + 0.18 per 32 rows)
-// and ~6 us to begin and end it (256 weight rows, gated or not); with K split, the fp32 partials written and
-// read at ~4 TB/s and one more launch.
-TilePlan plan_tiles(int R, int experts, int N, int K) {
+// Tile height and K split of the matrix-core tiles, from a time model: each of 256
+// compute units takes its share of the tiles (256 weight rows each, gated or not),
+// two at a time.  A 64-channel step of one tile takes 0.55 us + 0.115 per 32 rows
+// (128 rows: 1.01, 64: 0.78), of two tiles at once 0.7 + 0.25 (1.7, 1.2), 1.3 times
+// that in groups of 32; 5 us begin and end a tile; partial sums are written and read at 5.5 TB/s and
+// cost a launch (5 us).  us of the choice / of others, groups of 128:
+//   512 x 4096 -> 11008: 128 rows: 69.7 / in 2: 77.5; 64 rows: 78.6
+//   700 x 4096 -> 11008: 64 rows: 87.5 / 128 rows: 105.5 (258 tiles: two units have two)
+//   512 x 11008 -> 4096: 128 rows in 4: 65.8 / in 3: 71.8, unsplit: 167; 64 rows: 131
+//   1024 x 11008 -> 4096: 128 rows in 2: 109.1 / unsplit: 167, in 4: 113.1
+//   1000 tokens x 2 of 8, 11008 -> 4096 combined: in 3: 251 / unsplit: 320, in 2: 257
+//   2000 tokens x 6 of 64, 2048 -> 2816 gated: 196 / in 2: 291; 64 rows: 232
+// (20 shapes: at most 4% above the best of seven plans.)  `summed`: the
+// products are partial sums in any case (combining).
+TilePlan plan_tiles(int R, int experts, int N, int K, int group_size, bool summed) {
   const int steps = (K + 63) / 64, columns = (N + 255) / 256;
   constexpr double kUnits = 256;
-  TilePlan best{256, 1, steps};
+  const double slow = group_size == 32 ? 1.3 : 1.0;
+  TilePlan best{64, 1, steps};
   double best_us = 1e300;
-  for (int rows : {256, 128, 64}) {
+  for (int rows : {group_size == 32 ? 96 : 128, 64}) {
     // ragged experts end in half a tile each on average
     const double tiles = experts == 1 ? (R + rows - 1) / rows : experts * ((double)R / experts / rows + 0.5);
-    const double height = R / tiles / 32;
-    const double step_us = 0.29 + 0.18 * (experts == 1 ? ceil(height) : height < 2 ? 2 : height);
+    const double mean = R / tiles / 32, height = experts == 1 ? ceil(mean) : mean < 1 ? 1 : mean;
+    const double one = slow * (0.55 + 0.115 * height), two = slow * (0.7 + 0.25 * height);
     for (int s = 1; s <= 16 && s <= steps; ++s) {
-      const int per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
-      const double rounds = ceil(tiles * columns * splits / kUnits);
-      const double us = rounds * (per * step_us + 6.0) + (splits > 1 ? splits * (double)R * N * 8 / 4e6 + 3.0 : 0.0);
+      // (slices of an even number of steps: no group of 128 channels is cut)
+      const int per = s == 1 ? steps : ((steps + s - 1) / s + 1) & ~1, splits = (steps + per - 1) / per;
+      const int64_t each = (int64_t)ceil(tiles * columns * splits / kUnits);
+      const double us = (each / 2) * (per * two + 5.0) + (each % 2) * (per * one + 5.0) +
+                        (splits > 1 || summed ? splits * (double)R * N * 8 / 5.5e6 + 5.0 : 0.0);
       if (us < best_us) best_us = us, best = TilePlan{rows, splits, per};
     }
   }
@@ -163,7 +175,7 @@ StreamPlan plan_stream(int R, int experts, int N, int K) {
   return plan(32, 4, 2, c > 128 ? 1 : c > 80 ? 2 : c > 40 ? 4 : 8);
 }
 
-Plan plan_product(int R, int E, int N, int K) {
+Plan plan_product(int R, int E, int N, int K, int group_size, bool summed) {
   const int experts = E == 0 ? 1 : E < R ? E : R;  // E = 0: one expert, R rows known to the host
   const double each = (double)R / experts;
   // (the first two kernels address an expert's packed words with 31 bits)
@@ -171,7 +183,7 @@ Plan plan_product(int R, int E, int N, int K) {
     if (each <= (E == 0 ? 8 : 2)) return Plan{Plan::kFew, E == 0 && R > 4 ? 8 : 4, {}, {}};
     if (each <= (E == 0 ? 256 : 64)) return Plan{Plan::kStream, 0, plan_stream(R, experts, N, K), {}};
   }
-  return Plan{Plan::kTiles, 0, {}, plan_tiles(R, experts, N, K)};
+  return Plan{Plan::kTiles, 0, {}, plan_tiles(R, experts, N, K, group_size, summed)};
 }
 
 size_t part_bytes(const Plan& plan, int R, int N) {
@@ -194,37 +206,37 @@ hipError_t launch_planned(const PackedArgs& w, const ProductArgs& p, const Plan&
 
 }  // namespace
 
-size_t product_workspace_bytes(int R, int E, int N, int K, bool) {
+size_t product_workspace_bytes(int R, int E, int N, int K, int group_size) {
   if (one_row_each(R, E)) return 0;
-  const Plan plan = plan_product(R, E, N, K);
+  const Plan plan = plan_product(R, E, N, K, group_size, false);
   return plan.splits() > 1 ? part_bytes(plan, R, N) : 0;
 }
 
 hipError_t launch_product(const PackedArgs& w, const ProductArgs& p, void* workspace, hipStream_t stream) {
   if (one_row_each(p.R, p.offsets ? w.E : 0)) return launch_fused_gemv(w, p, log2_group(w.group_size), stream);
-  const Plan plan = plan_product(p.R, p.offsets ? w.E : 0, w.N, w.K);
+  const Plan plan = plan_product(p.R, p.offsets ? w.E : 0, w.N, w.K, w.group_size, false);
   if (plan.splits() <= 1) return launch_planned(w, p, plan, nullptr, stream);
   float* part = part_of(workspace);
   const hipError_t e = launch_planned(w, p, plan, part, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(finish_kernel, finish_grid(p.gated ? w.N / 2 : w.N, p.R), dim3(kFinish), 0, stream, part, plan.splits(), w, p);
+  hipLaunchKernelGGL(finish_kernel, finish_grid(p.gated ? w.N / 2 : w.N, p.R), dim3(kFinish), 0, stream, part,
+                     plan.splits(), w, p);
   return hipGetLastError();
 }
 
-size_t combine_workspace_bytes(int T, int top_k, int E, int N, int K) {
+size_t combine_workspace_bytes(int T, int top_k, int E, int N, int K, int group_size) {
   if (one_row_each(T * top_k, E)) return 0;
-  return part_bytes(plan_product(T * top_k, E, N, K), T * top_k, N);
+  return part_bytes(plan_product(T * top_k, E, N, K, group_size, true), T * top_k, N);
 }
 
 hipError_t launch_combine(const PackedArgs& w, const ProductArgs& p, const CombineArgs& c, void* workspace,
                           hipStream_t stream) {
   if (one_row_each(p.R, w.E)) return launch_combine_gemv(w, p, c, log2_group(w.group_size), stream);
-  const Plan plan = plan_product(p.R, w.E, w.N, w.K);
+  const Plan plan = plan_product(p.R, w.E, w.N, w.K, w.group_size, true);
   float* part = part_of(workspace);
   const hipError_t e = launch_planned(w, p, plan, part, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(combine_kernel, finish_grid(w.N, c.T), dim3(kFinish), 0, stream, part,
-                     plan.splits(), w, p, c);
+  hipLaunchKernelGGL(combine_kernel, finish_grid(w.N, c.T), dim3(kFinish), 0, stream, part, plan.splits(), w, p, c);
   return hipGetLastError();
 }
 

@@ -70,7 +70,7 @@ extern "C" {
 
 size_t awq_linear_fused_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t group_size, int32_t gated) {
   if (M < 1 || M > kMaxRows || !shape_known(N, K, group_size, gated)) return 0;
-  return awq::product_workspace_bytes(M, 0, N, K, gated != 0);
+  return awq::product_workspace_bytes(M, 0, N, K, group_size);
 }
 
 int awq_linear_fused(const void* x, int32_t ldx, const uint32_t* qweight, const void* scales, const uint32_t* qzeros,
@@ -114,7 +114,7 @@ int awq_route_experts(const void* logits, int32_t ld, int32_t fp32_logits, int32
 size_t awq_linear_experts_workspace_bytes(int32_t R, int32_t E, int32_t N, int32_t K, int32_t group_size,
                                           int32_t gated) {
   if (R < 1 || R > kMaxRows || E < 1 || E > kMaxExperts || !shape_known(N, K, group_size, gated)) return 0;
-  return awq::product_workspace_bytes(R, E, N, K, gated != 0);
+  return awq::product_workspace_bytes(R, E, N, K, group_size);
 }
 
 int awq_linear_experts(const void* x, int32_t ldx, int32_t x_rows, const int32_t* rows, int32_t slots_per_row,
@@ -145,7 +145,7 @@ size_t awq_combine_experts_workspace_bytes(int32_t T, int32_t top_k, int32_t E, 
   if (T < 1 || top_k < 1 || (int64_t)T * top_k > kMaxRows || E < 1 || E > kMaxExperts ||
       !shape_known(N, K, group_size, 0))
     return 0;
-  return awq::combine_workspace_bytes(T, top_k, E, N, K);
+  return awq::combine_workspace_bytes(T, top_k, E, N, K, group_size);
 }
 
 int awq_combine_experts(const void* x, int32_t ldx, const int32_t* offsets, const int32_t* positions,

@@ -72,12 +72,12 @@ hipError_t launch_combine_gemv(const PackedArgs& w, const ProductArgs& p, const 
 // A few rows (awq_fused_few.hip): tiles of at most 4 or 8 rows; N * K < 2^32.
 hipError_t launch_few(const PackedArgs& w, const ProductArgs& p, int gshift, int rows, float* part, hipStream_t stream);
 
-size_t product_workspace_bytes(int R, int E, int N, int K, bool gated);
+size_t product_workspace_bytes(int R, int E, int N, int K, int group_size);
 hipError_t launch_product(const PackedArgs& w, const ProductArgs& p, void* workspace, hipStream_t stream);
 
 // `p` describes the product (x already sorted by expert, no gather, gate or
 // residual); its y is not used.
-size_t combine_workspace_bytes(int T, int top_k, int E, int N, int K);
+size_t combine_workspace_bytes(int T, int top_k, int E, int N, int K, int group_size);
 hipError_t launch_combine(const PackedArgs& w, const ProductArgs& p, const CombineArgs& c, void* workspace,
                           hipStream_t stream);
 

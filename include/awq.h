@@ -313,10 +313,9 @@ size_t awq_clip_search_workspace_bytes(int32_t count, int32_t M, int32_t N, int3
  * ("AI-Research-SKILLs AWQ 高级使用指南", section 层融合: gate and up fused; the
  * MLP's activation, the bias and the residual stream are what a decoder
  * block puts around the layer.)  Sums, bias, activation, product and residual
- * are fp32; the output is rounded once to fp16.  Up to 8 tokens, and up to 256
- * with groups of 64 and more (N K < 2^32), no weight is rounded (exact q - z, the
- * group scale on their fp32 sums); 9 to 256 tokens with groups of 32, and all
- * larger products, take fp16((q - z) s), one rounding per weight, as awq_gemm's.
+ * are fp32; the output is rounded once to fp16.  No weight is rounded, whatever
+ * the batch: the matrix cores multiply the exact q - z, and the group's scale
+ * multiplies their fp32 sum (awq_gemm's larger batches round (q - z) s to fp16).
  * A row that holds infinities or NaN gives NaN or infinities in its own outputs
  * only.  Deterministic: the same bits again for the same call.
  * x         in   fp16, row m at x + m * ldx; bias fp16 [N] or NULL.
@@ -383,9 +382,8 @@ size_t awq_route_experts_workspace_bytes(int32_t T, int32_t E);
  * y        out  fp16, row r at y + r * ldy, offsets[0] <= r < offsets[E]; the rows
  *               before and past them are left as they are.
  * R rows at most (R = T * top_k after a router), 1 <= R <= 2^24, E <= 1024; with
- * `rows`, x_rows * ldx < 2^30.  Weights are exact as above while R is at most
- * 2 rows per expert, or 64 with groups of 64 and more, and rounded past that; the rest
- * as in awq_linear_fused; workspace likewise, awq_linear_experts_workspace_bytes().
+ * `rows`, x_rows * ldx < 2^30.  The rest as in awq_linear_fused; workspace
+ * likewise, awq_linear_experts_workspace_bytes().
  */
 int awq_linear_experts(const void* x, int32_t ldx, int32_t x_rows, const int32_t* rows, int32_t slots_per_row,
                        const int32_t* offsets, int32_t R, int32_t E, const uint32_t* qweight, const void* scales,
