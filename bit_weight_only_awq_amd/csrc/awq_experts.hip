@@ -16,8 +16,8 @@ namespace {
 int log2_group(int g) { return g == 32 ? 5 : g == 64 ? 6 : g == 128 ? 7 : 8; }
 
 // The two kernels below: a single wave per workgroup, four columns of one row
-// per thread, so that a few rows spread over the chip and no thread divides (of
-// 12.2 us for 61 x 4096 -> 4096, K in 2, 2.4 are this launch).  Past kFinishRows
+// per thread, so that a few rows spread over the chip and no thread divides (13 x
+// 11008 -> 4096, K in 4: about 3 of 16.2 us are this launch).  Past kFinishRows
 // rows a workgroup takes every kFinishRows-th.
 constexpr int kFinish = 64, kFinishRows = 32768;
 
@@ -84,8 +84,8 @@ __global__ __launch_bounds__(kFinish) void combine_kernel(const float* __restric
   }
 }
 
-// How a product runs, by the rows per expert (on average: the host does not
-// know the counts): a few, the weight stream, or the matrix cores.
+// How a product runs: one row or a few at a time, the weight stream, or the
+// matrix-core tiles.
 struct Plan {
   enum Kind { kFew, kStream, kTiles } kind;
   int few_rows;
@@ -95,95 +95,118 @@ struct Plan {
 };
 
 // One row per workgroup set: a single token, or so few rows that experts with
-// two are rare (their weights are then read twice, the second time from L2).
+// two are rare (their weights are then read twice, the second time from L2).  us,
+// one row at a time / tiles of 4 rows, at R = E / 2: 2 tokens x 2 of 8, 4096 ->
+// 22016 gated: 34 / 40; 2 x 4 of 16, 4096 -> 8192: 27 / 30; 8 x 8 of 128, 2048 ->
+// 1536 gated: 22 / 24.  At R = E: 4 x 2 of 8: 60.5 / 58.9; 4 x 4 of 16: 45.1 / 43.6.
 bool one_row_each(int R, int E) { return R == 1 || 2 * R <= E; }
 
-// Tile height and K split of the matrix-core tiles, from a time model: each of 256
-// compute units takes its share of the tiles (256 weight rows each, gated or not),
-// two at a time.  A 64-channel step of one tile takes 0.55 us + 0.115 per 32 rows
-// (128 rows: 1.01, 64: 0.78), of two tiles at once 0.7 + 0.25 (1.7, 1.2), 1.3 times
-// that in groups of 32; 5 us begin and end a tile; partial sums are written and read at 5.5 TB/s and
-// cost a launch (5 us).  us of the choice / of others, groups of 128:
-//   512 x 4096 -> 11008: 128 rows: 69.7 / in 2: 77.5; 64 rows: 78.6
-//   700 x 4096 -> 11008: 64 rows: 87.5 / 128 rows: 105.5 (258 tiles: two units have two)
-//   512 x 11008 -> 4096: 128 rows in 4: 65.8 / in 3: 71.8, unsplit: 167; 64 rows: 131
-//   1024 x 11008 -> 4096: 128 rows in 2: 109.1 / unsplit: 167, in 4: 113.1
-//   1000 tokens x 2 of 8, 11008 -> 4096 combined: in 3: 251 / unsplit: 320, in 2: 257
-//   2000 tokens x 6 of 64, 2048 -> 2816 gated: 196 / in 2: 291; 64 rows: 232
-// (20 shapes: at most 4% above the best of seven plans.)  `summed`: the
-// products are partial sums in any case (combining).
-TilePlan plan_tiles(int R, int experts, int N, int K, int group_size, bool summed) {
-  const int steps = (K + 63) / 64, columns = (N + 255) / 256;
-  constexpr double kUnits = 256;
+// Tiles of a few rows: up to 8 tokens of one layer, up to 3 rows for every two
+// experts.  us, few rows / the best of the weight stream: 8 x 4096 -> 4096: 6.2 /
+// 9.1; 8 x 11008 -> 4096: 12.8 / 14.5; 8 x 4096 -> 11008: 12.1 / 10.9 (they hold 8
+// rows at most: 9 take two).  Experts at R = E: 16 x 8 of 128, 768 -> 2048
+// combined: 27.7 / 30.2; 4 x 4 of 16, 4096 -> 8192: 43.6 / 45.6; at 1.5 E: 16 x 6 of 64, 2048 -> 2816
+// gated: 36.1 / 36.4; at 2 E: 8 x 2 of 8, 11008 -> 4096 combined: 58.2 / 44.1;
+// 32 x 8 of 128, 2048 -> 1536 gated: 49.4 / 44.6.
+bool few_rows_each(int R, int E) { return E == 0 ? R <= 8 : 2 * R <= 3 * E; }
+
+// Past that a time model chooses among five weight-stream variants and two tile
+// heights, each with K whole or split across workgroups.  Each of 256 compute
+// units takes its share of the workgroups, one at a time or two at once where two
+// fit its LDS; a workgroup takes `begin` us and `one` (two at once: `two`) for each
+// of its stages or steps; partial sums cost a launch (4 us) and are written and
+// read at 5.5 TB/s.  The constants are fitted to 1687 measured plans of 177 shapes
+// in groups of 128 (1-256 rows of nine layers, N and K from 768 to 28672; 2-256
+// tokens through 2 of 8, 4 of 16, 6 of 64 and 8 of 128 experts, combined and not;
+// 300-2048 rows on tiles): half the plans are within 7%.  The choices are on
+// average 1% above the best plan measured, over those and 75 shapes that are not
+// among them (300-2048 rows); worst: 500 tokens x 6 of 64, 1408 -> 2048 combined, 83 / 62.
+// Two sides (us, the choice / another):
+//   16 x 4096 -> 4096: 16 rows, 2 x 2 waves, K in 4: 9.6-9.8 / whole: 11.0; 2 x 4 waves: 9.2
+//   13 x 11008 -> 4096: 16 rows, 2 x 4 waves, K in 4: 16.2 / 2 x 4, whole: 23
+//   64 x 4096 -> 4096: 16 rows, 2 x 4 waves: 9.8 / 32 rows, 4 x 2, K in 4: 12.7
+//   48 tokens x 6 of 64, 2048 -> 2816 gated: 32 rows, 4 x 1: 46.6 / 16 rows, 2 x 2: 54
+//   61 x 4096 -> 11008: 32 rows, 4 x 2: 18 / 4 x 1: 20.9; 64 rows, K in 2: 22.7
+//   64 x 8192 -> 28672: 64 rows, 4 x 1: 56.6 / 32 rows, 4 x 1: 58.5, 4 x 2: 62.9
+//   100 x 8192 -> 28672: 64 rows, 4 x 1: 85-87 / 32 rows, 4 x 1: 104
+//   200 x 8192 -> 28672: tiles of 128 rows: 128 / stream, 64 rows: 160
+//   512 x 4096 -> 11008: tiles of 128 rows: 70 / in 2: 77; 64 rows: 78; stream: 69
+//   700 x 4096 -> 11008: tiles of 64 rows: 81-89 / 128 rows: 101-106
+//   512 x 11008 -> 4096: tiles of 128 rows in 4: 63 / whole: 167; 64 rows, whole: 131
+//   1000 tokens x 2 of 8, 11008 -> 4096 combined: tiles, K in 3: 241 / whole: 307-320
+struct StreamKind {
+  int rows, cw, kw;
+  bool pairs;  // two workgroups fit a compute unit
+  double one, two, begin;
+};
+constexpr StreamKind kStreamKinds[] = {{16, 2, 2, true, 1.0, 1.6, 2.7},
+                                       {16, 2, 4, false, 1.7, 0.0, 2.7},
+                                       {32, 4, 1, true, 1.0, 1.6, 2.6},
+                                       {32, 4, 2, false, 1.6, 0.0, 2.9},
+                                       {64, 4, 1, true, 0.74, 1.2, 3.1}};
+
+// The most loaded unit's time with `count` workgroups of `steps` steps.
+double unit_us(double count, int steps, bool pairs, double one, double two, double begin) {
+  const int each = (int)ceil(count / 256.0);
+  if (!pairs) return each * (steps * one + begin);
+  return (each / 2) * (steps * two + begin) + (each % 2) * (steps * one + begin);
+}
+
+// `summed`: the products are partial sums in any case (combining).
+Plan plan_by_time(int R, int experts, int N, int K, int group_size, bool summed) {
+  const double each = (double)R / experts;
+  // groups of 32 apply a scale every two matrix instructions
   const double slow = group_size == 32 ? 1.3 : 1.0;
-  TilePlan best{64, 1, steps};
+  // ragged experts end in half a tile each on average
+  auto row_tiles_of = [&](int rows) {
+    const double n = each / rows + 0.5;
+    return experts == 1 ? (double)((R + rows - 1) / rows) : experts * (n < 1 ? 1 : n);
+  };
+  auto sums_us = [&](int splits) { return splits > 1 || summed ? 4.0 + splits * (double)R * N * 8 / 5.5e6 : 0.0; };
+  Plan best{Plan::kTiles, 0, {}, TilePlan{64, 1, (K + 63) / 64}};
   double best_us = 1e300;
+  // (the stream addresses an expert's packed words with 31 bits)
+  if ((int64_t)N * K < ((int64_t)1 << 32)) {
+    for (const StreamKind& v : kStreamKinds) {
+      const int channels = (v.rows <= 32 ? 256 : 128) * v.kw, stages = (K + channels - 1) / channels;
+      const int columns = (N + 32 * v.cw - 1) / (32 * v.cw);
+      const double tiles = row_tiles_of(v.rows) * columns;
+      // (a launch holds less than 2^32 threads; with half of that most tiles there can be)
+      if ((double)((R + v.rows - 1) / v.rows + experts) * columns * (64 * v.cw * v.kw) >= 2147483648.0) continue;
+      for (int s = 1; s <= 8 && s <= stages; ++s) {
+        const int per = (stages + s - 1) / s, splits = (stages + per - 1) / per;
+        // no empty slice, and none of a single stage: its loads would run beside nothing
+        if (splits != s || (s > 1 && per < 2)) continue;
+        const double us =
+            unit_us(tiles * splits, per, v.pairs, slow * v.one, slow * v.two, v.begin) + sums_us(splits);
+        if (us < best_us) best_us = us, best = Plan{Plan::kStream, 0, StreamPlan{v.rows, v.cw, v.kw, splits}, {}};
+      }
+    }
+  }
+  const int steps = (K + 63) / 64, columns = (N + 255) / 256;
   for (int rows : {group_size == 32 ? 96 : 128, 64}) {
-    // ragged experts end in half a tile each on average
-    const double tiles = experts == 1 ? (R + rows - 1) / rows : experts * ((double)R / experts / rows + 0.5);
-    const double mean = R / tiles / 32, height = experts == 1 ? ceil(mean) : mean < 1 ? 1 : mean;
-    const double one = slow * (0.55 + 0.115 * height), two = slow * (0.7 + 0.25 * height);
+    if (each <= 32 && best.kind == Plan::kStream) break;  // a tile has 64 rows at least to multiply
+    const double tiles = row_tiles_of(rows), mean = R / tiles / 32;
+    const double height = mean < 2 ? 2 : experts == 1 ? ceil(mean) : mean;
+    const double one = slow * (0.51 + 0.107 * height), two = slow * (0.73 + 0.245 * height);
     for (int s = 1; s <= 16 && s <= steps; ++s) {
       // (slices of an even number of steps: no group of 128 channels is cut)
       const int per = s == 1 ? steps : ((steps + s - 1) / s + 1) & ~1, splits = (steps + per - 1) / per;
-      const int64_t each = (int64_t)ceil(tiles * columns * splits / kUnits);
-      const double us = (each / 2) * (per * two + 5.0) + (each % 2) * (per * one + 5.0) +
-                        (splits > 1 || summed ? splits * (double)R * N * 8 / 5.5e6 + 5.0 : 0.0);
-      if (us < best_us) best_us = us, best = TilePlan{rows, splits, per};
+      if (splits != s) continue;
+      const double us = unit_us(tiles * columns * splits, per, true, one, two, 5.5) + sums_us(splits);
+      if (us < best_us) best_us = us, best = Plan{Plan::kTiles, 0, {}, TilePlan{rows, splits, per}};
     }
   }
   return best;
 }
 
-// Weight-stream tiles, by how many there are.  Many (c: 128-row columns times
-// row tiles): 4 waves side by side.  Fewer: the waves of a workgroup split K, and
-// then the workgroups do, until about 256 of them run.  us on the 7B shapes,
-// the variant chosen / the one on the other side of the rule:
-//   13 x 11008 -> 4096: 2 x 2 waves, K in 4: 14.9 / 2 x 4 waves, no split: 23.0
-//   16 x 4096 -> 4096: 2 x 4: 9.1 / 4 x 1: 16.8;  16 x 4096 -> 11008: 11.6 / 17.9
-//   16 x 4096 -> 32768: 2 x 2: 21.7 / 4 x 1 with 32 rows: 22.9 (with 16 rows: 22.3)
-//   16 tokens x 2 of 8, 11008 -> 4096: 2 x 2: 47.2 / 4 x 1 with 32 rows: 54.4
-//   48 tokens x 6 of 64, 2048 -> 2816: 4 x 1 with 32 rows: 46.1 / 2 x 2: 54.0
-// (4 x 1 waves take tiles of 32 rows however few there are: an expert with 17 is
-// then read once, and 96 tokens x 6 of 64 take 51.6 us against 57.0 with 16.)
-//   61 x 4096 -> 11008 (32-row tiles): 4 x 2: 17.9 / 4 x 1: 20.8; 64 rows: 22.2
-//   100 x 4096 -> 4096: 4 x 2, K in 2: 14.0 / 4 x 1: 27
-//   200 x 4096 -> 11008: 4 x 1: 42.5 / 4 x 2: 46.5
-StreamPlan plan_stream(int R, int experts, int N, int K) {
-  const double each = (double)R / experts;
-  auto plan = [&](int rows, int cw, int kw, int splits) {
-    // no empty slice: every slice but the last has the same number of stages
-    const int channels = (rows <= 32 ? 256 : 128) * kw, stages = (K + channels - 1) / channels;
-    if (splits > stages / 2) splits = stages / 2;
-    if (splits < 1) splits = 1;
-    const int per = (stages + splits - 1) / splits;
-    return StreamPlan{rows, cw, kw, (stages + per - 1) / per};
-  };
-  const int c64 = experts * ((N + 63) / 64);
-  if (each <= (experts == 1 ? 16 : 10) || (experts == 1 && R <= 32 && K <= 6144 && 2 * c64 <= 160)) {
-    const int c = each <= 16 ? c64 : 2 * c64;
-    if (c >= 768) return plan(32, 4, 1, 1);
-    if (c >= 224) return plan(16, 2, 2, 1);
-    if (c >= 96 || K <= 6144) return plan(16, 2, 4, 1);
-    return plan(16, 2, 2, c >= 64 ? 4 : 8);
-  }
-  if (experts > 1 && each > 40) return plan(64, 4, 1, 1);
-  const double tiles = experts == 1 ? (R + 31) / 32 : experts * (each / 32 + 0.5);
-  const double c = tiles * ((N + 127) / 128);
-  if (c >= 320) return plan(32, 4, 1, 1);
-  if (c >= 160) return plan(32, 4, 2, 1);
-  return plan(32, 4, 2, c > 128 ? 1 : c > 80 ? 2 : c > 40 ? 4 : 8);
-}
-
+// E = 0: one expert, R rows known to the host.  Experts' counts live on the
+// device: the plan is for their average.
 Plan plan_product(int R, int E, int N, int K, int group_size, bool summed) {
-  const int experts = E == 0 ? 1 : E < R ? E : R;  // E = 0: one expert, R rows known to the host
-  const double each = (double)R / experts;
-  // (the first two kernels address an expert's packed words with 31 bits)
-  if ((int64_t)N * K < ((int64_t)1 << 32)) {
-    if (each <= (E == 0 ? 8 : 2)) return Plan{Plan::kFew, E == 0 && R > 4 ? 8 : 4, {}, {}};
-    if (each <= (E == 0 ? 256 : 64)) return Plan{Plan::kStream, 0, plan_stream(R, experts, N, K), {}};
-  }
-  return Plan{Plan::kTiles, 0, {}, plan_tiles(R, experts, N, K, group_size, summed)};
+  // (an expert's packed words are addressed with 31 bits there, too)
+  if (few_rows_each(R, E) && (int64_t)N * K < ((int64_t)1 << 32))
+    return Plan{Plan::kFew, E == 0 && R > 4 ? 8 : 4, {}, {}};
+  return plan_by_time(R, E == 0 ? 1 : E < R ? E : R, N, K, group_size, summed);
 }
 
 size_t part_bytes(const Plan& plan, int R, int N) {

@@ -33,7 +33,7 @@ def test_linear_fused(lib, M, N, K, gated):
             lib.awq_linear_fused_workspace_bytes(M, N, K, 128, gated))
 
 
-@pytest.mark.parametrize("T,k,E,N,K", [(20, 2, 6, 144, 7168), (100, 2, 6, 144, 2048)])
+@pytest.mark.parametrize("T,k,E,N,K", [(20, 2, 6, 144, 7168), (100, 2, 6, 144, 11008)])
 def test_linear_experts(lib, T, k, E, N, K):
     for gated in (0, 1):
         refuses(lambda ws, n: lib.awq_linear_experts(X, K, T, ROWS, k, OFF, T * k, E, Q, S, Z, None, 0, gated, Y, N, N, K,

@@ -29,20 +29,27 @@ def relative(K, g):
                                    (257, 512, 32), (300, 544, 32), (300, 11008, 32), (300, 512, 64), (290, 4096, 64),
                                    (600, 320, 64), (300, 1024, 128), (400, 11008, 128), (300, 1024, 256)])
 @pytest.mark.parametrize("zp", [True, False])
-def test_fused_layer(M, K, g, zp):
+def test_fused_layer(M, K, g, zp, N=264):
     awq = G.lib()
-    N = 264
     pw, wdq = H.packed_layer(awq, N, K, g, zp, M)
     X = one_hot(M, K, 2)
     ref = X.astype(np.float64) @ wdq.T
     rounded_once(G.host_f16(awq.linear_fused(G.dev_f16(X), pw)), ref, relative(K, g), f"M={M} K={K} g={g} zp={zp}")
 
 
+# matrix-core tiles, one round of them and several; K split in (700, 4104)
+@pytest.mark.parametrize("M,N,K,g", [(1100, 4104, 544, 32), (700, 8200, 512, 64), (700, 8200, 1024, 128),
+                                     (700, 8200, 1024, 256), (700, 4104, 11008, 128)])
+@pytest.mark.parametrize("zp", [True, False])
+def test_fused_layer_on_tiles(M, N, K, g, zp):
+    test_fused_layer(M, K, g, zp, N)
+
+
 @pytest.mark.parametrize("E,T,K,g", [(8, 20, 512, 32), (8, 100, 544, 32), (8, 250, 512, 32), (8, 400, 544, 32),
                                      (8, 400, 512, 64), (4, 400, 4096, 128), (70, 2500, 256, 64), (70, 2500, 288, 32)])
-def test_expert_layers(E, T, K, g):
+def test_expert_layers(E, T, K, g, N=136):
     awq = G.lib()
-    N, k = 136, 2
+    k = 2
     ids, weights, offsets, rows, positions = F.route(logits_of(T, E, 51), k, True)
     route = device_route(awq, (ids, weights, offsets, rows, positions))
     pe, wdq = H.packed_experts(awq, E, N, K, g, True, T)
@@ -65,14 +72,20 @@ def test_expert_layers(E, T, K, g):
     assert np.max(np.abs(y - ref) / bound) <= 1.0, f"combined E={E} T={T} K={K} g={g}"
 
 
+@pytest.mark.parametrize("E,T,N,K,g", [(8, 1500, 4104, 288, 32), (8, 1500, 4104, 320, 64), (70, 2500, 520, 288, 32),
+                                       (8, 1000, 2056, 4096, 128)])
+def test_expert_layers_on_tiles(E, T, N, K, g):
+    test_expert_layers(E, T, K, g, N)
+
+
 @pytest.mark.parametrize("M", [1, 5, 13, 40, 100, 300])
 @pytest.mark.parametrize("K,g", [(544, 32), (512, 64), (1024, 128), (1024, 256)])
 @pytest.mark.parametrize("zp", [True, False])
-def test_scales_of_every_size(M, K, g, zp):
+def test_scales_of_every_size(M, K, g, zp, N=136):
     """Groups whose scale is 0 (the first, the last, runs of them, whole rows), the smallest fp16 number, or 10^5 times
     it, next to each other, and negative ones."""
     awq = G.lib()
-    N, Gr = 136, K // g
+    Gr = K // g
     rng = np.random.default_rng([29, K, g, zp])
     qw, _, qz = O.pack(workloads.weight(N, K, cfg=11, layer=3), g, zp)
     s = rng.choice(np.array([0.0, 0.0, 2.0 ** -24, 3e-6, 1e-4, 0.02, -0.01]), (N, Gr))
@@ -87,3 +100,9 @@ def test_scales_of_every_size(M, K, g, zp):
     ref, bound = F.linear_fused(X, wdq)
     assert np.all(y[:, 2::8] == 0)
     H.check(y, ref, bound, f"M={M} K={K} g={g} zp={zp}")
+
+
+@pytest.mark.parametrize("M,N,K,g", [(1100, 4104, 544, 32), (700, 8200, 512, 64), (700, 8200, 1024, 128),
+                                     (700, 8200, 1024, 256)])
+def test_scales_of_every_size_on_tiles(M, N, K, g):
+    test_scales_of_every_size(M, K, g, g != 128, N)

@@ -25,7 +25,8 @@ def stale(nbytes):
 
 # one row for each expert or fewer, 4-row tiles, 16- and 32-row tiles (K split and not), matrix-core tiles
 @pytest.mark.parametrize("T,N,K", [(1, 144, 256), (3, 144, 256), (5, 144, 256), (9, 144, 256), (20, 144, 7168),
-                                   (60, 144, 256), (100, 144, 2048), (170, 144, 256), (500, 144, 256)])
+                                   (60, 144, 256), (100, 144, 11008), (170, 144, 256), (500, 144, 256),
+                                   (1000, 2064, 2048)])
 def test_only_the_slice_is_computed(T, N, K):
     awq = G.lib()
     k = 1 if T == 3 else 2

@@ -27,9 +27,9 @@ def test_a_residual_copied_for_its_layout_lives_through_the_call(monkeypatch):
     """A residual of three dimensions with swapped strides is copied first: the copy is held until the kernels that read
     it are enqueued, so that no memory of the same call (partial sums) takes its place."""
     awq = G.lib()
-    M, N, K = 300, 2048, 2048
+    M, N, K = 300, 4096, 11008
     gen = torch.Generator(device="cuda").manual_seed(5)
-    pw = awq.pack((torch.randn((N, K), generator=gen, device="cuda") / 45).half())
+    pw = awq.pack((torch.randn((N, K), generator=gen, device="cuda") / 100).half())
     lib = awq.load_library()
     need = lib.awq_linear_fused_workspace_bytes(M, N, K, 128, 0)
     assert need > 0

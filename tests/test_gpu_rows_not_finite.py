@@ -30,9 +30,9 @@ def check(y, ref, bound, rows, what):
 
 @pytest.mark.parametrize("M,K,g", [(3, 288, 32), (8, 256, 64), (13, 11008, 128), (30, 288, 32), (100, 320, 64),
                                    (300, 288, 32), (600, 320, 64)])
-def test_fused_layer(M, K, g):
+def test_fused_layer(M, K, g, N=136):
     awq = G.lib()
-    pw, wdq = H.packed_layer(awq, 136, K, g, True, 6)
+    pw, wdq = H.packed_layer(awq, N, K, g, True, 6)
     X = workloads.activations(M, K, cfg=11, layer=6)
     rows = np.unique([1, M // 2, M - 1])
     y = G.host_f16(awq.linear_fused(G.dev_f16(spoiled(X, rows)), pw))
@@ -41,9 +41,9 @@ def test_fused_layer(M, K, g):
 
 @pytest.mark.parametrize("T,K,g", [(2, 256, 64), (7, 288, 32), (20, 288, 32), (20, 7168, 128), (100, 320, 64),
                                    (400, 288, 32), (700, 320, 64)])
-def test_expert_layers(T, K, g):
+def test_expert_layers(T, K, g, N=136):
     awq = G.lib()
-    E, N, k = 8, 136, 2
+    E, k = 8, 2
     ids, weights, offsets, rows, positions = F.route(logits_of(T, E, 61), k, True)
     route = device_route(awq, (ids, weights, offsets, rows, positions))
     pe, wdq = H.packed_experts(awq, E, N, K, g, True, 7)
@@ -55,3 +55,13 @@ def test_expert_layers(T, K, g):
     y = G.host_f16(awq.combine_experts(G.dev_f16(spoiled(h, slots)), pe, route))
     hit = np.flatnonzero(np.isin(positions, slots).any(1))
     check(y, *F.combine_experts(h, wdq, offsets, positions, weights.astype(np.float32)), hit, f"combined T={T}")
+
+
+@pytest.mark.parametrize("M,N,K,g", [(700, 8200, 320, 64), (1100, 4104, 288, 32)])
+def test_fused_layer_on_tiles(M, N, K, g):
+    test_fused_layer(M, K, g, N)
+
+
+@pytest.mark.parametrize("T,N,K,g", [(1500, 4104, 320, 64), (1500, 4104, 288, 32)])
+def test_expert_layers_on_tiles(T, N, K, g):
+    test_expert_layers(T, K, g, N)
