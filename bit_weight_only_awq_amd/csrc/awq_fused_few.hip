@@ -1,4 +1,4 @@
-// A few rows: the fused layer for 2-8 tokens, and expert rows in tiles of 4 or 8.
+// A few rows: the fused layer for 2-8 tokens, and expert rows in tiles of 4.
 //
 // Mathematics: awq_experts.hip's, with the exact integers q - z on the matrix
 // cores and the group's scale on each 32-channel fp32 sum, so no weight is
@@ -15,7 +15,7 @@
 // waves in LDS, in a fixed order; the last few threads apply the epilogue.
 //
 // Measured (us): 4 / 8 x 4096 -> 4096: 5.4 / 6.2; -> 11008: 9.6 / 12.2; -> 22016
-// gated: 16.0 / 20.9 (2.9 / 2.3 TB/s); 8 tokens x 2 of 8 -> 22016 gated: 78 (4.3 TB/s).
+// gated: 16.0 / 20.9 (2.9 / 2.3 TB/s); 4 tokens x 2 of 8 -> 22016 gated: 59 (4.3 TB/s).
 #include "awq_epilogue.hpp"
 #include "awq_launch_fused.hpp"
 
@@ -203,10 +203,11 @@ hipError_t launch_few_as(const PackedArgs& w, const ProductArgs& p, int gs, int 
   const int width = p.gated ? w.N / 2 : w.N, outs = p.gated ? 8 : kRows;
   const int groups = (width + outs - 1) / outs;
   const int slots = p.offsets ? row_tiles(p.R, w.E, TS * 4) : 1;
-  const auto kernel = p.offsets ? (rounds == 1 ? few_kernel<TS, S, MAXW, ZP, false, true>
-                                               : few_kernel<TS, S, MAXW, ZP, true, true>)
-                                : (rounds == 1 ? few_kernel<TS, S, MAXW, ZP, false, false>
-                                               : few_kernel<TS, S, MAXW, ZP, true, false>);
+  auto kernel = rounds == 1 ? few_kernel<TS, S, MAXW, ZP, false, false> : few_kernel<TS, S, MAXW, ZP, true, false>;
+  if constexpr (TS == 1) {
+    if (p.offsets)
+      kernel = rounds == 1 ? few_kernel<TS, S, MAXW, ZP, false, true> : few_kernel<TS, S, MAXW, ZP, true, true>;
+  }
   hipLaunchKernelGGL(kernel, dim3((unsigned)(groups * slots)), dim3(nw * 64), 0, stream, w.qweight, w.scales, w.qzeros, p.x,
                      w.N, w.K, (int)p.ldx, p.R, gs, (int)p.gated, groups, rounds, w.E, p, part);
   return hipGetLastError();
@@ -231,7 +232,8 @@ hipError_t launch_few_zp(const PackedArgs& w, const ProductArgs& p, int gs, int 
 }  // namespace
 
 hipError_t launch_few(const PackedArgs& w, const ProductArgs& p, int gshift, int rows, float* part, hipStream_t stream) {
-  if (!p.offsets && p.R > rows) return hipErrorInvalidValue;  // one tile holds all rows
+  // one tile holds all rows of a layer; experts' tiles have 4
+  if (p.offsets ? rows != 4 : p.R > rows) return hipErrorInvalidValue;
   return w.qzeros ? launch_few_zp<true>(w, p, gshift, rows, part, stream)
                   : launch_few_zp<false>(w, p, gshift, rows, part, stream);
 }

@@ -69,7 +69,7 @@ hipError_t launch_fused_gemv(const PackedArgs& w, const ProductArgs& p, int gshi
 hipError_t launch_combine_gemv(const PackedArgs& w, const ProductArgs& p, const CombineArgs& c, int gshift,
                                hipStream_t stream);
 
-// A few rows (awq_fused_few.hip): tiles of at most 4 or 8 rows; N * K < 2^32.
+// A few rows (awq_fused_few.hip): tiles of at most 4 rows, or 8 (one layer); N * K < 2^32.
 hipError_t launch_few(const PackedArgs& w, const ProductArgs& p, int gshift, int rows, float* part, hipStream_t stream);
 
 size_t product_workspace_bytes(int R, int E, int N, int K, int group_size);

@@ -400,7 +400,7 @@ size_t awq_linear_experts_workspace_bytes(int32_t R, int32_t E, int32_t N, int32
  * the expert whose range of offsets holds the row.  Slots whose position is
  * negative or in no expert's range (a slice of the experts, as above) add
  * nothing (a token without any: y = residual, or 0).  The sum
- * runs over j in order, in fp32, on unrounded products; one rounding to fp16.
+ * is taken in fp32, in a fixed order, on unrounded products; one rounding to fp16.
  * positions, weights  in  int32, fp32 [T][top_k], top_k <= min(E, 64); the other arguments as above.
  * workspace: awq_combine_experts_workspace_bytes() bytes (the fp32 products of
  * all T * top_k rows, past a few rows), as awq_linear_fused's.
