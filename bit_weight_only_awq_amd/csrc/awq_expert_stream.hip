@@ -1,6 +1,6 @@
-// Weight-stream bound products (up to 256 rows, or 64 per expert): tiles of
-// up to XR rows x 32 CW weight rows, with every operand flowing through a ring
-// of LDS stages.
+// Weight-stream bound products (from a few rows, or two per expert, to where the
+// matrix-core tiles take less time): tiles of up to XR rows x 32 CW weight rows,
+// with every operand flowing through a ring of LDS stages.
 //
 // Mathematics: awq_experts.hip's.  The matrix cores multiply the exact integers
 // q - z, and the group's scale multiplies the fp32 sum once per group and output
@@ -23,10 +23,10 @@
 // workgroup per compute unit a stage's decoding and products take about as long
 // as its loads.
 //
-// Measured: 48 tokens x 6 of 64, 2048 -> 2816 gated: 46.2 us, 4.1 TB/s of the
-// packed weights (floor 37.0); 24 tokens 40.0 us, 4.4 TB/s; 16 x 4096 -> 4096:
-// 9.3 us; 13 x 11008 -> 4096: 15.0; 61 x 4096 -> 11008, groups of 64: 18.2 (5.0),
-// of 32: 22.3.
+// Measured: 48 tokens x 6 of 64, 2048 -> 2816 gated: 46.6 us, 4.1 TB/s of the
+// packed weights (floor 37.0), in groups of 64: 51.5; 64 x 4096 -> 4096: 9.8 us; 13
+// x 11008 -> 4096 with its second launch: 16.2; 61 x 4096 -> 11008, groups of 64:
+// 18.2 (5.0), of 32: 22.3.
 #include "awq_epilogue.hpp"
 #include "awq_launch_fused.hpp"
 

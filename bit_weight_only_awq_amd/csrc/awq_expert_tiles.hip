@@ -31,11 +31,12 @@
 // unrolled for it, so that a tile multiplies at most 31 rows (63 below 64) that
 // do not exist; with more tiles than run at once the tallest come first.
 //
-// Measured: 2048 x 8192 -> 57344 gated: 1663-1710 us, 1.13-1.16 PFLOP/s (the dense
+// Measured: 2048 x 8192 -> 57344 gated: 1651-1710 us, 1.13-1.17 PFLOP/s (the dense
 // library product of the same shape: 1408 us); 2048 x 4096 -> 22016 gated: 363 us,
-// in groups of 64: 397, of 32: 513; 1000 tokens x 2 of 8, 4096 -> 22016 gated: 430
-// us (264 at the library's rate): whole tiles on two places per unit; 11008 -> 4096
-// combined: 242 us with K in 3.  With weights rounded to fp16 (and 256-row
+// in groups of 64: 397, of 32: 513; 1000 tokens x 2 of 8, 4096 -> 22016 gated:
+// 402-433 us (264 at the library's rate): whole tiles on two places per unit; 11008
+// -> 4096 combined: 242 us with K in 3.  The matrix cores are busy 64%, 48% and 39%
+// of their cycles, LDS conflicts 0.3%.  With weights rounded to fp16 (and 256-row
 // tiles) they take 1589, 352 (any groups), 430 and 238: exact ones cost 3-5%, 13%
 // in groups of 64 and 46% of 32.
 #include "awq_epilogue.hpp"

@@ -16,9 +16,9 @@
 // expert's rows it reads and whose weight multiplies its sum, so the weighted
 // sum over experts is the same reduction and needs no second launch.
 //
-// Measured: 4096 -> 4096: 3.7 us, with residual 3.8; 4096 -> 22016 gated: 10.5 us,
-// 4.46 TB/s; one token x 2 of 8, the same layer: 20.4 us, 4.60 TB/s; combined
-// 11008 -> 4096: 14.0 us, 3.35 TB/s.  Bytes read: 1.00-1.01 of the packed weights.
+// Measured: 4096 -> 4096: 3.7 us, with residual 3.8; 4096 -> 22016 gated: 10.1-10.5
+// us, 4.5-4.6 TB/s; one token x 2 of 8, the same layer: 20.2-20.9 us, 4.5-4.6 TB/s;
+// combined 11008 -> 4096: 14.1 us, 3.3 TB/s.  Bytes read: 1.00-1.01 of the packed weights.
 #include "awq_epilogue.hpp"
 #include "awq_launch_fused.hpp"
 

@@ -8,10 +8,12 @@
 // in fp32.  A logit of -inf or NaN is never chosen: its slot has id -1,
 // weight 0 and position -1.  With m = +inf the +inf logits share the weight.
 //
-// Bound: latency for a few tokens (one launch, 3-6 us), the picks for many: per
-// token top_k dependent maxima.  LG lanes hold a token's logits, consecutive
-// ones per lane, so the lowest lane with the maximum also has the lowest index;
-// a maximum over the lanes is log2(LG) register exchanges (DPP).
+// Bound: latency for a few tokens (one launch, 3-6 us), the vector instructions of
+// the picks for many: 126 per pick of a wave with 8 logits per lane (the owning
+// lane searches its logits and takes their maximum again, and the others wait).  LG
+// lanes hold a token's logits, consecutive ones per lane, so the lowest lane with
+// the maximum also has the lowest index; a maximum over the lanes is log2(LG)
+// register exchanges (DPP).
 //
 // The sort is a counting sort without atomics on anything but bits and integer
 // sums: a token chooses an expert at most once, so the choices of a block's 64
@@ -22,7 +24,7 @@
 // sums the counts along the blocks, so that the work stays linear.
 //
 // Measured (us): 1 token of 8 experts, top 2: 2.6; 64 tokens: 2.9; 1024 of 64, top
-// 6: 10.3; 16384 of 128, top 8: 18.4 (choosing 11, placing 7), and 51.5 with 256
+// 6: 10.3; 16384 of 128, top 8: 18.3 (choosing 12, placing 7), and 51.5 with 256
 // tokens per block.
 #include "awq_epilogue.hpp"
 #include "awq_launch_fused.hpp"
