@@ -32,6 +32,7 @@ and ``mlp(x, gate_up, down, residual)``, a decoder block's MLP in two launches.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -535,16 +536,24 @@ def _activation(name: str) -> int:
 
 
 def _with_workspace(call, need, where: str, workspace: Optional[torch.Tensor], t: torch.Tensor) -> None:
-    """``call(address, bytes)`` with the caller's workspace, or else without one: the call says itself when it needs one,
-    and then gets ``need()`` bytes beside ``t`` for this call only.  (Its two launches hand partial sums on in them, so
-    calls of several host threads on one stream must not share them; and a buffer kept for the stream would grow
-    with the largest batch and stay.  Under graph capture the bytes come from the graph's own memory.)"""
-    st = call(_ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
-    if st == AWQ_ERR_WORKSPACE and workspace is None:
-        ws = t.new_empty(need(), dtype=torch.uint8)
-        st = call(ws.data_ptr(), ws.numel())
+    """``call(address, bytes)`` with the caller's workspace, or else with ``need()`` bytes beside ``t`` for this call
+    only.  (Its two launches hand partial sums on in them, so calls of several host threads on one stream must not
+    share them; and a buffer kept for the stream would grow with the largest batch and stay.  Under graph capture the
+    bytes come from the graph's own memory.)"""
+    if workspace is None:
+        nbytes = need()
+        ws = t.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+        st = call(None if ws is None else ws.data_ptr(), nbytes)
+    else:
+        st = call(_ptr(workspace), workspace.numel() * workspace.element_size())
     if st != AWQ_OK:
         raise AwqError(st, where)
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes_of(name: str, *shape) -> int:
+    """The library's workspace size of a shape: a function of its numbers alone, asked once."""
+    return int(getattr(_lib or load_library(), name + "_workspace_bytes")(*shape))
 
 
 def linear_fused(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor] = None, activation: str = "none",
@@ -583,7 +592,7 @@ def linear_fused(x: torch.Tensor, pw: PackedWeight, bias: Optional[torch.Tensor]
         _with_workspace(
             lambda ws, n: lib.awq_linear_fused(xp, ldx, qp, sp, zp, bp, act, gated, rp, ldr, yp, ldy, M, N, K,
                                                group_size, zero_point, ws, n, stream),
-            lambda: lib.awq_linear_fused_workspace_bytes(M, N, K, group_size, gated), "awq_linear_fused", workspace, x2)
+            lambda: _bytes_of("awq_linear_fused", M, N, K, group_size, gated), "awq_linear_fused", workspace, x2)
     return out if y is not None or x.dim() == 2 else out.reshape(*x.shape[:-1], width)
 
 
@@ -710,8 +719,7 @@ def linear_experts(x: torch.Tensor, pe: PackedExperts, route: ExpertRoute, bias:
         _with_workspace(
             lambda ws, n: lib.awq_linear_experts(xp, ldx, T, wp, top_k, op, R, E, qp, sp, zp, bp, act, gated, yp, ldy, N,
                                                  K, group_size, zero_point, ws, n, stream),
-            lambda: lib.awq_linear_experts_workspace_bytes(R, E, N, K, group_size, gated), "awq_linear_experts",
-            workspace, x)
+            lambda: _bytes_of("awq_linear_experts", R, E, N, K, group_size, gated), "awq_linear_experts", workspace, x)
     return out
 
 
@@ -719,7 +727,8 @@ def combine_experts(h: torch.Tensor, pe: PackedExperts, route: ExpertRoute, bias
                     residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The experts' second layer on the sorted rows ``h`` [T * top_k, K] and each token's weighted sum, plus
-    ``residual`` [T, N]: fp16 [T, N], one rounding.  With a slice of the route's offsets, the sum over the slice."""
+    ``residual`` [T, N]: fp16 [T, N], one rounding.  With a slice of the route's offsets, the sum over the slice
+    (of at least ``top_k`` experts)."""
     lib = _lib or load_library()
     qweight, scales, qzeros, E, N, K, group_size, zero_point = pe
     T, top_k = shape = route.ids.shape
@@ -741,8 +750,7 @@ def combine_experts(h: torch.Tensor, pe: PackedExperts, route: ExpertRoute, bias
         _with_workspace(
             lambda ws, n: lib.awq_combine_experts(hp, ldh, op, pp, wp, T, top_k, E, qp, sp, zp, bp, rp, ldr, yp, ldy, N,
                                                   K, group_size, zero_point, ws, n, stream),
-            lambda: lib.awq_combine_experts_workspace_bytes(T, top_k, E, N, K, group_size), "awq_combine_experts",
-            workspace, h)
+            lambda: _bytes_of("awq_combine_experts", T, top_k, E, N, K, group_size), "awq_combine_experts", workspace, h)
     return out
 
 
