@@ -78,3 +78,36 @@ def test_rounds_of_one_layer_tiles(K, g, gated):
     y = G.host_f16(awq.linear_fused(G.dev_f16(X), pw, G.dev_f16(b), "silu", gated, G.dev_f16(r)))
     H.check(y[:, cols], *F.linear_fused(X, decoded(pe, wr)[0], b[wr], "silu", gated, r[:, cols]),
             f"{M} x {K} -> {N} gated={gated}")
+
+
+@pytest.mark.parametrize("K,g", [(384, 128), (320, 64), (288, 32)])
+def test_same_bits_again_on_another_stream_and_in_a_graph(K, g):
+    """Several rounds of tiles of ragged experts, and their weighted sum."""
+    awq = G.lib()
+    E, T, N, k = 8, 1500, 8192, 2
+    pe = experts(awq, E, N, K, g, True)
+    route = awq.route_experts(torch.from_numpy(logits_of(T, E, 45)).cuda(), k)
+    x = G.dev_f16(workloads.activations(T, K, cfg=12, layer=45))
+    h = G.dev_f16(workloads.activations(T * k, K, cfg=12, layer=46))
+
+    def both():
+        return (awq.linear_experts(x, pe, route, activation="silu", gated=True), awq.combine_experts(h, pe, route))
+
+    first = both()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        there = both()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = both()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, there))
+    for _ in range(4):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(first, both()))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, out))
