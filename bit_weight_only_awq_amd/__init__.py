@@ -27,7 +27,14 @@ The layer with its epilogue and the layers of experts:
 * ``combine_experts(h, experts, route, bias, residual)``
 * ``expert_mlp(x, logits, gate_up, down, top_k)``: the four together
 
-and ``mlp(x, gate_up, down, residual)``, a decoder block's MLP in two launches.
+``mlp(x, gate_up, down, residual)``, a decoder block's MLP in two launches, and
+the block's other half on a paged cache of keys and values:
+
+* ``kv_cache(pages, kv_heads, head_dim, page_size)`` -> ``KvCache``, ``Sequences(offsets, lengths, tables)``
+* ``append_kv(qkv, cache, seqs, inv_freq)`` -> rotated queries
+* ``attend(q, cache, seqs, scale, shared)``
+* ``select_pages(q, cache, seqs, count)``, ``attend_pages(q, cache, seqs, pages)``
+* ``attention(x, qkv, o, cache, seqs, inv_freq)``: the layers and the calls above together
 """
 from __future__ import annotations
 
@@ -62,7 +69,9 @@ EXPORTED = ("awq_pack", "awq_dequant", "awq_gemv", "awq_gemm", "awq_gemm_workspa
             "awq_gemm_noalloc", "awq_gemm_noalloc_max_workspace_bytes",
             "awq_linear_fused", "awq_linear_fused_workspace_bytes", "awq_route_experts",
             "awq_route_experts_workspace_bytes", "awq_linear_experts", "awq_linear_experts_workspace_bytes",
-            "awq_combine_experts", "awq_combine_experts_workspace_bytes")
+            "awq_combine_experts", "awq_combine_experts_workspace_bytes",
+            "awq_append_kv", "awq_attend", "awq_attend_workspace_bytes", "awq_select_pages",
+            "awq_select_pages_workspace_bytes", "awq_attend_pages", "awq_attend_pages_workspace_bytes")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -135,6 +144,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.awq_combine_experts.restype = ctypes.c_int
     lib.awq_combine_experts_workspace_bytes.argtypes = [I32, I32, I32, I32, I32, I32]
     lib.awq_combine_experts_workspace_bytes.restype = SZ
+    F32 = ctypes.c_float
+    batch = [P, P, P, I32, I32, I32, I32, I32, I32]  # offsets, lengths, tables, width, T, B, q_heads, kv_heads, head_dim
+    lib.awq_append_kv.argtypes = [P, I32, *batch, P, I32, I32, P, I32, P, P, I32, P, P, P, I32, I32, P]
+    lib.awq_append_kv.restype = ctypes.c_int
+    lib.awq_attend.argtypes = [P, I32, *batch, F32, I32, P, P, I32, I32, P, I32, P, SZ, P]
+    lib.awq_attend.restype = ctypes.c_int
+    lib.awq_attend_workspace_bytes.argtypes = [I32] * 8
+    lib.awq_attend_workspace_bytes.restype = SZ
+    lib.awq_select_pages.argtypes = [P, I32, *batch, P, I32, I32, I32, I32, I32, P, P, SZ, P]
+    lib.awq_select_pages.restype = ctypes.c_int
+    lib.awq_select_pages_workspace_bytes.argtypes = [I32] * 4
+    lib.awq_select_pages_workspace_bytes.restype = SZ
+    lib.awq_attend_pages.argtypes = [P, I32, *batch, F32, P, I32, P, P, I32, I32, P, I32, P, SZ, P]
+    lib.awq_attend_pages.restype = ctypes.c_int
+    lib.awq_attend_pages_workspace_bytes.argtypes = [I32] * 6
+    lib.awq_attend_pages_workspace_bytes.restype = SZ
     _lib = lib
     return lib
 
@@ -762,3 +787,201 @@ def expert_mlp(x: torch.Tensor, logits: torch.Tensor, gate_up: PackedExperts, do
     route = route_experts(logits, top_k, renormalize)
     h = linear_experts(x, gate_up, route, activation=activation, gated=True)
     return combine_experts(h, down, route, residual=residual)
+
+
+class KvCache(NamedTuple):
+    k: torch.Tensor                 # fp16 [pages, kv_heads, page_size, head_dim]
+    v: torch.Tensor
+    bounds: Optional[torch.Tensor]  # fp16 [pages, kv_heads, 2, head_dim]: each page's least and greatest key
+
+
+class Sequences(NamedTuple):
+    offsets: torch.Tensor  # int32 [B + 1]: sequence b's new tokens are rows offsets[b] .. offsets[b + 1] - 1
+    lengths: torch.Tensor  # int32 [B]: its tokens, the new ones among them
+    tables: torch.Tensor   # int32 [B, width]: its pages
+
+
+def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 32, bounds: bool = True,
+             device="cuda") -> KvCache:
+    """An uninitialised cache; with ``bounds``, one that ``select_pages`` can choose from."""
+    shape = (pages, kv_heads, page_size, head_dim)
+    k, v = (torch.empty(shape, dtype=torch.float16, device=device) for _ in range(2))
+    return KvCache(k, v, torch.empty((pages, kv_heads, 2, head_dim), dtype=torch.float16, device=device) if bounds else None)
+
+
+def _cache_call(x: torch.Tensor, cache: KvCache, seqs: Sequences, extra: int, what: str):
+    """(row address, row stride, the batch's arguments, those of the pages) of rows ``x`` that hold ``extra`` vectors
+    per key head beside the queries' (keys and values); everything on one device, which is the current one for the
+    call."""
+    k, v, bounds = cache
+    offsets, lengths, tables = seqs
+    pages, kv_heads, page_size, dim = shape = k.shape
+    if k.dtype is not _F16 or v.dtype is not _F16 or v.shape != shape:
+        raise ValueError("the cache's keys and values must be float16 tensors [pages, kv_heads, page_size, head_dim]")
+    if x.dim() != 2 or x.shape[1] % dim:
+        raise ValueError(f"{what} must be a float16 tensor [T, heads * {dim}]")
+    heads = x.shape[1] // dim - extra * kv_heads
+    if heads < 1 or heads % kv_heads:
+        raise ValueError(f"{what} must hold a multiple of {kv_heads} query heads")
+    xp, ldx = _rows2d(x, None, x.shape[1], what)
+    B, device = lengths.shape[0], x.device
+    if tables.dim() != 2:
+        raise ValueError("seqs.tables must be an int32 tensor [B, width]")
+    if not (k.device == v.device == offsets.device == lengths.device == tables.device == device):
+        raise ValueError("the cache, the sequences and the rows must live on one GPU")
+    batch = (_flat(offsets, (B + 1,), _I32, "seqs.offsets"), _flat(lengths, (B,), _I32, "seqs.lengths"),
+             _flat(tables, (B, tables.shape[1]), _I32, "seqs.tables"), tables.shape[1], x.shape[0], B, heads, kv_heads,
+             dim)
+    return xp, ldx, batch, (_ptr(k), _ptr(v), pages, page_size)
+
+
+def _page_bounds(cache: KvCache) -> Optional[int]:
+    if cache.bounds is None:
+        return None
+    if cache.bounds.device != cache.k.device:
+        raise ValueError("the cache must live on one GPU")
+    pages, kv_heads, _, dim = cache.k.shape
+    return _flat(cache.bounds, (pages, kv_heads, 2, dim), _F16, "cache.bounds")
+
+
+def _beside(t: Optional[torch.Tensor], x: torch.Tensor, what: str) -> None:
+    if t is not None and t.device != x.device:
+        raise ValueError(f"{what} must live on the GPU of the rows")
+
+
+def _output(y: Optional[torch.Tensor], x: torch.Tensor, width: int, what: str):
+    if y is None:
+        out = x.new_empty((x.shape[0], width))
+        return out, out.data_ptr(), width
+    _beside(y, x, what)
+    return (y, *_rows2d(y, x.shape[0], width, what))
+
+
+def append_kv(qkv: torch.Tensor, cache: KvCache, seqs: Sequences, inv_freq: Optional[torch.Tensor] = None,
+              positions: Optional[torch.Tensor] = None, axes: Optional[torch.Tensor] = None, interleaved: bool = False,
+              q: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The new tokens' rows ``qkv`` [T, (q_heads + 2 kv_heads) * head_dim] of a fused q/k/v layer: keys (rotated) and
+    values into the cache's pages, the pages' bounds kept up to date if it has them; returns the rotated queries
+    [T, q_heads * head_dim].  ``inv_freq`` (fp32 [R / 2]): pair i of the first R channels turns by position *
+    inv_freq[i]; None: no rotation.  ``positions`` int32 [T] or [T, axes]: None takes each token's place in its
+    sequence.  With several axes ``axes`` (int32 [R / 2]) says which one pair i turns by.  Pairs are channels
+    (i, R / 2 + i), or (2 i, 2 i + 1) with ``interleaved``.  ``q`` may be the queries' columns of ``qkv``."""
+    lib = _lib or load_library()
+    xp, ldx, batch, (kp, vp, pages, page_size) = _cache_call(qkv, cache, seqs, 2, "qkv")
+    bp = _page_bounds(cache)
+    width = batch[6] * batch[8]
+    out, qp, ldq = _output(q, qkv, width, "q")
+    T, count = qkv.shape[0], 1
+    half = 0 if inv_freq is None else inv_freq.shape[0]
+    fp = _flat(inv_freq, (half,), _F32, "inv_freq")
+    if positions is not None:
+        count = 1 if positions.dim() == 1 else positions.shape[1]
+    pp = _flat(positions, (T,) if positions is not None and positions.dim() == 1 else (T, count), _I32, "positions")
+    ap = _flat(axes, (half,), _I32, "axes")
+    for t, what in ((inv_freq, "inv_freq"), (positions, "positions"), (axes, "axes")):
+        _beside(t, qkv, what)
+    if T > 0:
+        with _device_of(qkv):
+            st = lib.awq_append_kv(xp, ldx, *batch, fp, 2 * half, interleaved, pp, count, ap, qp, ldq, kp, vp, bp, pages,
+                                   page_size, _handle(qkv))
+        _check(st, "awq_append_kv")
+    return out
+
+
+class _Here:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *_):
+        return False
+
+
+_HERE = _Here()
+
+
+def _device_of(t: torch.Tensor):
+    """The tensor's device as the current one, for a launch; nothing to do where it is already."""
+    return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _attend_rows(name: str, q, cache, seqs, scale, y, workspace, options, shape):
+    """awq_attend and awq_attend_pages: ``options`` between the scale and the pages, ``shape`` of the workspace."""
+    lib = _lib or load_library()
+    qp, ldq, batch, (kp, vp, pages, page_size) = _cache_call(q, cache, seqs, 0, "q")
+    _beside(workspace, q, "workspace")
+    out, yp, ldy = _output(y, q, q.shape[1], "y")
+    if scale is None:
+        scale = batch[8] ** -0.5
+    if q.shape[0] > 0:
+        call, stream = getattr(lib, name), _handle(q)
+        with _device_of(q):
+            _with_workspace(
+                lambda ws, n: call(qp, ldq, *batch, scale, *options, kp, vp, pages, page_size, yp, ldy, ws, n, stream),
+                lambda: _bytes_of(name, *shape(batch, page_size)), name, workspace, q)
+    return out
+
+
+def attend(q: torch.Tensor, cache: KvCache, seqs: Sequences, scale: Optional[float] = None, shared: int = 0,
+           y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention of the new tokens' queries ``q`` [T, q_heads * head_dim] over their sequences' pages (their own
+    keys appended already): fp16 [T, q_heads * head_dim].  ``scale``: head_dim ** -0.5 by default.  ``shared``: how many
+    tokens all sequences begin with (a multiple of the page size); their pages, those of the first sequence's table,
+    are read and multiplied once for the whole batch.  A row without keys gives 0; rows of no sequence are left as
+    they are."""
+    return _attend_rows("awq_attend", q, cache, seqs, scale, y, workspace, (shared,),
+                        lambda b, size: (b[4], b[5], b[6], b[7], b[8], b[3], size, shared))
+
+
+def select_pages(q: torch.Tensor, cache: KvCache, seqs: Sequences, count: int, first: int = 1, recent: int = 1,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """For each new token and key head the pages of its sequence to attend to, int32 [T, kv_heads, count], ascending,
+    -1 past the last: all of them up to the token's place if they are at most ``count``, or else the ``first`` first,
+    the ``recent`` last, and those between whose bounds allow the largest products with the queries."""
+    lib = _lib or load_library()
+    qp, ldq, batch, (_, _, pages, page_size) = _cache_call(q, cache, seqs, 0, "q")
+    _beside(workspace, q, "workspace")
+    if cache.bounds is None:
+        raise ValueError("select_pages needs a cache with bounds")
+    bp = _page_bounds(cache)
+    if not 1 <= count < 1 << 31:
+        raise AwqError(AWQ_ERR_OPTION, "awq_select_pages")
+    T, kv_heads = q.shape[0], batch[7]
+    out = q.new_empty((T, kv_heads, count), dtype=_I32)
+    if T > 0:
+        stream = _handle(q)
+        with _device_of(q):
+            _with_workspace(
+                lambda ws, n: lib.awq_select_pages(qp, ldq, *batch, bp, pages, page_size, count, first, recent,
+                                                   out.data_ptr(), ws, n, stream),
+                lambda: _bytes_of("awq_select_pages", T, kv_heads, batch[3], count), "awq_select_pages", workspace, q)
+    return out
+
+
+def attend_pages(q: torch.Tensor, cache: KvCache, seqs: Sequences, pages: torch.Tensor, scale: Optional[float] = None,
+                 y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``attend`` over chosen pages only (``select_pages``' int32 [T, kv_heads, count], or any such choice of a
+    sequence's pages: each at most once, negative ones last), up to each token's place."""
+    if pages.dim() != 3 or pages.shape[:2] != (q.shape[0], cache.k.shape[1]):
+        raise ValueError("pages must be an int32 tensor [T, kv_heads, count]")
+    _beside(pages, q, "pages")
+    count = pages.shape[2]
+    return _attend_rows("awq_attend_pages", q, cache, seqs, scale, y, workspace,
+                        (_flat(pages, pages.shape, _I32, "pages"), count),
+                        lambda b, size: (b[4], b[6], b[7], b[8], size, count))
+
+
+def attention(x: torch.Tensor, qkv: PackedWeight, o: PackedWeight, cache: KvCache, seqs: Sequences,
+              inv_freq: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+              residual: Optional[torch.Tensor] = None, scale: Optional[float] = None, shared: int = 0,
+              pages: int = 0, first: int = 1, recent: int = 1, positions: Optional[torch.Tensor] = None,
+              axes: Optional[torch.Tensor] = None, interleaved: bool = False) -> torch.Tensor:
+    """A decoder block's attention for new tokens ``x`` [T, K]: the fused q/k/v layer (``pack_fused([q, k, v])``,
+    ``bias`` its own), the tokens' keys and values appended, attention over the cache, the output layer, plus
+    ``residual``.  With ``pages`` above 0 each token attends to that many pages only (``select_pages``)."""
+    rows = linear_fused(x, qkv, bias=bias)
+    q = append_kv(rows, cache, seqs, inv_freq, positions, axes, interleaved)
+    if pages:
+        y = attend_pages(q, cache, seqs, select_pages(q, cache, seqs, pages, first, recent), scale)
+    else:
+        y = attend(q, cache, seqs, scale, shared)
+    return linear_fused(y, o, residual=residual)

@@ -413,6 +413,116 @@ int awq_combine_experts(const void* x, int32_t ldx, const int32_t* offsets, cons
 size_t awq_combine_experts_workspace_bytes(int32_t T, int32_t top_k, int32_t E, int32_t N, int32_t K,
                                            int32_t group_size);
 
+/*
+ * Paged cache of keys and values.  Four entry points between a block's fused
+ * q/k/v layer and its output layer ("AI-Research-SKILLs AWQ 高级使用指南", section
+ * 层融合: fused attention; "Optimization Awq", fuse_max_seq_len: its cache).
+ *   k_pages, v_pages  fp16 [pages][kv_heads][page_size][head_dim]; page_size a
+ *                     power of two from 16 to 256, head_dim 64, 96, 128 or 256
+ *                     (AWQ_ERR_UNSUPPORTED otherwise).  Any size: pages are
+ *                     addressed with 64 bits.
+ *   bounds            fp16 [pages][kv_heads][2][head_dim]: per channel the least
+ *                     and the greatest of a page's keys (awq_select_pages).
+ *   offsets           int32 [B + 1], ascending: sequence b's new tokens are rows
+ *                     offsets[b] .. offsets[b + 1] - 1.  Rows of no sequence (behind
+ *                     the last, in a padded batch) are neither read nor written.
+ *   lengths           int32 [B]: each sequence's tokens, the new ones (its last)
+ *                     among them.  A sequence of length 0 has none.
+ *   tables            int32 [B][width]: each sequence's pages; token p is in slot
+ *                     p % page_size of page tables[b][p / page_size].  Entries past
+ *                     the length may hold anything.
+ * These three are read on the device (4-byte aligned).  Wrong ones give wrong
+ * results but never lead outside the buffers: rows are clamped to [0, T],
+ * lengths to [0, width * page_size], page numbers to [0, pages) for reading; to a
+ * page out of range nothing is written.  A new token whose place is negative (more
+ * rows than length) is not appended, and its attention is 0.
+ * q_heads is a multiple of kv_heads: key head h serves query heads h * G .. h * G
+ * + G - 1, G = q_heads / kv_heads.  1 <= B <= 2^16, T * q_heads <= 2^24, q_heads
+ * <= 1024.  Row strides as everywhere (multiples of 8, at most 2^21).
+ *
+ * awq_append_kv - new tokens into the cache, rotated on the way.
+ * x          in   fp16, row t at x + t * ldx: q_heads query vectors, kv_heads key
+ *                 vectors, kv_heads value vectors (the fused q/k/v layer's output).
+ * inv_freq   in   fp32 [rotary / 2] (device): pair i of the first `rotary` channels
+ *                 of each query and key turns by position * inv_freq[i], (a, b) ->
+ *                 (a cos - b sin, b cos + a sin); the pair is channels (i, rotary / 2 +
+ *                 i), or with interleaved != 0 (2 i, 2 i + 1).  The angle is formed and
+ *                 reduced in fp64, the rotation is fp32, one rounding to fp16.  rotary: a
+ *                 multiple of 16 up to head_dim (AWQ_ERR_OPTION); 0: no rotation.
+ * positions  in   int32 [T][axes] (device), or NULL: each token's place in its sequence.
+ * axis       in   int32 [rotary / 2] (device): the axis whose position pair i turns by
+ *                 (time, height, width); may be NULL with one axis.  1 <= axes <= 16.
+ * q          out  fp16, row t at q + t * ldq: the rotated queries.  May be the queries in
+ *                 x (same address and stride).
+ * k_pages, v_pages  the new tokens' slots are written, nothing else.
+ * bounds     NULL, or kept up to date: a page whose first slot is written starts anew,
+ *            any other page's grow to hold the new keys (as stored; NaN is passed over).
+ * A page that two sequences' new tokens fall into is a race.  Deterministic.
+ */
+int awq_append_kv(const void* x, int32_t ldx, const int32_t* offsets, const int32_t* lengths, const int32_t* tables,
+                  int32_t width, int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                  const float* inv_freq, int32_t rotary, int32_t interleaved, const int32_t* positions, int32_t axes,
+                  const int32_t* axis, void* q, int32_t ldq, void* k_pages, void* v_pages, void* bounds, int32_t pages,
+                  int32_t page_size, void* stream);
+
+/*
+ * awq_attend - causal attention of new tokens over their sequences' pages:
+ *   y[t][h] = sum_j p_j v_j,  p = softmax over the keys j <= place(t) of scale (q[t][h] . k_j)
+ * (the keys of a batch's new tokens are in the cache already: awq_append_kv).
+ * q          in   fp16, row t at q + t * ldq: q_heads vectors.
+ * scale      finite and > 0 (AWQ_ERR_OPTION).
+ * shared     keys that all sequences begin with (a common prompt; 0: none), a multiple
+ *            of page_size: read through the first sequence's table once for the whole
+ *            batch, whatever the other tables hold there.  Every sequence with rows must
+ *            have them.
+ * y          out  fp16, row t at y + t * ldy; must not overlap an input.  A row without
+ *                 keys gives 0.
+ * Products, softmax statistics and sums are fp32; the weights p are rounded to fp16 for
+ * the matrix cores, the result once.  Keys and values that a row does not see (past its
+ * place, or in a page's unused slots) never touch it, NaN and infinities included.
+ * Deterministic: the same bits again for the same call.
+ * workspace: awq_attend_workspace_bytes() bytes (NULL when 0), contents not needed
+ * before or after; shared as awq_linear_fused's.
+ */
+int awq_attend(const void* q, int32_t ldq, const int32_t* offsets, const int32_t* lengths, const int32_t* tables,
+               int32_t width, int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, float scale,
+               int32_t shared, const void* k_pages, const void* v_pages, int32_t pages, int32_t page_size, void* y,
+               int32_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+size_t awq_attend_workspace_bytes(int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                  int32_t width, int32_t page_size, int32_t shared);
+
+/*
+ * awq_select_pages - for each new token and key head the pages worth attending to:
+ * chosen[t][h][0 .. count - 1], page numbers within the token's sequence (not the
+ * cache's), ascending, -1 past the last.  A token with at most `count` pages up to its
+ * place takes them all; another takes the `first` first, the `recent` last and, of those
+ * between, the ones with the largest
+ *   score(page) = sum over the key head's query heads and the channels of max(q lo, q hi),
+ * lo and hi the page's bounds (the largest q . k that keys within them could have): q hi
+ * where q > 0, q lo where q < 0, nothing where q = 0; the lower page first among equal scores.  Scores are fp64 sums; NaN counts as the lowest.
+ * first >= 0, recent >= 1, first + recent <= count (AWQ_ERR_OPTION).  Deterministic.
+ * workspace: awq_select_pages_workspace_bytes() bytes (a score per token, key head and
+ * page of the tables), as awq_attend's.
+ */
+int awq_select_pages(const void* q, int32_t ldq, const int32_t* offsets, const int32_t* lengths, const int32_t* tables,
+                     int32_t width, int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                     const void* bounds, int32_t pages, int32_t page_size, int32_t count, int32_t first, int32_t recent,
+                     int32_t* chosen, void* workspace, size_t workspace_bytes, void* stream);
+size_t awq_select_pages_workspace_bytes(int32_t T, int32_t kv_heads, int32_t width, int32_t count);
+
+/*
+ * awq_attend_pages - awq_attend over chosen pages only: token t's query heads of key head
+ * h see the keys of pages chosen[t][h][..] up to the token's place.  Pages in any order,
+ * each at most once, negative ones (none) last; no key seen: 0.  Arguments and
+ * accuracy as awq_attend's.
+ */
+int awq_attend_pages(const void* q, int32_t ldq, const int32_t* offsets, const int32_t* lengths, const int32_t* tables,
+                     int32_t width, int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, float scale,
+                     const int32_t* chosen, int32_t count, const void* k_pages, const void* v_pages, int32_t pages,
+                     int32_t page_size, void* y, int32_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+size_t awq_attend_pages_workspace_bytes(int32_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                        int32_t page_size, int32_t count);
+
 /* Static, NUL-terminated description of a status code. */
 const char* awq_strerror(int status);
 
