@@ -24,7 +24,7 @@ ARCH = "gfx950"
 SOURCES = ("awq_api.hip", "awq_pack.hip", "awq_gemv.hip", "awq_gemv_small.hip", "awq_gemm.hip", "awq_scale.hip",
            "awq_noalloc.hip", "awq_experts.hip", "awq_expert_tiles.hip", "awq_expert_stream.hip",
            "awq_fused_gemv.hip", "awq_fused_few.hip", "awq_route.hip", "awq_fused_api.hip", "awq_append.hip",
-           "awq_select.hip", "awq_attend.hip", "awq_cache_api.hip")
+           "awq_select.hip", "awq_attend.hip", "awq_attend_waves.hip", "awq_attend_tiles.hip", "awq_cache_api.hip")
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -1,0 +1,197 @@
+// How the attention kernels share a batch's work, and where they leave what is
+// to be joined.
+#pragma once
+
+#include "awq_attend_block.hpp"
+
+namespace awq {
+
+// Rows of 32 and keys of 32 of one wave (few), rows of 128 and splits of the keys (many).
+struct AttendPlan {
+  bool own_few;       // a sequence's own keys: a wave per 32 rows, or a workgroup per 128
+  int prefix;         // the shared keys: 0: none, 1: with the waves (and own_few), 2: with the workgroups
+  int waves, least;   // waves of the first kind; key blocks that each takes at least
+  int own_splits, prefix_splits;  // of the second kind
+  int own_slices() const { return own_few ? (prefix ? 1 : 0) : prefix || own_splits > 1 ? own_splits : 0; }
+  int slices() const { return own_slices() + (prefix == 2 ? prefix_splits : prefix); }
+};
+
+// Partial results: for each row's query head (numbered t * q_heads + head) and slice the maximum (in powers of two),
+// the sum and the values' sums: slice 0 (to own_splits - 1) the own keys, the rest the shared ones; and two of
+// those of 32 rows per wave, for a piece that starts within a segment and one that ends within one.
+struct Partials {
+  float2* stat;    // [slices][rows]
+  float* sums;     // [slices][rows][dim]
+  float2* wave_stat;  // [waves][2][32]
+  float* wave_sums;   // [waves][2][32][dim]
+  int64_t rows;
+};
+
+inline Partials partials(const AttendPlan& p, int64_t rows, int dim, void* workspace) {
+  Partials x;
+  const int64_t waves = p.own_few ? 64 * (int64_t)p.waves : 0;
+  x.rows = rows;
+  x.sums = static_cast<float*>(workspace);
+  x.wave_sums = x.sums + p.slices() * rows * dim;
+  x.stat = reinterpret_cast<float2*>(x.wave_sums + waves * dim);
+  x.wave_stat = x.stat + p.slices() * rows;
+  return x;
+}
+inline size_t partial_bytes(const AttendPlan& p, int64_t rows, int dim) {
+  const int64_t all = p.slices() * rows + (p.own_few ? 64 * (int64_t)p.waves : 0);
+  return ((size_t)all * (dim * 4 + 8) + 15) & ~(size_t)15;
+}
+
+hipError_t launch_attend_waves(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan,
+                               const Partials& p, hipStream_t stream);
+hipError_t launch_attend_tiles(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan,
+                               const Partials& p, hipStream_t stream);
+
+__device__ __forceinline__ long long wave_sum64(long long v) {
+  for (int m = 1; m < 64; m <<= 1) {
+    const int lo = __shfl_xor((int)(uint32_t)v, m), hi = __shfl_xor((int)(v >> 32), m);
+    v += (long long)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+  }
+  return (long long)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v));
+}
+__device__ __forceinline__ long long prefix_sum64(long long v) {
+  const int lane = __lane_id();
+  for (int m = 1; m < 64; m <<= 1) {
+    const int lo = __shfl_up((int)(uint32_t)v, m), hi = __shfl_up((int)(v >> 32), m);
+    if (lane >= m) v += (long long)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+  }
+  return v;
+}
+__device__ __forceinline__ long long lane64(long long v, int lane) {
+  return (long long)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+                     (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane));
+}
+
+
+// The units of work of the waves (32 rows, a key head, 32 keys), in order: the shared keys' (all rows together), then
+// sequence after sequence; within one, rows, then key heads, then keys.  Every row has at least one.  Wave w takes the units
+// w * each .. w * each + each - 1.
+struct Units {
+  long long total, shared;
+  int each;
+};
+struct UnitArgs {
+  int group, heads, shift, shared_keys, waves, least;
+  bool shared;  // the shared keys are the waves' too
+};
+inline UnitArgs unit_args(const AttendArgs& a, const CacheArgs& c, const AttendPlan& plan) {
+  return UnitArgs{a.q_heads / c.heads, c.heads, c.shift, a.shared, plan.waves, plan.least, plan.prefix == 1};
+}
+__device__ __forceinline__ int key_blocks(const UnitArgs& u, int length) { return max((length - u.shared_keys + 31) >> 5, 1); }
+__device__ __forceinline__ int row_blocks(const UnitArgs& u, int rows) { return (rows * u.group + 31) >> 5; }
+__device__ __forceinline__ long long units_of(const UnitArgs& u, const Sequence& q) {
+  return q.rows ? (long long)row_blocks(u, q.rows) * u.heads * key_blocks(u, q.length) : 0;
+}
+// All rows of the batch as one sequence that ends with the shared keys.
+__device__ __forceinline__ Sequence all_rows(const SeqArgs& s, int shared_keys) {
+  const int from = min(max(s.offsets[0], 0), s.T);
+  return Sequence{0, from, max(min(s.offsets[s.B], s.T) - from, 0), shared_keys};
+}
+__device__ __forceinline__ Units count_units(const SeqArgs& s, const UnitArgs& u) {
+  long long own = 0;
+  for (int b0 = 0; b0 < s.B; b0 += 64) own += units_of(u, sequence_at(s, u.shift, b0 + __lane_id()));
+  Units n;
+  n.shared = u.shared ? (long long)row_blocks(u, all_rows(s, 0).rows) * u.heads * ((u.shared_keys + 31) >> 5) : 0;
+  n.total = n.shared + wave_sum64(own);
+  n.each = (int)max((n.total + u.waves - 1) / u.waves, (long long)u.least);
+  return n;
+}
+
+// 32 rows, numbered token after token, the key head's query heads within one: `first` is the number of the first,
+// `total` how many the sequence has; `place0` and `row0` are of its first token.
+struct Rows32 {
+  int first, total, row0, place0;
+};
+
+// The part of a segment's keys that a wave reads its page numbers for: 64 entries of a table or list, one per lane.
+struct Entries {
+  const int* table;  // the sequence's
+  const int* list;   // or NULL: every page of the table
+  int count, width;  // of the list, of the table
+  int first;         // entry of lane 0
+  int page, number;  // the lane's page of the sequence (-1: none) and its number in the cache
+
+  __device__ __forceinline__ void read(const CacheArgs& c, int from) {
+    first = from;
+    const int e = from + (int)__lane_id();
+    page = list ? (e < count ? list[e] : -1) : e;
+    if (page < 0 || page >= width) page = -1;
+    number = page_number(c, page >= 0 ? table[page] : 0);
+  }
+};
+
+constexpr int kNowhere = 1 << 30;  // a place behind every row's (subtracting it stays in 32 bits)
+
+// Where 16 keys are, and the place of the first of them in the sequence.
+struct Keys16 {
+  int64_t at;  // row of the cache
+  int place;
+};
+__device__ __forceinline__ Keys16 keys16(const Entries& e, const CacheArgs& c, int head, int key) {
+  const int lane = (key >> c.shift) - e.first, slot = key & ((1 << c.shift) - 1);
+  const int page = __builtin_amdgcn_readlane(e.page, lane), number = __builtin_amdgcn_readlane(e.number, lane);
+  return Keys16{(((int64_t)number * c.heads + head) << c.shift) + slot,
+                page < 0 ? kNowhere : (page << c.shift) + slot};
+}
+
+// The queries of a wave's 32 rows.
+template <int D>
+__device__ __forceinline__ void read_queries(Queries<D>& q, const AttendArgs& a, const Rows32& r, int group, int head) {
+  const int lane = __lane_id(), row = r.first + (lane & 31), token = row / group;
+  const bool live = row < r.total;
+  const _Float16* from = a.q + (live ? (r.row0 + token) * a.ldq + (int64_t)(head * group + row - token * group) * D : 0) +
+                         8 * (lane >> 5);
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    half8_t v = *reinterpret_cast<const half8_t*>(from + 16 * j);
+    if (!live) v = half8_t((_Float16)0.0f);
+    q.put(j, v);
+  }
+}
+
+// Results of a wave's 32 rows: to y (`slice` below 0), or unfinished to a slice of the rows, or to `wave_stat` and
+// `wave_sums` of 32 rows.
+template <int D>
+__device__ __forceinline__ void write_rows(const Gathered<D>& g, float c, const AttendArgs& a, const Partials& p,
+                                           const Rows32& r, int group, int head, int slice, float2* wave_stat,
+                                           float* wave_sums) {
+  const int lane = __lane_id(), row = r.first + (lane & 31), token = row / group, half = lane >> 5;
+  if (row >= r.total) return;
+  const float sum = both_halves_sum(g.sum);
+  const int64_t t = r.row0 + token;
+  const int at = head * group + row - token * group;
+  if (slice < 0 && !wave_stat) {
+    const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+    _Float16* y = a.y + t * a.ldy + (int64_t)at * D + 4 * half;
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        half4_t v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = (_Float16)(sum == 0.0f ? 0.0f : g.sums[b][4 * n + i] * by);
+        *reinterpret_cast<half4_t*>(y + 32 * b + 8 * n) = v;
+      }
+    return;
+  }
+  const int64_t to = wave_stat ? lane & 31 : (int64_t)slice * p.rows + t * a.q_heads + at;
+  if (half == 0) (wave_stat ? wave_stat : p.stat)[to] = float2{g.top * c, sum};
+  float* sums = (wave_stat ? wave_sums : p.sums) + to * D + 4 * half;
+#pragma unroll
+  for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      float4_t v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = g.sums[b][4 * n + i];
+      *reinterpret_cast<float4_t*>(sums + 32 * b + 8 * n) = v;
+    }
+}
+
+}  // namespace awq

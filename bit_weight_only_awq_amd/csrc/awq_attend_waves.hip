@@ -1,0 +1,185 @@
+// Attention of few rows per sequence (decoding): each wave on its own, 32 rows of
+// queries against an equal share of all keys.
+//
+// Mathematics: awq_attend_block.hpp's.  A unit of work is 32 keys for up to 32 rows
+// (tokens times query heads of one key head); all units of the batch, whatever the
+// lengths, are one list, and each of the `waves` waves takes an equal run of it, so
+// ragged batches and single long sequences fill the chip alike.  A wave that
+// takes a whole segment (rows, key head) writes its result; the pieces of the
+// others are joined by a second launch.
+//
+// Bound: HBM, each key and value once.  Keys and values go straight to LDS
+// (16 bytes per lane, whole rows), one block of 32 keys ahead of the products; a
+// workgroup is one wave, so nothing waits for a barrier.
+#include "awq_attend.hpp"
+
+namespace awq {
+namespace {
+
+template <int D, bool LIST>
+__global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(AttendArgs a, CacheArgs c, SeqArgs s, UnitArgs units, Partials p) {
+  using T = Tile<D>;
+  constexpr int LOADS = T::LOADS;
+  __shared__ __attribute__((aligned(1024))) char k0[32 * T::ROW], v0[32 * T::ROW], k1[32 * T::ROW], v1[32 * T::ROW];
+  __shared__ __attribute__((aligned(1024))) char queries[Queries<D>::BYTES ? Queries<D>::BYTES : 16];
+  const int lane = threadIdx.x, wave = blockIdx.x, group = units.group;
+  const float scale = a.scale * kLog2E;
+
+  Units n;
+  int list_blocks = 0, list_rows = 0;
+  if constexpr (LIST) {
+    list_blocks = ((a.count << c.shift) + 31) >> 5;
+    list_rows = row_blocks(units, 1);
+    n.shared = 0;
+    n.total = (long long)s.T * c.heads * list_rows * list_blocks;
+    n.each = (int)max((n.total + units.waves - 1) / units.waves, (long long)units.least);
+  } else {
+    n = count_units(s, units);
+  }
+  long long at = (long long)wave * n.each;
+  const long long end = min(n.total, at + n.each);
+
+  const Sources<D> kept(lane, 0);
+
+  while (at < end) {
+    // the segment that unit `at` is in
+    Sequence seq{0, 0, 0, 0};
+    long long nth;  // of the sequence's units
+    int blocks, key0 = 0, count = 0;
+    const int* list = nullptr;
+    bool shared = false;
+    if constexpr (LIST) {
+      const long long per_token = (long long)c.heads * list_rows * list_blocks;
+      const int t = (int)(at / per_token);
+      nth = at - t * per_token;
+      blocks = list_blocks;
+      const Sequence of = sequence_of(s, c.shift, t);
+      if (of.rows == 0) {  // a row of no sequence
+        at += per_token - nth;
+        continue;
+      }
+      seq = Sequence{of.index, t, 1, t - of.row0 + of.place0() + 1};
+    } else if (at < n.shared) {
+      shared = true;
+      seq = all_rows(s, a.shared);
+      nth = at;
+      blocks = (a.shared + 31) >> 5;
+    } else {
+      long long seen = n.shared;
+      for (int b0 = 0;; b0 += 64) {  // (some sequence holds it: at < total)
+        const Sequence q = sequence_at(s, c.shift, b0 + lane);
+        const long long mine = units_of(units, q), sum = seen + prefix_sum64(mine);
+        const unsigned long long owner = __ballot(sum > at && sum - mine <= at);
+        if (owner != 0) {
+          const int l = __builtin_ctzll(owner);
+          seq = pick(q, l);
+          nth = at - lane64(sum - mine, l);
+          break;
+        }
+        seen = lane64(sum, 63);
+      }
+      blocks = key_blocks(units, seq.length);
+      key0 = a.shared;
+    }
+    const int which = (int)(nth / blocks), block0 = (int)(nth - (long long)which * blocks);
+    const int row_block = which / c.heads, head = which - row_block * c.heads;
+    const int here = (int)min((long long)(blocks - block0), end - at);
+    at += here;
+    const Rows32 rows{32 * row_block, seq.rows * group, seq.row0, seq.place0()};
+    // places of the rows: their own, and the least and greatest of them (past the shared keys: the last of these)
+    const int mine = (min(rows.first + (lane & 31), rows.total - 1)) / group;
+    const int place = shared ? a.shared - 1 : rows.place0 + mine;
+    const int least = shared ? a.shared - 1 : rows.place0 + rows.first / group;
+    const int most = shared ? a.shared - 1 : rows.place0 + (min(rows.first + 32, rows.total) - 1) / group;
+    if constexpr (LIST) {
+      list = a.list + ((int64_t)seq.row0 * c.heads + head) * a.count;
+      count = a.count;
+    }
+    Entries pages{s.tables + (int64_t)seq.index * s.width, list, count, s.width, 0, 0, 0};
+
+    Queries<D> q;
+    q.place((lds_char*)queries);
+    read_queries(q, a, rows, group, head);
+    Gathered<D> g;
+    g.clear();
+
+    int place0 = 0, place1 = 0, next0 = 0, next1 = 0;  // of the first of 16 keys
+    auto load = [&](int block, lds_char* keys, lds_char* values) __attribute__((always_inline)) {
+      const int key = key0 + 32 * (block0 + block);
+      if (block == 0 || ((key + 16) >> c.shift) - pages.first >= 64) pages.read(c, key >> c.shift);
+      Sources<D> from_lane = kept;
+      asm volatile("" : "+v"(from_lane.keys[0]), "+v"(from_lane.values[0]));  // (each load's is formed here, not kept)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const Keys16 from = keys16(pages, c, head, key + 16 * h);
+        (h ? next1 : next0) = from.place;
+        const char* k = reinterpret_cast<const char*>(c.k + from.at * D);
+        const char* v = reinterpret_cast<const char*>(c.v + from.at * D);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load_to_lds(k + from_lane.key(i), keys + 16 * h * T::ROW + 1024 * i);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load_to_lds(v + from_lane.value(i), values + 16 * h * T::ROW + 1024 * i);
+      }
+    };
+    auto step = [&](int block, lds_char* keys, lds_char* values, lds_char* next_keys, lds_char* next_values)
+                    __attribute__((always_inline)) {
+      place0 = next0;
+      place1 = next1;
+      if (block + 1 < here) {
+        load(block + 1, next_keys, next_values);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * LOADS) : "memory");
+      } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      }
+      const Seen seen{place - place0, place - place1, least - place0 >= 15 && least - place1 >= 15};
+      uint32_t strange = 0;
+      if (!seen.all) {
+        const uint64_t met = hide_strange<D, 32>(values, lane, 64, [&](int h, int& behind, int& upto) {
+          behind = least - (h ? place1 : place0);
+          upto = most - (h ? place1 : place0);
+        });
+        if (__any(met != 0)) {
+          strange = (uint32_t)met;
+          for (int m = 1; m < 64; m <<= 1) strange |= (uint32_t)__shfl_xor((int)strange, m);
+          strange = __builtin_amdgcn_readfirstlane(strange);
+        }
+      }
+      attend_block<D>(keys, values, q, scale, seen, strange, [&](int k) {
+        const int key = key0 + 32 * (block0 + block) + k;
+        const int page = list ? list[key >> c.shift] : key >> c.shift;
+        const int64_t number = page_number(c, pages.table[page]);
+        return c.v + (((number * c.heads + head) << c.shift) + (key & ((1 << c.shift) - 1))) * D;
+      }, g);
+    };
+    load(0, (lds_char*)k0, (lds_char*)v0);
+    for (int block = 0; block < here; block += 2) {
+      step(block, (lds_char*)k0, (lds_char*)v0, (lds_char*)k1, (lds_char*)v1);
+      if (block + 1 < here) step(block + 1, (lds_char*)k1, (lds_char*)v1, (lds_char*)k0, (lds_char*)v0);
+    }
+    const bool whole = here == blocks;
+    const int64_t slot = 2 * (int64_t)wave + (block0 > 0 ? 0 : 1);
+    write_rows(g, scale, a, p, rows, group, head, shared ? 1 : a.shared > 0 ? 0 : -1,
+               whole ? nullptr : p.wave_stat + slot * 32, p.wave_sums + slot * 32 * D);
+  }
+}
+
+template <int D>
+void launch(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan, const Partials& p,
+            const UnitArgs& u, hipStream_t stream) {
+  if (a.list) hipLaunchKernelGGL((attend_waves_kernel<D, true>), dim3(plan.waves), dim3(64), 0, stream, a, c, s, u, p);
+  else hipLaunchKernelGGL((attend_waves_kernel<D, false>), dim3(plan.waves), dim3(64), 0, stream, a, c, s, u, p);
+}
+
+}  // namespace
+
+hipError_t launch_attend_waves(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan,
+                               const Partials& p, hipStream_t stream) {
+  const UnitArgs u = unit_args(a, c, plan);
+  if (c.dim == 64) launch<64>(a, c, s, plan, p, u, stream);
+  else if (c.dim == 96) launch<96>(a, c, s, plan, p, u, stream);
+  else if (c.dim == 128) launch<128>(a, c, s, plan, p, u, stream);
+  else launch<256>(a, c, s, plan, p, u, stream);
+  return hipGetLastError();
+}
+
+}  // namespace awq

@@ -22,11 +22,11 @@ constexpr int32_t kMaxAxes = 16;
 bool dim_known(int32_t dim) { return dim == 64 || dim == 96 || dim == 128 || dim == 256; }
 bool page_known(int32_t size) { return size >= 16 && size <= 256 && (size & (size - 1)) == 0; }
 
-// Token and head counts and the tables' width; then the page size, so that places stay in 31 bits.
+// Token and head counts and the tables' width; then the page size, so that places stay within 30 bits.
 bool counts_ok(int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t width, int32_t page_size) {
   return T >= 1 && B >= 1 && B <= kMaxSeqs && kv_heads >= 1 && q_heads >= kv_heads && q_heads <= kMaxHeads &&
          q_heads % kv_heads == 0 && (int64_t)T * q_heads <= kMaxRows && width >= 1 && page_known(page_size) &&
-         (int64_t)width * page_size < ((int64_t)1 << 31);
+         (int64_t)width * page_size <= ((int64_t)1 << 30);
 }
 
 int check_cache(const int32_t* offsets, const int32_t* lengths, const int32_t* tables, int32_t width, int32_t T, int32_t B,
@@ -156,7 +156,7 @@ int awq_attend_pages(const void* q, int32_t ldq, const int32_t* offsets, const i
   if (!stride_ok(ldq, row) || !stride_ok(ldy, row)) return AWQ_ERR_SHAPE;
   if (!(scale > 0.0f) || isinf(scale)) return AWQ_ERR_OPTION;
   if (count < 1 || (int64_t)T * kv_heads * count >= ((int64_t)1 << 31) ||
-      (int64_t)count * page_size >= ((int64_t)1 << 31))
+      (int64_t)count * page_size > ((int64_t)1 << 30))
     return AWQ_ERR_OPTION;
   st = check_pointers(q, k_pages, v_pages, y);
   if (st != AWQ_OK) return st;
