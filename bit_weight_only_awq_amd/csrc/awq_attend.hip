@@ -18,124 +18,140 @@ struct JoinArgs {
   int own_slices, shared_slices;
 };
 
-// The join of some parts of one row, four channels per lane.
-struct Joined {
-  float4_t sums;
-  float top, sum;
-  __device__ __forceinline__ void add(float part_top, float part_sum, float4_t part) {
-    if (part_top == -INFINITY && part_sum == 0.0f) return;  // (a part that saw no key)
-    const float m = fmaxf(top, part_top);
-    const float was = top == m ? 1.0f : __builtin_amdgcn_exp2f(top - m);
-    const float is = part_top == m ? 1.0f : __builtin_amdgcn_exp2f(part_top - m);
-    top = m;
-    sum = sum * was + part_sum * is;
-    sums = sums * was + part * is;
-  }
-};
-
-// A row (token and query head) for WAVES waves; in a wave, LANES lanes hold the
-// row's channels and 64 / LANES groups of them share the parts.
-template <int D, int WAVES>
+// A wave per row (token and query head): 64 parts at a time, a lane holding each
+// part's maximum and sum, then LANES lanes their share of the channels and 64 /
+// LANES groups of lanes every such part.
+template <int D>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, SeqArgs s, JoinArgs j, Partials p) {
-  constexpr int LANES = D <= 64 ? 16 : D <= 128 ? 32 : 64, PARTS = 64 / LANES * WAVES;
-  __shared__ float4_t sums[4][64];
-  __shared__ float2 stats[4];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * (4 / WAVES) + wave / WAVES;  // (every wave of the workgroup has one)
-  const int t = (int)(row / a.q_heads), at = (int)(row - (int64_t)t * a.q_heads);
-  const int group = j.units.group, head = at / group, channel = 4 * (lane & (LANES - 1));
-  const int part = wave % WAVES * (64 / LANES) + lane / LANES;
-  const bool live = channel < D && t < s.T;
-  Joined x{float4_t(0.0f), -INFINITY, 0.0f};
+  constexpr int LANES = D <= 64 ? 16 : D <= 128 ? 32 : 64, GROUPS = 64 / LANES, AHEAD = 4;
+  const int lane = threadIdx.x & 63;
+  const int row = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  const int t = row / a.q_heads, at = row - t * a.q_heads;
+  if (t >= s.T) return;
+  const int group = j.units.group, head = at / group, g = at - head * group;
 
   // the row's sequence and, among the waves' units, the first of it
   Sequence seq{0, 0, 0, 0};
-  long long first = 0;
+  int first = 0;
   Units n{0, 0, 1};
   if (j.own_few && !a.list) {
-    n = count_units(s, j.units);
-    long long seen = n.shared;
+    const int shared = j.units.shared ? row_blocks(j.units, all_rows(s, 0).rows) * c.heads * ((j.units.shared_keys + 31) >> 5) : 0;
+    int seen = shared;
     for (int b0 = 0; b0 < s.B; b0 += 64) {
       const Sequence q = sequence_at(s, c.shift, b0 + lane);
-      const long long mine = units_of(j.units, q), sum = seen + prefix_sum64(mine);
+      const int mine = units_of(j.units, q), sum = seen + prefix_sum(mine);
       const unsigned long long owner = __ballot(t >= q.row0 && t < q.row0 + q.rows);
-      if (owner != 0) {
+      if (owner != 0 && seq.rows == 0) {
         const int l = __builtin_ctzll(owner);
         seq = pick(q, l);
-        first = lane64(sum - mine, l);
-        break;
+        first = __builtin_amdgcn_readlane(sum - mine, l);
       }
-      seen = lane64(sum, 63);
+      seen = __builtin_amdgcn_readlane(sum, 63);
     }
+    n = share_units(j.units, seen, shared);
   } else {
     seq = sequence_of(s, c.shift, t);
+    if (a.list) n = share_units(j.units, s.T * c.heads * row_blocks(j.units, 1) * list_blocks(j.units, a.count), 0);
   }
-  bool write = seq.rows > 0;
-  if (seq.rows > 0 && t - seq.row0 + seq.place0() >= 0) {
-    auto slice = [&](int i) __attribute__((always_inline)) {
-      const int64_t from = i * p.rows + row;
-      const float2 stat = p.stat[from];
-      x.add(stat.x, stat.y, *reinterpret_cast<const float4_t*>(p.sums + from * D + channel));
-    };
-    // the waves' pieces of the segment that begins at `unit`, row r of its 32; whole, it is in slice `whole`, or in y
-    auto pieces = [&](long long unit, int blocks, int r, int whole) __attribute__((always_inline)) {
-      const int w0 = (int)(unit / n.each), w1 = (int)((unit + blocks - 1) / n.each);
-      if (w0 == w1) {
-        if (whole < 0) write = false;
-        else if (live && part == 0) slice(whole);
-        return;
+  if (seq.rows == 0) return;  // a row of no sequence stays as it is
+
+  // The row's parts: own_waves pieces of waves from `own_wave` on and shared_waves from `shared_wave` on, then slices.
+  // (A row without a place has parts as well: those of its own keys, all empty, and those of shared keys, not its.)
+  int own_unit = 0, own_wave = 0, own_waves = 0, own_row = 0, shared_unit = 0, shared_wave = 0, shared_waves = 0,
+      shared_row = 0, slice0 = 0, slices = 0;
+  const bool placed = t - seq.row0 + seq.place0() >= 0;
+  if (j.own_few) {
+    const int blocks = a.list ? list_blocks(j.units, a.count) : key_blocks(j.units, seq.length);
+    const int r = a.list ? g : (t - seq.row0) * group + g;
+    const int before = a.list ? t * row_blocks(j.units, 1) : 0;
+    own_unit = first + ((before + (r >> 5)) * c.heads + head) * blocks;
+    own_row = r & 31;
+    own_wave = own_unit / n.each;
+    own_waves = (own_unit + blocks - 1) / n.each - own_wave + 1;
+    if (own_waves == 1) {
+      if (j.own_slices == 0) return;  // the result is in place
+      own_waves = 0;
+      slices = 1;
+    } else {
+      slice0 = j.own_slices;
+    }
+  } else {
+    slices = j.own_slices;
+  }
+  if (j.units.shared) {
+    const int blocks = (j.units.shared_keys + 31) >> 5, r = (t - all_rows(s, 0).row0) * group + g;
+    shared_unit = ((r >> 5) * c.heads + head) * blocks;
+    shared_row = r & 31;
+    shared_wave = shared_unit / n.each;
+    shared_waves = (shared_unit + blocks - 1) / n.each - shared_wave + 1;
+    if (shared_waves == 1) {
+      shared_waves = 0;
+      slices = 2 - slice0;  // (slice 0: the own keys, 1: the shared)
+    }
+  } else {
+    slices += j.shared_slices;
+  }
+  const int parts = placed ? own_waves + shared_waves + slices : 0;
+
+  float4_t sums = float4_t(0.0f);
+  float top = -INFINITY, total = 0.0f;
+  const int channel = 4 * (lane & (LANES - 1));
+  const bool live = channel < D;
+  for (int i0 = 0; i0 < parts; i0 += 64) {
+    // where part i0 + lane is: a number of 32 rows of a wave, negative, or of a row of a slice
+    int i = i0 + lane, from = 0;
+    float2 stat{-INFINITY, 0.0f};
+    if (i < parts) {
+      if (i < own_waves + shared_waves) {
+        const bool own = i < own_waves;
+        const int w = own ? own_wave + i : shared_wave + i - own_waves;
+        from = -1 - ((2 * w + (w * n.each > (own ? own_unit : shared_unit) ? 0 : 1)) * 32 + (own ? own_row : shared_row));
+        stat = p.wave_stat[-1 - from];
+      } else {
+        from = (int)((slice0 + i - own_waves - shared_waves) * p.rows) + row;
+        stat = p.stat[from];
       }
-      if (live)
-        for (int w = w0 + part; w <= w1; w += PARTS) {
-          const int64_t from = (2 * (int64_t)w + ((long long)w * n.each > unit ? 0 : 1)) * 32 + r;
-          const float2 stat = p.wave_stat[from];
-          x.add(stat.x, stat.y, *reinterpret_cast<const float4_t*>(p.wave_sums + from * D + channel));
-        }
-    };
-    if (a.list) {
-      const int list_rows = row_blocks(j.units, 1), r = at - head * group, blocks = ((a.count << c.shift) + 31) >> 5;
-      const long long all = (long long)s.T * c.heads * list_rows * blocks;
-      n.each = (int)max((all + j.units.waves - 1) / j.units.waves, (long long)j.units.least);
-      pieces((((long long)t * list_rows + (r >> 5)) * c.heads + head) * blocks, blocks, r & 31, -1);
-    } else if (j.own_few) {
-      const int r = (t - seq.row0) * group + at - head * group, blocks = key_blocks(j.units, seq.length);
-      pieces(first + ((long long)(r >> 5) * c.heads + head) * blocks, blocks, r & 31, j.own_slices > 0 ? 0 : -1);
     }
-    if (j.units.shared) {
-      const int r = (t - all_rows(s, 0).row0) * group + at - head * group, blocks = (j.units.shared_keys + 31) >> 5;
-      pieces(((long long)(r >> 5) * c.heads + head) * blocks, blocks, r & 31, 1);
-    }
-    // what workgroups of 128 rows made
-    if (live) {
-      const int from = j.own_few ? j.own_slices : 0, to = j.own_slices + (j.units.shared ? 0 : j.shared_slices);
-      for (int i = from + part; i < to; i += PARTS) slice(i);
+    float m = stat.x;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
+    m = fmaxf(m, top);
+    // (a part that saw no key counts nothing, also where none did)
+    const float share = stat.x == -INFINITY && stat.y == 0.0f ? 0.0f : stat.x == m ? 1.0f : __builtin_amdgcn_exp2f(stat.x - m);
+    float sum = share * stat.y;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
+    const float carry = top == m ? 1.0f : __builtin_amdgcn_exp2f(top - m);
+    total = total * carry + sum;
+    if (i0 > 0) sums *= carry;
+    top = m;
+    const int here = min(64, parts - i0);
+    for (int k0 = 0; k0 < here; k0 += AHEAD * GROUPS) {
+      float4_t v[AHEAD];
+      float by[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const int of = k0 + k * GROUPS + lane / LANES, where = __shfl(from, of & 63);
+        by[k] = __shfl(share, of & 63);
+        v[k] = float4_t(0.0f);
+        if (of >= here) by[k] = 0.0f;
+        else if (live)
+          v[k] = *reinterpret_cast<const float4_t*>(
+              (where < 0 ? p.wave_sums + (int64_t)(-1 - where) * D : p.sums + (int64_t)where * D) + channel);
+      }
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) sums += v[k] * by[k];
     }
   }
 #pragma unroll
-  for (int m = LANES; m < 64; m <<= 1) {
-    float4_t other;
+  for (int m = LANES; m < 64; m <<= 1)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) other[i] = __shfl_xor(x.sums[i], m);
-    const float top = __shfl_xor(x.top, m), sum = __shfl_xor(x.sum, m);
-    // (in the order of the lanes, so that both get the same)
-    Joined lower = lane & m ? Joined{other, top, sum} : x;
-    if (lane & m) lower.add(x.top, x.sum, x.sums);
-    else lower.add(top, sum, other);
-    x = lower;
-  }
-  if constexpr (WAVES > 1) {
-    sums[wave][lane] = x.sums;
-    if (lane == 0) stats[wave] = float2{x.top, x.sum};
-    __syncthreads();
-    if (wave != 0) return;
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) x.add(stats[w].x, stats[w].y, sums[w][lane]);
-  }
-  if (!write || !live || lane >= LANES) return;
-  const float by = x.sum == 0.0f ? 0.0f : 1.0f / x.sum;
+    for (int i = 0; i < 4; ++i) sums[i] += __shfl_xor(sums[i], m);
+  if (!live || lane >= LANES) return;
+  const float by = total == 0.0f ? 0.0f : 1.0f / total;
   half4_t v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = (_Float16)(x.sum == 0.0f ? 0.0f : x.sums[i] * by);
+  for (int i = 0; i < 4; ++i) v[i] = (_Float16)(total == 0.0f ? 0.0f : sums[i] * by);
   *reinterpret_cast<half4_t*>(a.y + t * a.ldy + (int64_t)at * D + channel) = v;
 }
 
@@ -146,7 +162,7 @@ constexpr int kUnits = 256;  // compute units
 int splits_of(int64_t tiles, int64_t stages, int slots, double extra) {
   int best = 1;
   double least = 1e300;
-  for (int n = 1; n <= 64 && n * 2 <= stages + 1; ++n) {
+  for (int n = 1; n <= 64 && n * 2 <= stages + 1 && (n == 1 || tiles * n <= 16 * slots); ++n) {
     const double rounds = (double)((tiles * n + slots - 1) / slots);
     const double time = rounds * ((double)((stages + n - 1) / n) + extra) + 0.3 * n;
     if (time < least) {
@@ -161,7 +177,9 @@ AttendPlan plan_of(int T, int B, int q_heads, int kv_heads, int dim, int page_si
   const int group = q_heads / kv_heads, stage = dim == 256 ? 32 : 64, slots = dim == 256 ? kUnits : 2 * kUnits;
   const int64_t rows = (int64_t)T * group;
   AttendPlan p{};
-  p.own_few = list || rows <= 32 * (int64_t)B;
+  // (units of the waves: 32 rows, at least a block of them per sequence, times key heads and blocks of 32 keys)
+  const int64_t units = kv_heads * ((rows / 32 + B) * ((int64_t)width * page_size / 32 + 1) + (rows / 32 + 1) * (shared / 32 + 1));
+  p.own_few = list || (rows <= 32 * (int64_t)B && units < kMostUnits);
   p.prefix = shared == 0 ? 0 : p.own_few && rows <= 32 ? 1 : 2;
   p.waves = kUnits * (dim == 256 ? 2 : dim == 128 ? 5 : 6);
   p.least = 2;
@@ -178,8 +196,7 @@ template <int D>
 void launch_join(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const JoinArgs& j, const Partials& p,
                  hipStream_t stream) {
   const int64_t rows = (int64_t)s.T * a.q_heads;
-  if (j.own_few) hipLaunchKernelGGL((join_kernel<D, 4>), dim3((unsigned)rows), dim3(256), 0, stream, a, c, s, j, p);
-  else hipLaunchKernelGGL((join_kernel<D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, c, s, j, p);
+  hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, c, s, j, p);
 }
 
 }  // namespace

@@ -47,34 +47,11 @@ hipError_t launch_attend_waves(const AttendArgs& a, const CacheArgs& c, const Se
 hipError_t launch_attend_tiles(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan,
                                const Partials& p, hipStream_t stream);
 
-__device__ __forceinline__ long long wave_sum64(long long v) {
-  for (int m = 1; m < 64; m <<= 1) {
-    const int lo = __shfl_xor((int)(uint32_t)v, m), hi = __shfl_xor((int)(v >> 32), m);
-    v += (long long)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
-  }
-  return (long long)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
-                     (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v));
-}
-__device__ __forceinline__ long long prefix_sum64(long long v) {
-  const int lane = __lane_id();
-  for (int m = 1; m < 64; m <<= 1) {
-    const int lo = __shfl_up((int)(uint32_t)v, m), hi = __shfl_up((int)(v >> 32), m);
-    if (lane >= m) v += (long long)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
-  }
-  return v;
-}
-__device__ __forceinline__ long long lane64(long long v, int lane) {
-  return (long long)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
-                     (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane));
-}
-
-
 // The units of work of the waves (32 rows, a key head, 32 keys), in order: the shared keys' (all rows together), then
 // sequence after sequence; within one, rows, then key heads, then keys.  Every row has at least one.  Wave w takes the units
-// w * each .. w * each + each - 1.
+// w * each .. w * each + each - 1.  (The host makes sure that their number stays below kMostUnits.)
 struct Units {
-  long long total, shared;
-  int each;
+  int total, shared, each;
 };
 struct UnitArgs {
   int group, heads, shift, shared_keys, waves, least;
@@ -85,23 +62,28 @@ inline UnitArgs unit_args(const AttendArgs& a, const CacheArgs& c, const AttendP
 }
 __device__ __forceinline__ int key_blocks(const UnitArgs& u, int length) { return max((length - u.shared_keys + 31) >> 5, 1); }
 __device__ __forceinline__ int row_blocks(const UnitArgs& u, int rows) { return (rows * u.group + 31) >> 5; }
-__device__ __forceinline__ long long units_of(const UnitArgs& u, const Sequence& q) {
-  return q.rows ? (long long)row_blocks(u, q.rows) * u.heads * key_blocks(u, q.length) : 0;
+__device__ __forceinline__ int units_of(const UnitArgs& u, const Sequence& q) {
+  return q.rows ? row_blocks(u, q.rows) * u.heads * key_blocks(u, q.length) : 0;
 }
 // All rows of the batch as one sequence that ends with the shared keys.
 __device__ __forceinline__ Sequence all_rows(const SeqArgs& s, int shared_keys) {
   const int from = min(max(s.offsets[0], 0), s.T);
   return Sequence{0, from, max(min(s.offsets[s.B], s.T) - from, 0), shared_keys};
 }
-__device__ __forceinline__ Units count_units(const SeqArgs& s, const UnitArgs& u) {
-  long long own = 0;
-  for (int b0 = 0; b0 < s.B; b0 += 64) own += units_of(u, sequence_at(s, u.shift, b0 + __lane_id()));
-  Units n;
-  n.shared = u.shared ? (long long)row_blocks(u, all_rows(s, 0).rows) * u.heads * ((u.shared_keys + 31) >> 5) : 0;
-  n.total = n.shared + wave_sum64(own);
-  n.each = (int)max((n.total + u.waves - 1) / u.waves, (long long)u.least);
-  return n;
+__device__ __forceinline__ Units share_units(const UnitArgs& u, int total, int shared) {
+  return Units{total, shared, max((total + u.waves - 1) / u.waves, u.least)};
 }
+__device__ __forceinline__ Units count_units(const SeqArgs& s, const UnitArgs& u) {
+  const int shared = u.shared ? row_blocks(u, all_rows(s, 0).rows) * u.heads * ((u.shared_keys + 31) >> 5) : 0;
+  int total = shared;
+  for (int b0 = 0; b0 < s.B; b0 += 64)
+    total += __builtin_amdgcn_readlane(prefix_sum(units_of(u, sequence_at(s, u.shift, b0 + __lane_id()))), 63);
+  return share_units(u, total, shared);
+}
+// For a list of pages per token: units of a token.
+__device__ __forceinline__ int list_blocks(const UnitArgs& u, int count) { return ((count << u.shift) + 31) >> 5; }
+
+constexpr int64_t kMostUnits = 1 << 30;
 
 // 32 rows, numbered token after token, the key head's query heads within one: `first` is the number of the first,
 // `total` how many the sequence has; `place0` and `row0` are of its first token.

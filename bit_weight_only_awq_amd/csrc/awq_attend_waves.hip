@@ -25,34 +25,24 @@ __global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(Atte
   const int lane = threadIdx.x, wave = blockIdx.x, group = units.group;
   const float scale = a.scale * kLog2E;
 
-  Units n;
-  int list_blocks = 0, list_rows = 0;
-  if constexpr (LIST) {
-    list_blocks = ((a.count << c.shift) + 31) >> 5;
-    list_rows = row_blocks(units, 1);
-    n.shared = 0;
-    n.total = (long long)s.T * c.heads * list_rows * list_blocks;
-    n.each = (int)max((n.total + units.waves - 1) / units.waves, (long long)units.least);
-  } else {
-    n = count_units(s, units);
-  }
-  long long at = (long long)wave * n.each;
-  const long long end = min(n.total, at + n.each);
+  const int list_rows = row_blocks(units, 1), of_list = LIST ? list_blocks(units, a.count) : 0;
+  const int per_token = c.heads * list_rows * of_list;
+  const Units n = LIST ? share_units(units, s.T * per_token, 0) : count_units(s, units);
+  int at = wave * n.each;
+  const int end = min(n.total, at + n.each);
 
   const Sources<D> kept(lane, 0);
 
   while (at < end) {
     // the segment that unit `at` is in
     Sequence seq{0, 0, 0, 0};
-    long long nth;  // of the sequence's units
-    int blocks, key0 = 0, count = 0;
+    int nth, blocks, key0 = 0, count = 0;  // nth: of the sequence's units
     const int* list = nullptr;
     bool shared = false;
     if constexpr (LIST) {
-      const long long per_token = (long long)c.heads * list_rows * list_blocks;
-      const int t = (int)(at / per_token);
+      const int t = at / per_token;
       nth = at - t * per_token;
-      blocks = list_blocks;
+      blocks = of_list;
       const Sequence of = sequence_of(s, c.shift, t);
       if (of.rows == 0) {  // a row of no sequence
         at += per_token - nth;
@@ -65,25 +55,25 @@ __global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(Atte
       nth = at;
       blocks = (a.shared + 31) >> 5;
     } else {
-      long long seen = n.shared;
+      int seen = n.shared;
       for (int b0 = 0;; b0 += 64) {  // (some sequence holds it: at < total)
         const Sequence q = sequence_at(s, c.shift, b0 + lane);
-        const long long mine = units_of(units, q), sum = seen + prefix_sum64(mine);
+        const int mine = units_of(units, q), sum = seen + prefix_sum(mine);
         const unsigned long long owner = __ballot(sum > at && sum - mine <= at);
         if (owner != 0) {
           const int l = __builtin_ctzll(owner);
           seq = pick(q, l);
-          nth = at - lane64(sum - mine, l);
+          nth = at - __builtin_amdgcn_readlane(sum - mine, l);
           break;
         }
-        seen = lane64(sum, 63);
+        seen = __builtin_amdgcn_readlane(sum, 63);
       }
       blocks = key_blocks(units, seq.length);
       key0 = a.shared;
     }
-    const int which = (int)(nth / blocks), block0 = (int)(nth - (long long)which * blocks);
+    const int which = nth / blocks, block0 = nth - which * blocks;
     const int row_block = which / c.heads, head = which - row_block * c.heads;
-    const int here = (int)min((long long)(blocks - block0), end - at);
+    const int here = min(blocks - block0, end - at);
     at += here;
     const Rows32 rows{32 * row_block, seq.rows * group, seq.row0, seq.place0()};
     // places of the rows: their own, and the least and greatest of them (past the shared keys: the last of these)

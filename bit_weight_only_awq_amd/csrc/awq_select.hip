@@ -21,8 +21,6 @@
 namespace awq {
 namespace {
 
-constexpr int kPages = 64;  // pages of a wave of the first kernel
-
 // A score as a number whose unsigned order is the scores' order.
 __device__ __forceinline__ uint64_t ordered(double v) {
   if (v != v) return 0;
@@ -47,79 +45,117 @@ __device__ __forceinline__ Span span_of(const SelectArgs& a, const SeqArgs& s, i
   return Span{place, have, a.first, have > a.count ? have - a.recent : a.first};
 }
 
-// Scores of kPages pages of one token and key head: L lanes per row of bounds.
+// Scores of 16 ROWS pages of one token and key head per wave: L lanes per row of bounds.
+template <int D>
+struct Score {
+  static constexpr int CHUNKS = D / 4, L = CHUNKS <= 16 ? 16 : CHUNKS <= 32 ? 32 : 64, ROWS = 64 / L, PAGES = 16 * ROWS;
+};
+
 template <int D>
 __global__ __launch_bounds__(256) void score_kernel(SelectArgs a, CacheArgs c, SeqArgs s, uint64_t* __restrict__ keys) {
-  constexpr int CHUNKS = D / 4, L = CHUNKS <= 16 ? 16 : CHUNKS <= 32 ? 32 : 64, ROWS = 64 / L, STEPS = kPages / (16 * ROWS);
+  using P = Score<D>;
+  constexpr int L = P::L;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = blockIdx.x / c.heads, head = blockIdx.x % c.heads;
   Sequence q;
   const Span span = span_of(a, s, c.shift, t, q);
-  const int p0 = span.from + (int)(blockIdx.y * 4 + wave) * kPages;
+  const int p0 = span.from + (int)(blockIdx.y * 4 + wave) * P::PAGES;
   if (p0 >= span.to) return;
   const int chunk = lane & (L - 1), row = lane / L;
-  const bool high = chunk >= D / 8, live = chunk < CHUNKS;
+  const bool high = chunk >= D / 8, live = chunk < P::CHUNKS;
   const int group = a.q_heads / c.heads, channel = 8 * (high ? chunk - D / 8 : chunk);
+  // the pages' numbers, one per lane, while the queries arrive
+  const int* table = s.tables + (int64_t)q.index * s.width;
+  const int number = page_number(c, table[min(p0 + min(lane, P::PAGES - 1), span.to - 1)]);
   double w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = 0.0;
-  if (live) {
-    const _Float16* at = a.q + t * a.ldq + (int64_t)head * group * D + channel;
-    for (int g = 0; g < group; ++g) {
-      const half8_t v = *reinterpret_cast<const half8_t*>(at + (int64_t)g * D);
+  {
+    const _Float16* at = a.q + t * a.ldq + (int64_t)head * group * D + (live ? channel : 0);
+    for (int g0 = 0; g0 < group; g0 += 4) {
+      half8_t v[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float f = v[i];
-        w[i] += (double)(high ? (f > 0.0f ? f : f != f ? f : 0.0f) : (f < 0.0f ? f : 0.0f));
-      }
+      for (int g = 0; g < 4; ++g) v[g] = *reinterpret_cast<const half8_t*>(at + (int64_t)min(g0 + g, group - 1) * D);
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f = v[g][i], side = high ? (f < 0.0f ? 0.0f : f) : (f > 0.0f ? 0.0f : f);
+          w[i] += (double)(live && g0 + g < group ? side : 0.0f);
+        }
     }
   }
   // channels that no head has on this side add 0, whatever the bound (infinities among them)
   u32x4 used;
 #pragma unroll
   for (int i = 0; i < 4; ++i) used[i] = (w[2 * i] != 0.0 ? 0xFFFFu : 0u) | (w[2 * i + 1] != 0.0 ? 0xFFFF0000u : 0u);
-  const int* table = s.tables + (int64_t)q.index * s.width;
   uint64_t* out = keys + ((int64_t)t * c.heads + head) * s.width;
-#pragma unroll 1
-  for (int step = 0; step < STEPS; ++step) {
-    double sum[16];
+  u32x4 raw[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int page = p0 + (step * 16 + j) * ROWS + row;
-      u32x4 raw = u32x4(0u);
-      if (live && page < span.to)
-        raw = *reinterpret_cast<const u32x4*>(
-            c.bounds + ((int64_t)page_number(c, table[page]) * c.heads + head) * 2 * D + 8 * chunk);
-      const half8_t v = as_half8(raw & used);
-      sum[j] = 0.0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[j] = __builtin_fma(w[i], (double)(float)v[i], sum[j]);
-    }
-    // the lanes' sums: at each exchange half of the pages go to the other lane, then the rest of the lanes add up
-#pragma unroll
-    for (int h = 8; h >= 1; h >>= 1) {
-      const bool upper = (lane & h) != 0;
-#pragma unroll
-      for (int j = 0; j < h; ++j) {
-        const double keep = upper ? sum[j + h] : sum[j], give = upper ? sum[j] : sum[j + h];
-        sum[j] = keep + swap_lanes(give, h);
-      }
-    }
-    double total = sum[0];
-#pragma unroll
-    for (int m = 16; m < L; m <<= 1) total += swap_lanes(total, m);
-    const int page = p0 + (step * 16 + (lane & 15)) * ROWS + row;
-    if (chunk < 16 && page < span.to) out[page - span.from] = ordered(total);
+  for (int j = 0; j < 16; ++j) {
+    const int64_t page = __shfl(number, j * P::ROWS + row);
+    raw[j] = *reinterpret_cast<const u32x4*>(c.bounds + (page * c.heads + head) * 2 * D + (live ? 8 * chunk : 0));
   }
+  double sum[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const half8_t v = as_half8(raw[j] & used);
+    sum[j] = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[j] = __builtin_fma(w[i], (double)(float)v[i], sum[j]);
+  }
+  // the lanes' sums: at each exchange half of the pages go to the other lane, then the rest of the lanes add up
+#pragma unroll
+  for (int h = 8; h >= 1; h >>= 1) {
+    const bool upper = (lane & h) != 0;
+#pragma unroll
+    for (int j = 0; j < h; ++j) {
+      const double keep = upper ? sum[j + h] : sum[j], give = upper ? sum[j] : sum[j + h];
+      sum[j] = keep + swap_lanes(give, h);
+    }
+  }
+  double total = sum[0];
+#pragma unroll
+  for (int m = 16; m < L; m <<= 1) total += swap_lanes(total, m);
+  const int page = p0 + (lane & 15) * P::ROWS + row;
+  if (chunk < 16 && page < span.to) out[page - span.from] = ordered(total);
 }
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kKept = 8;  // scores that a thread holds at a time: numbers tid, tid + 1024, ... of 8192
+
+// The place of each flagged score among all flagged ones before it, `placed` so far.
+struct Places {
+  unsigned at[kKept];
+};
+__device__ __forceinline__ Places places_of(const bool (&flag)[kKept], unsigned* part, unsigned& placed) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  Places p;
+#pragma unroll
+  for (int k = 0; k < kKept; ++k) {
+    const unsigned long long all = __ballot(flag[k]);
+    p.at[k] = __popcll(all & ((1ull << lane) - 1));
+    if (lane == 0) part[k * kWaves + wave] = __popcll(all);
+  }
+  __syncthreads();
+  if (wave == 0) {  // (128 counts, two per lane)
+    static_assert(kKept * kWaves == 128, "two counts per lane");
+    const unsigned x = part[2 * lane], y = part[2 * lane + 1], upto = prefix_sum((int)(x + y));
+    part[2 * lane] = upto - x - y;
+    part[2 * lane + 1] = upto - y;
+    if (lane == 63) part[128] = upto;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kKept; ++k) p.at[k] += placed + part[k * kWaves + wave];
+  placed += part[128];
+  __syncthreads();
+  return p;
+}
 
 __global__ __launch_bounds__(kThreads) void choose_kernel(SelectArgs a, CacheArgs c, SeqArgs s,
                                                           const uint64_t* __restrict__ keys) {
-  __shared__ unsigned count[256];
-  __shared__ unsigned part[kThreads / 64][2];
-  __shared__ uint64_t bits[kThreads / 64];
-  __shared__ unsigned found[2];
+  __shared__ unsigned count[256], part[130], found[3];
+  __shared__ uint64_t bits[kWaves];
   const int t = blockIdx.x / c.heads, head = blockIdx.x % c.heads, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   Sequence q;
   const Span span = span_of(a, s, c.shift, t, q);
@@ -129,89 +165,105 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectArgs a, CacheArg
     for (int i = tid; i < a.count; i += kThreads) out[i] = i < span.have ? i : -1;
     return;
   }
+  for (int i = tid; i < a.first; i += kThreads) out[i] = i;
+  for (int i = tid; i < a.recent; i += kThreads) out[a.count - a.recent + i] = span.to + i;
   const uint64_t* in = keys + ((int64_t)t * c.heads + head) * s.width;
-  const int n = span.to - span.from;
+  const int n = span.to - span.from, rounds = (n + kKept * kThreads - 1) / (kKept * kThreads);
   int wanted = a.count - a.first - a.recent;  // 0 <= wanted < n
+  if (wanted == 0) return;
+
+  uint64_t kept[kKept];
+  auto read = [&](int round) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+      const int i = (round * kKept + k) * kThreads + tid;
+      kept[k] = i < n ? in[i] : 0;
+    }
+  };
+  auto number = [&](int round, int k) __attribute__((always_inline)) { return (round * kKept + k) * kThreads + tid; };
 
   // the highest bit in which the scores differ
-  uint64_t differ = 0;
   const uint64_t one = in[0];
-  for (int i = tid; i < n; i += kThreads) differ |= in[i] ^ one;
+  uint64_t differ = 0;
+  for (int r = 0; r < rounds; ++r) {
+    read(r);
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) differ |= number(r, k) < n ? kept[k] ^ one : 0;
+  }
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
     const uint32_t lo = __shfl_xor((int)(uint32_t)differ, m), hi = __shfl_xor((int)(uint32_t)(differ >> 32), m);
     differ |= (uint64_t)hi << 32 | lo;
   }
   if (lane == 0) bits[wave] = differ;
+  if (tid < 256) count[tid] = 0;
   __syncthreads();
   differ = 0;
-  for (int w = 0; w < kThreads / 64; ++w) differ |= bits[w];
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) differ |= bits[w];
   const int top = differ ? 64 - __builtin_clzll(differ) : 0;  // bits 0 .. top - 1 differ
-  // the wanted-th largest: its bits from `top` down, 8 at a time
+  // the wanted-th largest: its bits from `top` down, 8 at a time, until no more scores share those found than are
+  // wanted of them
   uint64_t edge = top < 64 ? one >> top << top : 0;
-  for (int shift = top; shift > 0 && wanted > 0;) {
-    const int next = shift > 8 ? shift - 8 : 0, width = shift - next;
-    for (int i = tid; i < 256; i += kThreads) count[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-      const uint64_t k = in[i];
-      if (shift == 64 || k >> shift == edge >> shift) atomicAdd(&count[(k >> next) & ((1u << width) - 1)], 1u);
+  bool ties = true;
+  for (int shift = top; shift > 0 && ties;) {
+    const int next = shift > 8 ? shift - 8 : 0;
+    for (int r = 0; r < rounds; ++r) {
+      if (rounds > 1) read(r);
+#pragma unroll
+      for (int k = 0; k < kKept; ++k)
+        if (number(r, k) < n && (shift == 64 || kept[k] >> shift == edge >> shift))
+          atomicAdd(&count[(kept[k] >> next) & 255 & ((1u << (shift - next)) - 1)], 1u);
     }
     __syncthreads();
-    // the digit whose keys hold the wanted-th: lane l sums digits 255 - 4 l .. 252 - 4 l
+    // the digit whose scores hold the wanted-th: lane l sums digits 255 - 4 l .. 252 - 4 l
     if (wave == 0) {
       unsigned c4[4], sum = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum += c4[i] = count[255 - 4 * lane - i];
       const unsigned upto = prefix_sum((int)sum);
       unsigned above = upto - sum;
-      if (above < (unsigned)wanted && upto >= (unsigned)wanted) {
+      bool done = above >= (unsigned)wanted || upto < (unsigned)wanted;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (above < (unsigned)wanted && above + c4[i] >= (unsigned)wanted) {
-            found[0] = 255 - 4 * lane - i;
-            found[1] = above;
-            break;
-          }
-          above += c4[i];
+      for (int i = 0; i < 4; ++i) {
+        if (!done && above + c4[i] >= (unsigned)wanted) {
+          found[0] = 255 - 4 * lane - i;
+          found[1] = above;
+          found[2] = c4[i];
+          done = true;
         }
+        above += c4[i];
       }
     }
     __syncthreads();
     edge |= (uint64_t)found[0] << next;
     wanted -= (int)found[1];
+    ties = found[2] != (unsigned)wanted;
     shift = next;
+    if (tid < 256) count[tid] = 0;
     __syncthreads();
   }
-  // in order: the pages above the edge, and the first `wanted` of those at it
-  const bool none = a.count == a.first + a.recent;
-  for (int i = tid; i < a.first; i += kThreads) out[i] = i;
-  for (int i = tid; i < a.recent; i += kThreads) out[a.count - a.recent + i] = span.to + i;
-  if (none) return;
-  unsigned placed = a.first, ties = 0;
-  for (int i0 = 0; i0 < n; i0 += kThreads) {
-    const int i = i0 + tid;
-    const uint64_t k = i < n ? in[i] : 0;
-    const bool tie = i < n && k == edge;
-    const unsigned long long below = (1ull << lane) - 1, tied = __ballot(tie);
-    if (lane == 0) part[wave][0] = __popcll(tied);
-    __syncthreads();
-    unsigned before = ties;
-    for (int w = 0; w < kThreads / 64; ++w) {
-      before += w < wave ? part[w][0] : 0;
-      ties += part[w][0];
+  // in order: the pages at or above the edge; with ties, those above it and the first `wanted` of those at it
+  unsigned placed = a.first, tied = 0;
+  for (int r = 0; r < rounds; ++r) {
+    if (rounds > 1) read(r);
+    bool take[kKept];
+    if (ties) {
+      bool equal[kKept];
+#pragma unroll
+      for (int k = 0; k < kKept; ++k) equal[k] = number(r, k) < n && kept[k] == edge;
+      const Places p = places_of(equal, part, tied);
+#pragma unroll
+      for (int k = 0; k < kKept; ++k)
+        take[k] = number(r, k) < n && (kept[k] > edge || (equal[k] && p.at[k] < (unsigned)wanted));
+    } else {
+#pragma unroll
+      for (int k = 0; k < kKept; ++k) take[k] = number(r, k) < n && kept[k] >= edge;
     }
-    const bool take = i < n && (k > edge || (tie && before + __popcll(tied & below) < (unsigned)wanted));
-    const unsigned long long taken = __ballot(take);
-    if (lane == 0) part[wave][1] = __popcll(taken);
-    __syncthreads();
-    unsigned at = placed + __popcll(taken & below);
-    for (int w = 0; w < kThreads / 64; ++w) {
-      at += w < wave ? part[w][1] : 0;
-      placed += part[w][1];
-    }
-    if (take) out[at] = span.from + i;
-    __syncthreads();
+    const Places p = places_of(take, part, placed);
+#pragma unroll
+    for (int k = 0; k < kKept; ++k)
+      if (take[k]) out[p.at[k]] = span.from + number(r, k);
   }
 }
 
@@ -224,8 +276,10 @@ size_t select_workspace_bytes(int T, int kv_heads, int width, int count) {
 hipError_t launch_select(const SelectArgs& a, const CacheArgs& c, const SeqArgs& s, void* workspace, hipStream_t stream) {
   uint64_t* keys = static_cast<uint64_t*>(workspace);
   if (s.width > a.count) {  // (otherwise no sequence has more pages than are wanted)
-    const dim3 grid(s.T * c.heads, (s.width + 4 * kPages - 1) / (4 * kPages));
-#define AWQ_SCORE(D) hipLaunchKernelGGL((score_kernel<D>), grid, dim3(256), 0, stream, a, c, s, keys)
+#define AWQ_SCORE(D)                                                                                            \
+  hipLaunchKernelGGL((score_kernel<D>),                                                                         \
+                     dim3(s.T * c.heads, (s.width + 4 * Score<D>::PAGES - 1) / (4 * Score<D>::PAGES)), dim3(256), 0, \
+                     stream, a, c, s, keys)
     if (c.dim == 64) AWQ_SCORE(64);
     else if (c.dim == 96) AWQ_SCORE(96);
     else if (c.dim == 128) AWQ_SCORE(128);
