@@ -18,12 +18,13 @@ struct JoinArgs {
   int own_slices, shared_slices;
 };
 
-// A wave per row (token and query head): 64 parts at a time, a lane holding each
+// Where waves made the parts of the own keys: a wave per row (token and query
+// head), 64 parts at a time, a lane holding each
 // part's maximum and sum, then LANES lanes their share of the channels and 64 /
 // LANES groups of lanes every such part.
 template <int D>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, SeqArgs s, JoinArgs j, Partials p) {
-  constexpr int LANES = D <= 64 ? 16 : D <= 128 ? 32 : 64, GROUPS = 64 / LANES, AHEAD = 4;
+  constexpr int LANES = D <= 64 ? 16 : D <= 128 ? 32 : 64, GROUPS = 64 / LANES, AHEAD = 8;
   const int lane = threadIdx.x & 63;
   const int row = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
   const int t = row / a.q_heads, at = row - t * a.q_heads;
@@ -34,7 +35,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
   Sequence seq{0, 0, 0, 0};
   int first = 0;
   Units n{0, 0, 1};
-  if (j.own_few && !a.list) {
+  if (!a.list) {
     const int shared = j.units.shared ? row_blocks(j.units, all_rows(s, 0).rows) * c.heads * ((j.units.shared_keys + 31) >> 5) : 0;
     int seen = shared;
     for (int b0 = 0; b0 < s.B; b0 += 64) {
@@ -51,7 +52,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
     n = share_units(j.units, seen, shared);
   } else {
     seq = sequence_of(s, c.shift, t);
-    if (a.list) n = share_units(j.units, s.T * c.heads * row_blocks(j.units, 1) * list_blocks(j.units, a.count), 0);
+    n = share_units(j.units, s.T * c.heads * row_blocks(j.units, 1) * list_blocks(j.units, a.count), 0);
   }
   if (seq.rows == 0) return;  // a row of no sequence stays as it is
 
@@ -60,7 +61,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
   int own_unit = 0, own_wave = 0, own_waves = 0, own_row = 0, shared_unit = 0, shared_wave = 0, shared_waves = 0,
       shared_row = 0, slice0 = 0, slices = 0;
   const bool placed = t - seq.row0 + seq.place0() >= 0;
-  if (j.own_few) {
+  {
     const int blocks = a.list ? list_blocks(j.units, a.count) : key_blocks(j.units, seq.length);
     const int r = a.list ? g : (t - seq.row0) * group + g;
     const int before = a.list ? t * row_blocks(j.units, 1) : 0;
@@ -75,8 +76,6 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
     } else {
       slice0 = j.own_slices;
     }
-  } else {
-    slices = j.own_slices;
   }
   if (j.units.shared) {
     const int blocks = (j.units.shared_keys + 31) >> 5, r = (t - all_rows(s, 0).row0) * group + g;
@@ -155,16 +154,63 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
   *reinterpret_cast<half4_t*>(a.y + t * a.ldy + (int64_t)at * D + channel) = v;
 }
 
+// The same where all parts are slices (workgroups of 128 rows made them): LANES
+// lanes per row, nothing to look up but whether the row is of a sequence at all.
+template <int D>
+__global__ __launch_bounds__(256) void join_slices_kernel(AttendArgs a, SeqArgs s, int slices, Partials p) {
+  constexpr int LANES = D <= 64 ? 16 : D <= 128 ? 32 : 64, AHEAD = 4;
+  const int row = (int)(blockIdx.x * (256 / LANES) + threadIdx.x / LANES), channel = 4 * (threadIdx.x & (LANES - 1));
+  const int t = row / a.q_heads, at = row - t * a.q_heads;
+  if (t < s.offsets[0] || t >= min(s.offsets[s.B], s.T) || channel >= D) return;
+  float4_t sums = float4_t(0.0f);
+  float top = -INFINITY, total = 0.0f;
+  bool placed = true;
+  for (int i0 = 0; i0 < slices; i0 += AHEAD) {
+    float2 stat[AHEAD];
+    float4_t part[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {  // (past the last slice: the last again, counted as nothing)
+      const int64_t from = min(i0 + i, slices - 1) * p.rows + row;
+      stat[i] = p.stat[from];
+      part[i] = *reinterpret_cast<const float4_t*>(p.sums + from * D + channel);
+    }
+    float m = top;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      placed = placed && stat[i].y != kNoPlace;
+      m = fmaxf(m, stat[i].x);
+    }
+    const float carry = top == m ? 1.0f : __builtin_amdgcn_exp2f(top - m);
+    total *= carry;
+    sums *= carry;
+    top = m;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (i0 + i >= slices || (stat[i].x == -INFINITY && stat[i].y == 0.0f)) continue;
+      const float share = stat[i].x == m ? 1.0f : __builtin_amdgcn_exp2f(stat[i].x - m);
+      total += stat[i].y * share;
+      sums += part[i] * share;
+    }
+  }
+  const bool none = total == 0.0f || !placed;
+  const float by = 1.0f / total;
+  half4_t v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = (_Float16)(none ? 0.0f : sums[i] * by);
+  *reinterpret_cast<half4_t*>(a.y + t * a.ldy + (int64_t)at * D + channel) = v;
+}
+
 constexpr int kUnits = 256;  // compute units
 
 // The keys' splits over which `tiles` workgroups take the least time, in rounds of two per compute unit (one where
-// a head is 256 wide), a stage being the unit and what a workgroup does besides costing `extra` of them.
+// a head is 256 wide), a stage being the unit, what a workgroup does besides costing `extra` of them, and writing and
+// reading the parts of a tile 0.0085 (128 rows of fp32 sums, there and back).
 int splits_of(int64_t tiles, int64_t stages, int slots, double extra) {
   int best = 1;
   double least = 1e300;
   for (int n = 1; n <= 64 && n * 2 <= stages + 1 && (n == 1 || tiles * n <= 16 * slots); ++n) {
     const double rounds = (double)((tiles * n + slots - 1) / slots);
-    const double time = rounds * ((double)((stages + n - 1) / n) + extra) + 0.3 * n;
+    const double time = rounds * ((double)((stages + n - 1) / n) + extra) + (n > 1 ? 0.0085 * n * tiles : 0.0);
     if (time < least) {
       least = time;
       best = n;
@@ -196,7 +242,12 @@ template <int D>
 void launch_join(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const JoinArgs& j, const Partials& p,
                  hipStream_t stream) {
   const int64_t rows = (int64_t)s.T * a.q_heads;
-  hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, c, s, j, p);
+  constexpr int ROWS = 256 / (D <= 64 ? 16 : D <= 128 ? 32 : 64);  // of a workgroup
+  if (j.own_few)
+    hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, c, s, j, p);
+  else
+    hipLaunchKernelGGL((join_slices_kernel<D>), dim3((unsigned)((rows + ROWS - 1) / ROWS)), dim3(256), 0, stream, a, s,
+                       j.own_slices + j.shared_slices, p);
 }
 
 }  // namespace

@@ -137,6 +137,8 @@ __device__ __forceinline__ void read_queries(Queries<D>& q, const AttendArgs& a,
   }
 }
 
+constexpr float kNoPlace = -1.0f;  // a sum that no row can have
+
 // Results of a wave's 32 rows: to y (`slice` below 0), or unfinished to a slice of the rows, or to `wave_stat` and
 // `wave_sums` of 32 rows.
 template <int D>
@@ -163,7 +165,9 @@ __device__ __forceinline__ void write_rows(const Gathered<D>& g, float c, const 
     return;
   }
   const int64_t to = wave_stat ? lane & 31 : (int64_t)slice * p.rows + t * a.q_heads + at;
-  if (half == 0) (wave_stat ? wave_stat : p.stat)[to] = float2{g.top * c, sum};
+  // (a row without a place is marked: shared keys, which it does not have, must not count for it)
+  if (half == 0)
+    (wave_stat ? wave_stat : p.stat)[to] = r.place0 + token < 0 ? float2{0.0f, kNoPlace} : float2{g.top * c, sum};
   float* sums = (wave_stat ? wave_sums : p.sums) + to * D + 4 * half;
 #pragma unroll
   for (int b = 0; b < D / 32; ++b)

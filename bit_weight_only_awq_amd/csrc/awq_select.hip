@@ -34,6 +34,18 @@ __device__ __forceinline__ double swap_lanes(double v, int mask) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+// At each exchange half of a lane's sums go to the lane H away, which has its share of them, and as many come back.
+template <int H>
+__device__ __forceinline__ void halve(double (&sum)[16], int lane) {
+  const bool upper = (lane & H) != 0;
+#pragma unroll
+  for (int j = 0; j < H; ++j) {
+    const double keep = upper ? sum[j + H] : sum[j], give = upper ? sum[j] : sum[j + H];
+    sum[j] = keep + swap_lanes(give, H);
+  }
+  if constexpr (H > 1) halve<H / 2>(sum, lane);
+}
+
 // The pages that are scored: first .. have - recent - 1 of a row whose sequence has `have` pages up to its place.
 struct Span {
   int place, have, from, to;
@@ -52,20 +64,23 @@ struct Score {
 };
 
 template <int D>
-__global__ __launch_bounds__(256) void score_kernel(SelectArgs a, CacheArgs c, SeqArgs s, uint64_t* __restrict__ keys) {
+__global__ __launch_bounds__(256) void score_kernel(SelectArgs a, CacheArgs c, SeqArgs s, int batches,
+                                                    uint64_t* __restrict__ keys) {
   using P = Score<D>;
   constexpr int L = P::L;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = blockIdx.x / c.heads, head = blockIdx.x % c.heads;
   Sequence q;
   const Span span = span_of(a, s, c.shift, t, q);
-  const int p0 = span.from + (int)(blockIdx.y * 4 + wave) * P::PAGES;
+  int p0 = span.from + (int)(blockIdx.y * 4 + wave) * batches * P::PAGES;
   if (p0 >= span.to) return;
+  const int p1 = min(span.to, p0 + batches * P::PAGES);
   const int chunk = lane & (L - 1), row = lane / L;
   const bool high = chunk >= D / 8, live = chunk < P::CHUNKS;
   const int group = a.q_heads / c.heads, channel = 8 * (high ? chunk - D / 8 : chunk);
   // the pages' numbers, one per lane, while the queries arrive
   const int* table = s.tables + (int64_t)q.index * s.width;
-  const int number = page_number(c, table[min(p0 + min(lane, P::PAGES - 1), span.to - 1)]);
+  auto number_of = [&](int from) { return page_number(c, table[min(from + min(lane, P::PAGES - 1), p1 - 1)]); };
+  int number = number_of(p0);
   double w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = 0.0;
@@ -76,12 +91,19 @@ __global__ __launch_bounds__(256) void score_kernel(SelectArgs a, CacheArgs c, S
 #pragma unroll
       for (int g = 0; g < 4; ++g) v[g] = *reinterpret_cast<const half8_t*>(at + (int64_t)min(g0 + g, group - 1) * D);
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+      for (int g = 0; g < 4; ++g) {
+        // (the sign picks the side: halves with the other sign become 0)
+        const uint32_t mine = high ? 0xFFFFFFFFu : 0u, in = live && g0 + g < group ? 0xFFFFFFFFu : 0u;
+        const u32x4 bits = __builtin_bit_cast(u32x4, v[g]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float f = v[g][i], side = high ? (f < 0.0f ? 0.0f : f) : (f > 0.0f ? 0.0f : f);
-          w[i] += (double)(live && g0 + g < group ? side : 0.0f);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t pair = bits[i];
+          const uint32_t negative = ((int)pair < 0 ? 0xFFFF0000u : 0u) | (pair & 0x8000u ? 0xFFFFu : 0u);
+          const half2_t side = as_half2(pair & (negative ^ mine) & in);
+          w[2 * i] += (double)(float)side[0];
+          w[2 * i + 1] += (double)(float)side[1];
         }
+      }
     }
   }
   // channels that no head has on this side add 0, whatever the bound (infinities among them)
@@ -89,36 +111,34 @@ __global__ __launch_bounds__(256) void score_kernel(SelectArgs a, CacheArgs c, S
 #pragma unroll
   for (int i = 0; i < 4; ++i) used[i] = (w[2 * i] != 0.0 ? 0xFFFFu : 0u) | (w[2 * i + 1] != 0.0 ? 0xFFFF0000u : 0u);
   uint64_t* out = keys + ((int64_t)t * c.heads + head) * s.width;
-  u32x4 raw[16];
+#pragma unroll 1
+  for (; p0 < p1; p0 += P::PAGES) {
+    u32x4 raw[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const int64_t page = __shfl(number, j * P::ROWS + row);
-    raw[j] = *reinterpret_cast<const u32x4*>(c.bounds + (page * c.heads + head) * 2 * D + (live ? 8 * chunk : 0));
-  }
-  double sum[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const half8_t v = as_half8(raw[j] & used);
-    sum[j] = 0.0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum[j] = __builtin_fma(w[i], (double)(float)v[i], sum[j]);
-  }
-  // the lanes' sums: at each exchange half of the pages go to the other lane, then the rest of the lanes add up
-#pragma unroll
-  for (int h = 8; h >= 1; h >>= 1) {
-    const bool upper = (lane & h) != 0;
-#pragma unroll
-    for (int j = 0; j < h; ++j) {
-      const double keep = upper ? sum[j + h] : sum[j], give = upper ? sum[j] : sum[j + h];
-      sum[j] = keep + swap_lanes(give, h);
+    for (int j = 0; j < 16; ++j) {
+      const int64_t page = __shfl(number, j * P::ROWS + row);
+      raw[j] = *reinterpret_cast<const u32x4*>(c.bounds + (page * c.heads + head) * 2 * D + (live ? 8 * chunk : 0));
     }
-  }
-  double total = sum[0];
+    if (p0 + P::PAGES < p1) number = number_of(p0 + P::PAGES);
+    double sum[16];
 #pragma unroll
-  for (int m = 16; m < L; m <<= 1) total += swap_lanes(total, m);
-  const int page = p0 + (lane & 15) * P::ROWS + row;
-  if (chunk < 16 && page < span.to) out[page - span.from] = ordered(total);
+    for (int j = 0; j < 16; ++j) {
+      const half8_t v = as_half8(raw[j] & used);
+      sum[j] = 0.0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[j] = __builtin_fma(w[i], (double)(float)v[i], sum[j]);
+    }
+    // the lanes' sums, page by page, then those of the lanes 16 and 32 away
+    halve<8>(sum, lane);
+    double total = sum[0];
+#pragma unroll
+    for (int m = 16; m < L; m <<= 1) total += swap_lanes(total, m);
+    const int page = p0 + (lane & 15) * P::ROWS + row;
+    if (chunk < 16 && page < p1) out[page - span.from] = ordered(total);
+  }
 }
+
+constexpr int kScoreWaves = 4096;  // four per SIMD
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kKept = 8;  // scores that a thread holds at a time: numbers tid, tid + 1024, ... of 8192
@@ -267,6 +287,16 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectArgs a, CacheArg
   }
 }
 
+template <int D>
+void launch_score(const SelectArgs& a, const CacheArgs& c, const SeqArgs& s, uint64_t* keys, hipStream_t stream) {
+  constexpr int PAGES = Score<D>::PAGES;
+  // a wave's pages: one batch where that fills the chip, more where the queries' sums would be formed too often
+  const int64_t all = (int64_t)s.T * c.heads * ((s.width + PAGES - 1) / PAGES), want = all / kScoreWaves;
+  const int batches = want < 1 ? 1 : want > 8 ? 8 : (int)want, pages = 4 * batches * PAGES;
+  hipLaunchKernelGGL((score_kernel<D>), dim3(s.T * c.heads, (s.width + pages - 1) / pages), dim3(256), 0, stream, a, c, s,
+                     batches, keys);
+}
+
 }  // namespace
 
 size_t select_workspace_bytes(int T, int kv_heads, int width, int count) {
@@ -276,10 +306,7 @@ size_t select_workspace_bytes(int T, int kv_heads, int width, int count) {
 hipError_t launch_select(const SelectArgs& a, const CacheArgs& c, const SeqArgs& s, void* workspace, hipStream_t stream) {
   uint64_t* keys = static_cast<uint64_t*>(workspace);
   if (s.width > a.count) {  // (otherwise no sequence has more pages than are wanted)
-#define AWQ_SCORE(D)                                                                                            \
-  hipLaunchKernelGGL((score_kernel<D>),                                                                         \
-                     dim3(s.T * c.heads, (s.width + 4 * Score<D>::PAGES - 1) / (4 * Score<D>::PAGES)), dim3(256), 0, \
-                     stream, a, c, s, keys)
+#define AWQ_SCORE(D) launch_score<D>(a, c, s, keys, stream)
     if (c.dim == 64) AWQ_SCORE(64);
     else if (c.dim == 96) AWQ_SCORE(96);
     else if (c.dim == 128) AWQ_SCORE(128);
