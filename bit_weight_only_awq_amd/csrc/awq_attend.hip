@@ -200,7 +200,6 @@ __global__ __launch_bounds__(256) void join_slices_kernel(AttendArgs a, SeqArgs 
   *reinterpret_cast<half4_t*>(a.y + t * a.ldy + (int64_t)at * D + channel) = v;
 }
 
-constexpr int kUnits = 256;  // compute units
 
 // The keys' splits over which `tiles` workgroups take the least time, in rounds of two per compute unit (one where
 // a head is 256 wide), a stage being the unit, what a workgroup does besides costing `extra` of them, and writing and

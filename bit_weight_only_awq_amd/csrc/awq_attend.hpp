@@ -6,6 +6,8 @@
 
 namespace awq {
 
+constexpr int kUnits = 256;  // compute units
+
 // Rows of 32 and keys of 32 of one wave (few), rows of 128 and splits of the keys (many).
 struct AttendPlan {
   bool own_few;       // a sequence's own keys: a wave per 32 rows, or a workgroup per 128

@@ -210,6 +210,25 @@ __device__ __forceinline__ void read_values(const uint32_t (&from)[N], half8_t (
                                                 hi[b][3]});
 }
 
+// A lane's addresses in LDS: of its fragments of the keys (swizzling moves chunks within 16: the next 16 are 256 bytes
+// on) and of the values' 32 channels each, in a stage whose first byte is at `base`; another block or stage is an
+// offset in the instruction.
+template <int D>
+struct Addresses {
+  using T = Tile<D>;
+  static constexpr int KEYS = D < 128 ? D / 16 : 8, VALUES = D / 32 <= 4 ? D / 32 : 4;
+  uint32_t key[KEYS], value[VALUES];
+  __device__ __forceinline__ Addresses(uint32_t base, int lane) {
+    const int row = lane & 31, half = lane >> 5, swz = T::key_swizzle(row) ^ half;
+#pragma unroll
+    for (int j = 0; j < KEYS; ++j) key[j] = base + row * T::ROW + 16 * ((2 * j) ^ swz);
+    const int l = lane & 15, chunk = 2 * ((lane >> 4) & 1) + ((l & 3) >> 1), vswz = T::value_swizzle(l >> 2);
+#pragma unroll
+    for (int b = 0; b < VALUES; ++b)
+      value[b] = base + (4 * half + (l >> 2)) * T::ROW + 8 * (l & 1) + 16 * ((4 * b + chunk) ^ vswz);
+  }
+};
+
 // f(I), f(I + STEP), ... below END, with constants.
 template <int I, int END, int STEP, typename F>
 __device__ __forceinline__ void each(F f) {
@@ -219,26 +238,17 @@ __device__ __forceinline__ void each(F f) {
   }
 }
 
-// One block: keys and values of 32 tokens at LDS addresses `keys` and `values`.  `strange`: rows of the values that
-// hold values taken out by hide_strange; value_of(k): where row k of them is in the cache.
-template <int D, typename ValueOf>
-__device__ __forceinline__ void attend_block(const lds_char* keys, const lds_char* values, const Queries<D>& q, float c,
-                                             const Seen& seen, uint32_t strange, ValueOf value_of, Gathered<D>& g) {
+// One block of 32 tokens, whose keys are K and whose values V bytes behind the lane's addresses.  `strange`: rows of
+// the values that hold values taken out by hide_strange; value_of(k): where row k of them is in the cache.
+template <int D, int K, int V, typename ValueOf>
+__device__ __forceinline__ void attend_block(const Addresses<D>& at, const Queries<D>& q, float c, const Seen& seen,
+                                             uint32_t strange, ValueOf value_of, Gathered<D>& g) {
   using T = Tile<D>;
-  // (the lane's place is formed anew for each block: kept through the loop, the addresses would take 12 registers more)
-  int lane = __lane_id();
-  asm volatile("" : "+v"(lane));
-  const int row = lane & 31, half = lane >> 5;
+  const int lane = __lane_id(), row = lane & 31, half = lane >> 5;
   // scores, a few fragments of the keys at a time: the next are read while the matrix cores have these
   float16_t s = float16_t(0.0f);
   {
     constexpr int N = D == 96 ? 3 : 4;
-    const uint32_t at = (uint32_t)(uintptr_t)keys + row * T::ROW;
-    const int swz = T::key_swizzle(row) ^ half;
-    constexpr int ADDRESSES = D < 128 ? D / 16 : 8;  // (swizzling moves chunks within 16: the next 16 are 256 bytes on)
-    uint32_t from[ADDRESSES];
-#pragma unroll
-    for (int j = 0; j < ADDRESSES; ++j) from[j] = at + 16 * ((2 * j) ^ swz);
     auto part = [&](auto j0c) __attribute__((always_inline)) {
       constexpr int j0 = decltype(j0c)::value;
       half8_t k[N];
@@ -247,12 +257,12 @@ __device__ __forceinline__ void attend_block(const lds_char* keys, const lds_cha
         const uint32_t base = (uint32_t)(uintptr_t)q.at;
         const uint32_t queries[4] = {base, base + 1024, base + 2048, base + 3072};
         read_keys<1024 * j0, N>(queries, x);
-        read_keys<32 * (j0 / 8 * 8), N>(from + j0 % 8, k);
+        read_keys<K + 32 * (j0 / 8 * 8), N>(at.key + j0 % 8, k);
 #pragma unroll
         for (int j = 0; j < N; ++j) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[j], x[j], s, 0, 0, 0);
         asm volatile("" ::"v"(x[0]));
       } else {
-        read_keys<0, N>(from + j0, k);
+        read_keys<K, N>(at.key + j0, k);
 #pragma unroll
         for (int j = 0; j < N; ++j) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[j], q.part[j0 + j], s, 0, 0, 0);
       }
@@ -264,13 +274,8 @@ __device__ __forceinline__ void attend_block(const lds_char* keys, const lds_cha
   }
   // the values' first 16 keys, while the last scores are being made
   constexpr int N = D / 32 <= 4 ? D / 32 : 4, PARTS = D / 32 / N;
-  const int l = lane & 15, swz = T::value_swizzle(l >> 2), chunk = 2 * ((lane >> 4) & 1) + ((l & 3) >> 1);
-  uint32_t from[N];
-#pragma unroll
-  for (int b = 0; b < N; ++b)
-    from[b] = (uint32_t)(uintptr_t)values + (4 * half + (l >> 2)) * T::ROW + 8 * (l & 1) + 16 * ((4 * b + chunk) ^ swz);
   half8_t v[N];
-  read_values<0, T::ROW, N>(from, v);
+  read_values<V, T::ROW, N>(at.value, v);
   if (!seen.all) {
     const int limit0 = seen.limit0 - 4 * half, limit1 = seen.limit1 - 4 * half;
 #pragma unroll
@@ -301,7 +306,7 @@ __device__ __forceinline__ void attend_block(const lds_char* keys, const lds_cha
   g.sum += sum;
   each<0, 2 * PARTS, 1>([&](auto ic) __attribute__((always_inline)) {
     constexpr int i = decltype(ic)::value, step = i / PARTS, part = i % PARTS;
-    if constexpr (i > 0) read_values<16 * step * T::ROW + 256 * part, T::ROW, N>(from, v);
+    if constexpr (i > 0) read_values<V + 16 * step * T::ROW + 256 * part, T::ROW, N>(at.value, v);
 #pragma unroll
     for (int b = 0; b < N; ++b)
       g.sums[part * N + b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[b], p[step], g.sums[part * N + b], 0, 0, 0);

@@ -21,6 +21,7 @@ constexpr int kTile = 128;  // rows of a workgroup
 // `shared_tiles` workgroup rows of the shared keys first, then the sequences' own.
 struct TileArgs {
   int group, shared_tiles, shared_splits, own_tiles, own_splits, own_slice, shared_slice;
+  int descending;  // of the own tiles (per key head and split), those that come first, from the last rows up
 };
 
 template <int D>
@@ -30,14 +31,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tiles_kernel(Att
   constexpr int KEYS = D == 256 ? 32 : 64;                  // of a stage
   constexpr int LOADS = KEYS / 16 * T::LOADS / 4;           // of a wave and stage, of keys and of values each
   constexpr int SLOT = KEYS * T::ROW;
-  __shared__ __attribute__((aligned(1024))) char k0[SLOT], v0[SLOT], k1[SLOT], v1[SLOT];
+  __shared__ __attribute__((aligned(1024))) char ring[4 * SLOT];  // keys, then values, of two stages
   __shared__ __attribute__((aligned(1024))) char queries[Queries<D>::BYTES ? 4 * Queries<D>::BYTES : 16];
   __shared__ uint32_t strange[2][2];  // of a stage and the next
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = x.group;
   const float scale = a.scale * kLog2E;
 
-  // the tile: key heads next to each other (one XCD keeps meeting the same), the last rows, which have the most
-  // keys, first
+  // the tile: key heads next to each other (one XCD keeps meeting the same); the last rows, which have the most keys,
+  // first, and where there are at most two workgroups per compute unit the second ones the other way around, so that
+  // each unit gets one with many keys and one with few
   const int head = blockIdx.x % c.heads;
   int nth = blockIdx.x / c.heads;
   const bool shared = nth < x.shared_tiles * x.shared_splits;
@@ -58,7 +60,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tiles_kernel(Att
     split = nth / x.own_tiles;
     splits = x.own_splits;
     slice = x.own_slice < 0 ? -1 : x.own_slice + split;
-    const int wanted = x.own_tiles - 1 - (nth - split * x.own_tiles);
+    const int turn = nth - split * x.own_tiles, wanted = turn < x.descending ? x.own_tiles - 1 - turn : turn - x.descending;
     int seen = 0;
     bool found = false;
     for (int b0 = 0; b0 < s.B; b0 += 64) {
@@ -103,8 +105,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tiles_kernel(Att
   static_assert(T::LOADS % LOADS == 0, "a wave's loads are of one group of keys");
   const int sixteen = wave / PER, part = wave % PER;
   const Sources<D> kept(lane, part * LOADS);
+  const Addresses<D> places((uint32_t)(uintptr_t)(lds_char*)ring, lane);
   Entries pages{s.tables + (int64_t)seq.index * s.width, nullptr, 0, s.width, 0, 0, 0};
-  auto load = [&](int stage, lds_char* to_keys, lds_char* to_values) __attribute__((always_inline)) {
+  auto load = [&](int stage, lds_char* slot) __attribute__((always_inline)) {
     const int key = key0 + KEYS * stage;
     if (stage == from || ((key + KEYS - 16) >> c.shift) - pages.first >= 64) pages.read(c, key >> c.shift);
     const Keys16 source = keys16(pages, c, head, key + 16 * sixteen);
@@ -112,23 +115,23 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tiles_kernel(Att
     const char* v = reinterpret_cast<const char*>(c.v + source.at * D);
     Sources<D> from_lane = kept;
     asm volatile("" : "+v"(from_lane.keys[0]), "+v"(from_lane.values[0]));  // (each load's is formed here, not kept)
-    const int at = 16 * sixteen * T::ROW + 1024 * part * LOADS;
+    lds_char* to = slot + 16 * sixteen * T::ROW + 1024 * part * LOADS;
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) load_to_lds(k + from_lane.key(i), to_keys + at + 1024 * i);
+    for (int i = 0; i < LOADS; ++i) load_to_lds(k + from_lane.key(i), to + 1024 * i);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) load_to_lds(v + from_lane.value(i), to_values + at + 1024 * i);
+    for (int i = 0; i < LOADS; ++i) load_to_lds(v + from_lane.value(i), to + SLOT + 1024 * i);
   };
-  auto step = [&](int stage, lds_char* ks, lds_char* vs, lds_char* next_keys, lds_char* next_values)
-                  __attribute__((always_inline)) {
+  auto step = [&](int stage, auto parity) __attribute__((always_inline)) {
+    constexpr int HERE = 2 * SLOT * decltype(parity)::value, NEXT = 2 * SLOT - HERE;
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (stage + 1 < to) load(stage + 1, next_keys, next_values);
+    if (stage + 1 < to) load(stage + 1, (lds_char*)ring + NEXT);
     // past the least place of the workgroup's rows some values are not to be seen by some row
     const int key = key0 + KEYS * stage;
     const bool ragged = key + KEYS - 1 > tile_least;
     if (ragged) {
-      const uint64_t met = hide_strange<D, KEYS>(vs, threadIdx.x, 256, [&](int h, int& behind, int& upto) {
+      const uint64_t met = hide_strange<D, KEYS>((lds_char*)ring + HERE + SLOT, threadIdx.x, 256, [&](int h, int& behind, int& upto) {
         behind = tile_least - key - 16 * h;
         upto = tile_most - key - 16 * h;
       });
@@ -139,22 +142,22 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tiles_kernel(Att
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     }
-#pragma unroll
-    for (int b = 0; b < KEYS / 32; ++b) {
+    each<0, KEYS / 32, 1>([&](auto bc) __attribute__((always_inline)) {
+      constexpr int b = decltype(bc)::value;
       const int first = key + 32 * b;
-      if (first > most) continue;
+      if (first > most) return;
       const Seen seen{place - first, place - first - 16, least - first >= 31};
       const uint32_t odd = ragged ? __builtin_amdgcn_readfirstlane(strange[stage & 1][b]) : 0;
-      attend_block<D>(ks + 32 * b * T::ROW, vs + 32 * b * T::ROW, q, scale, seen, odd, [&](int k) {
+      attend_block<D, HERE + 32 * b * T::ROW, HERE + SLOT + 32 * b * T::ROW>(places, q, scale, seen, odd, [&](int k) {
         const int64_t number = page_number(c, pages.table[(first + k) >> c.shift]);
         return c.v + (((number * c.heads + head) << c.shift) + ((first + k) & ((1 << c.shift) - 1))) * D;
       }, g);
-    }
+    });
   };
-  if (from < to) load(from, (lds_char*)k0, (lds_char*)v0);
+  if (from < to) load(from, (lds_char*)ring);
   for (int stage = from; stage < to; stage += 2) {
-    step(stage, (lds_char*)k0, (lds_char*)v0, (lds_char*)k1, (lds_char*)v1);
-    if (stage + 1 < to) step(stage + 1, (lds_char*)k1, (lds_char*)v1, (lds_char*)k0, (lds_char*)v0);
+    step(stage, std::integral_constant<int, 0>{});
+    if (stage + 1 < to) step(stage + 1, std::integral_constant<int, 1>{});
   }
   if (live) write_rows(g, scale, a, p, rows, group, head, slice, nullptr, nullptr);
 }
@@ -172,7 +175,7 @@ hipError_t launch_attend_tiles(const AttendArgs& a, const CacheArgs& c, const Se
                                const Partials& p, hipStream_t stream) {
   const int group = a.q_heads / c.heads;
   const int64_t rows = (int64_t)s.T * group, most = rows / kTile + s.B;  // (a ragged tile per sequence at most)
-  TileArgs x{group, 0, 1, 0, 1, plan.own_slices() > 0 ? 0 : -1, plan.own_slices()};
+  TileArgs x{group, 0, 1, 0, 1, plan.own_slices() > 0 ? 0 : -1, plan.own_slices(), 0};
   if (plan.prefix == 2) {
     x.shared_tiles = (int)((rows + kTile - 1) / kTile);
     x.shared_splits = plan.prefix_splits;
@@ -180,6 +183,9 @@ hipError_t launch_attend_tiles(const AttendArgs& a, const CacheArgs& c, const Se
   if (!plan.own_few) {
     x.own_tiles = (int)(most < rows ? most : rows);
     x.own_splits = plan.own_splits;
+    const int first = (kUnits + c.heads - 1) / c.heads;
+    const bool twice = x.shared_tiles == 0 && x.own_splits == 1 && x.own_tiles > first && x.own_tiles <= 2 * first;
+    x.descending = twice && c.dim < 256 ? first : x.own_tiles;
   }
   if (c.dim == 64) launch<64>(a, c, s, x, p, stream);
   else if (c.dim == 96) launch<96>(a, c, s, x, p, stream);

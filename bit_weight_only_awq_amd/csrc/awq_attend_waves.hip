@@ -20,7 +20,8 @@ template <int D, bool LIST>
 __global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(AttendArgs a, CacheArgs c, SeqArgs s, UnitArgs units, Partials p) {
   using T = Tile<D>;
   constexpr int LOADS = T::LOADS;
-  __shared__ __attribute__((aligned(1024))) char k0[32 * T::ROW], v0[32 * T::ROW], k1[32 * T::ROW], v1[32 * T::ROW];
+  constexpr int SLOT = 32 * T::ROW;  // keys, then values, of a block; two blocks
+  __shared__ __attribute__((aligned(1024))) char ring[4 * SLOT];
   __shared__ __attribute__((aligned(1024))) char queries[Queries<D>::BYTES ? Queries<D>::BYTES : 16];
   const int lane = threadIdx.x, wave = blockIdx.x, group = units.group;
   const float scale = a.scale * kLog2E;
@@ -32,6 +33,7 @@ __global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(Atte
   const int end = min(n.total, at + n.each);
 
   const Sources<D> kept(lane, 0);
+  const Addresses<D> places((uint32_t)(uintptr_t)(lds_char*)ring, lane);
 
   while (at < end) {
     // the segment that unit `at` is in
@@ -94,7 +96,7 @@ __global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(Atte
     g.clear();
 
     int place0 = 0, place1 = 0, next0 = 0, next1 = 0;  // of the first of 16 keys
-    auto load = [&](int block, lds_char* keys, lds_char* values) __attribute__((always_inline)) {
+    auto load = [&](int block, lds_char* to) __attribute__((always_inline)) {
       const int key = key0 + 32 * (block0 + block);
       if (block == 0 || ((key + 16) >> c.shift) - pages.first >= 64) pages.read(c, key >> c.shift);
       Sources<D> from_lane = kept;
@@ -106,17 +108,17 @@ __global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(Atte
         const char* k = reinterpret_cast<const char*>(c.k + from.at * D);
         const char* v = reinterpret_cast<const char*>(c.v + from.at * D);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load_to_lds(k + from_lane.key(i), keys + 16 * h * T::ROW + 1024 * i);
+        for (int i = 0; i < LOADS; ++i) load_to_lds(k + from_lane.key(i), to + 16 * h * T::ROW + 1024 * i);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load_to_lds(v + from_lane.value(i), values + 16 * h * T::ROW + 1024 * i);
+        for (int i = 0; i < LOADS; ++i) load_to_lds(v + from_lane.value(i), to + SLOT + 16 * h * T::ROW + 1024 * i);
       }
     };
-    auto step = [&](int block, lds_char* keys, lds_char* values, lds_char* next_keys, lds_char* next_values)
-                    __attribute__((always_inline)) {
+    auto step = [&](int block, auto parity) __attribute__((always_inline)) {
+      constexpr int HERE = 2 * SLOT * decltype(parity)::value, NEXT = 2 * SLOT - HERE;
       place0 = next0;
       place1 = next1;
       if (block + 1 < here) {
-        load(block + 1, next_keys, next_values);
+        load(block + 1, (lds_char*)ring + NEXT);
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * LOADS) : "memory");
       } else {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -124,7 +126,7 @@ __global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(Atte
       const Seen seen{place - place0, place - place1, least - place0 >= 15 && least - place1 >= 15};
       uint32_t strange = 0;
       if (!seen.all) {
-        const uint64_t met = hide_strange<D, 32>(values, lane, 64, [&](int h, int& behind, int& upto) {
+        const uint64_t met = hide_strange<D, 32>((lds_char*)ring + HERE + SLOT, lane, 64, [&](int h, int& behind, int& upto) {
           behind = least - (h ? place1 : place0);
           upto = most - (h ? place1 : place0);
         });
@@ -134,17 +136,17 @@ __global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(Atte
           strange = __builtin_amdgcn_readfirstlane(strange);
         }
       }
-      attend_block<D>(keys, values, q, scale, seen, strange, [&](int k) {
+      attend_block<D, HERE, HERE + SLOT>(places, q, scale, seen, strange, [&](int k) {
         const int key = key0 + 32 * (block0 + block) + k;
         const int page = list ? list[key >> c.shift] : key >> c.shift;
         const int64_t number = page_number(c, pages.table[page]);
         return c.v + (((number * c.heads + head) << c.shift) + (key & ((1 << c.shift) - 1))) * D;
       }, g);
     };
-    load(0, (lds_char*)k0, (lds_char*)v0);
+    load(0, (lds_char*)ring);
     for (int block = 0; block < here; block += 2) {
-      step(block, (lds_char*)k0, (lds_char*)v0, (lds_char*)k1, (lds_char*)v1);
-      if (block + 1 < here) step(block + 1, (lds_char*)k1, (lds_char*)v1, (lds_char*)k0, (lds_char*)v0);
+      step(block, std::integral_constant<int, 0>{});
+      if (block + 1 < here) step(block + 1, std::integral_constant<int, 1>{});
     }
     const bool whole = here == blocks;
     const int64_t slot = 2 * (int64_t)wave + (block0 > 0 ? 0 : 1);
