@@ -69,10 +69,20 @@ struct Sources {
   }
 };
 
-// 16 bytes per lane from `from` (a byte address per lane) into LDS, lane after lane.
-__device__ __forceinline__ void load_to_lds(const char* from, lds_char* to) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
-                                   (AWQ_LDS void*)to, 16, 0, 0);
+// 16 bytes per lane from `base` + the lane's `offset` into LDS, lane after lane.  In assembly, so that the compiler does
+// not wait for it before it reads another part of the ring: the waits (vmcnt) stand where the stages change.  (Nothing
+// comes back into registers.  The ring's address goes in as well: to the compiler this writes to it.)
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t offset, lds_char* to) {
+  uint32_t kept;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
+               : "=&s"(kept)
+               : "s"(to), "v"(offset), "s"(base)
+               : "memory");
+}
+// (the count is of loads, in the order of their issue)
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ float both_halves_max(float v) {
@@ -152,64 +162,6 @@ __device__ __forceinline__ uint64_t hide_strange(lds_char* values, int id, int t
   return met;
 }
 
-// The reads of a stage are in assembly, with their wait: for the compiler they would be reads of LDS that loads into
-// the next stage are writing to, and it would wait for those first.
-
-// N fragments of 16 bytes, OFFSET behind the lane's LDS addresses `from`.
-template <int OFFSET, int N>
-__device__ __forceinline__ void read_keys(const uint32_t* from, half8_t (&k)[N]) {
-  static_assert(N == 3 || N == 4, "fragments of a read");
-  if constexpr (N == 3)
-    asm volatile("ds_read_b128 %0, %3 offset:%6\n\tds_read_b128 %1, %4 offset:%6\n\t"
-                 "ds_read_b128 %2, %5 offset:%6\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(k[0]), "=&v"(k[1]), "=&v"(k[2])
-                 : "v"(from[0]), "v"(from[1]), "v"(from[2]), "n"(OFFSET)
-                 : "memory");
-  else
-    asm volatile("ds_read_b128 %0, %4 offset:%8\n\tds_read_b128 %1, %5 offset:%8\n\t"
-                 "ds_read_b128 %2, %6 offset:%8\n\tds_read_b128 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(k[0]), "=&v"(k[1]), "=&v"(k[2]), "=&v"(k[3])
-                 : "v"(from[0]), "v"(from[1]), "v"(from[2]), "v"(from[3]), "n"(OFFSET)
-                 : "memory");
-}
-
-// Values of 16 keys and 32 N channels as first operands, OFFSET behind the lane's addresses `from` of each 32 channels:
-// lane l of 16 reads four channels 4 (l % 4) of key l / 4 and gets channel l of four keys; rows of ROW bytes.
-template <int OFFSET, int ROW, int N>
-__device__ __forceinline__ void read_values(const uint32_t (&from)[N], half8_t (&v)[N]) {
-  static_assert(N >= 2 && N <= 4, "channels of a read");
-  typedef short short8_t __attribute__((ext_vector_type(8)));
-  short4_t lo[4], hi[4];
-  if constexpr (N == 2)
-    asm volatile("ds_read_b64_tr_b16 %0, %4 offset:%6\n\tds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
-                 "ds_read_b64_tr_b16 %2, %5 offset:%6\n\tds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
-                 "s_waitcnt lgkmcnt(0)"
-                 : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1])
-                 : "v"(from[0]), "v"(from[1]), "n"(OFFSET), "n"(OFFSET + 8 * ROW)
-                 : "memory");
-  if constexpr (N == 3)
-    asm volatile("ds_read_b64_tr_b16 %0, %6 offset:%9\n\tds_read_b64_tr_b16 %1, %6 offset:%10\n\t"
-                 "ds_read_b64_tr_b16 %2, %7 offset:%9\n\tds_read_b64_tr_b16 %3, %7 offset:%10\n\t"
-                 "ds_read_b64_tr_b16 %4, %8 offset:%9\n\tds_read_b64_tr_b16 %5, %8 offset:%10\n\t"
-                 "s_waitcnt lgkmcnt(0)"
-                 : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2])
-                 : "v"(from[0]), "v"(from[1]), "v"(from[2]), "n"(OFFSET), "n"(OFFSET + 8 * ROW)
-                 : "memory");
-  if constexpr (N == 4)
-    asm volatile("ds_read_b64_tr_b16 %0, %8 offset:%12\n\tds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
-                 "ds_read_b64_tr_b16 %2, %9 offset:%12\n\tds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
-                 "ds_read_b64_tr_b16 %4, %10 offset:%12\n\tds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
-                 "ds_read_b64_tr_b16 %6, %11 offset:%12\n\tds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
-                 "s_waitcnt lgkmcnt(0)"
-                 : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]), "=&v"(lo[3]), "=&v"(hi[3])
-                 : "v"(from[0]), "v"(from[1]), "v"(from[2]), "v"(from[3]), "n"(OFFSET), "n"(OFFSET + 8 * ROW)
-                 : "memory");
-#pragma unroll
-  for (int b = 0; b < N; ++b)
-    v[b] = __builtin_bit_cast(half8_t, short8_t{lo[b][0], lo[b][1], lo[b][2], lo[b][3], hi[b][0], hi[b][1], hi[b][2],
-                                                hi[b][3]});
-}
-
 // A lane's addresses in LDS: of its fragments of the keys (swizzling moves chunks within 16: the next 16 are 256 bytes
 // on) and of the values' 32 channels each, in a stage whose first byte is at `base`; another block or stage is an
 // offset in the instruction.
@@ -238,54 +190,96 @@ __device__ __forceinline__ void each(F f) {
   }
 }
 
-// One block of 32 tokens, whose keys are K and whose values V bytes behind the lane's addresses.  `strange`: rows of
-// the values that hold values taken out by hide_strange; value_of(k): where row k of them is in the cache.
-template <int D, int K, int V, typename ValueOf>
-__device__ __forceinline__ void attend_block(const Addresses<D>& at, const Queries<D>& q, float c, const Seen& seen,
-                                             uint32_t strange, ValueOf value_of, Gathered<D>& g) {
-  using T = Tile<D>;
-  const int lane = __lane_id(), row = lane & 31, half = lane >> 5;
-  // scores, a few fragments of the keys at a time: the next are read while the matrix cores have these
+template <int OFFSET>
+__device__ __forceinline__ half8_t read16(uint32_t at) {
+  return *(const AWQ_LDS half8_t*)(uintptr_t)(at + OFFSET);
+}
+// Four channels of a row per lane, swapped among 16 lanes: lane l of 16 points to channels 4 (l % 4) of key l / 4 and
+// gets channel l of the four keys; and of those 8 rows on.
+template <int OFFSET, int ROW>
+__device__ __forceinline__ half8_t read_turned(uint32_t at) {
+  typedef short short8_t __attribute__((ext_vector_type(8)));
+  typedef AWQ_LDS short4_t* lds4;
+  const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(uintptr_t)(at + OFFSET));
+  const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(uintptr_t)(at + OFFSET + 8 * ROW));
+  return __builtin_bit_cast(half8_t, short8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+}
+
+// The order of the instructions below is the order of the source, step by step: left to itself the compiler reads a
+// fragment, waits for it and multiplies, one after the other, and keeps vector instructions apart from matrix ones.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// With a constant zero as its addend, the compiler may give a matrix instruction a destination that overlaps its
+// operands, which this one (8 passes) writes before it has read them all: they stay alive past it.
+__device__ __forceinline__ void outlive(half8_t a, half8_t b) {
+  in_order();
+  asm volatile("" ::"v"(a), "v"(b));
+}
+
+// Fragment j of 32 keys, K bytes behind the lane's addresses, and of the queries.
+template <int D, int K, int J>
+__device__ __forceinline__ half8_t key_part(const Addresses<D>& at) {
+  return read16<K + 32 * (J / 8 * 8)>(at.key[J % 8]);
+}
+template <int D, int J>
+__device__ __forceinline__ half8_t query_part(const Queries<D>& q) {
+  if constexpr (Queries<D>::BYTES > 0) return read16<1024 * J>((uint32_t)(uintptr_t)q.at);
+  else return q.part[J];
+}
+// Channels 32 b .. + 31 of 16 of 32 keys, V bytes behind the lane's addresses: I = (D / 32) (16 keys) + b.
+template <int D, int V, int I>
+__device__ __forceinline__ half8_t value_part(const Addresses<D>& at) {
+  constexpr int ROW = Tile<D>::ROW, step = I / (D / 32), b = I % (D / 32);
+  return read_turned<V + 16 * step * ROW + 256 * (b / 4), ROW>(at.value[b % 4]);
+}
+
+constexpr int kAhead = 4;  // fragments on their way from LDS
+
+// Scores of 32 keys, K bytes behind the lane's addresses: lane (row, half) has keys 8 (i / 4) + 4 half + i % 4.
+// beside(j): vector instructions for after matrix instruction j.
+template <int D, int K, typename Beside>
+__device__ __forceinline__ float16_t scores_of(const Addresses<D>& at, const Queries<D>& q, Beside beside) {
   float16_t s = float16_t(0.0f);
-  {
-    constexpr int N = D == 96 ? 3 : 4;
-    auto part = [&](auto j0c) __attribute__((always_inline)) {
-      constexpr int j0 = decltype(j0c)::value;
-      half8_t k[N];
-      if constexpr (Queries<D>::BYTES > 0) {
-        half8_t x[N];
-        const uint32_t base = (uint32_t)(uintptr_t)q.at;
-        const uint32_t queries[4] = {base, base + 1024, base + 2048, base + 3072};
-        read_keys<1024 * j0, N>(queries, x);
-        read_keys<K + 32 * (j0 / 8 * 8), N>(at.key + j0 % 8, k);
-#pragma unroll
-        for (int j = 0; j < N; ++j) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[j], x[j], s, 0, 0, 0);
-        asm volatile("" ::"v"(x[0]));
-      } else {
-        read_keys<K, N>(at.key + j0, k);
-#pragma unroll
-        for (int j = 0; j < N; ++j) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[j], q.part[j0 + j], s, 0, 0, 0);
-      }
-      // With a constant zero as its addend, the compiler may give a matrix instruction a destination that overlaps
-      // its operands, which this one (8 passes) writes before it has read them all: they stay alive past it.
-      asm volatile("" ::"v"(k[0]));
-    };
-    each<0, D / 16, N>(part);
-  }
-  // the values' first 16 keys, while the last scores are being made
-  constexpr int N = D / 32 <= 4 ? D / 32 : 4, PARTS = D / 32 / N;
-  half8_t v[N];
-  read_values<V, T::ROW, N>(at.value, v);
-  if (!seen.all) {
-    const int limit0 = seen.limit0 - 4 * half, limit1 = seen.limit1 - 4 * half;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      s[i] = 8 * ((i >> 2) & 1) + (i & 3) > (i < 8 ? limit0 : limit1) ? -INFINITY : s[i];
-  }
+  half8_t k[kAhead], x[kAhead];
+  each<0, kAhead, 1>([&](auto jc) __attribute__((always_inline)) {
+    constexpr int j = decltype(jc)::value;
+    k[j] = key_part<D, K, j>(at);
+    x[j] = query_part<D, j>(q);
+  });
+  in_order();
+  each<0, D / 16, 1>([&](auto jc) __attribute__((always_inline)) {
+    constexpr int j = decltype(jc)::value, n = j % kAhead;
+    s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[n], x[n], s, 0, 0, 0);
+    if constexpr (j == 0) outlive(k[n], x[n]);
+    if constexpr (j + kAhead < D / 16) {
+      k[n] = key_part<D, K, j + kAhead>(at);
+      x[n] = query_part<D, j + kAhead>(q);
+    }
+    beside(jc);
+    in_order();
+  });
+  return s;
+}
+
+// Greatest of 32 scores, of lane and partner.
+__device__ __forceinline__ float greatest(const float16_t& s) {
   float m = s[0];
 #pragma unroll
   for (int i = 1; i < 16; ++i) m = fmaxf(m, s[i]);
-  m = both_halves_max(m);
+  return both_halves_max(m);
+}
+
+// Masks 32 scores, whose greatest is `m` before that, and moves the maximum on; returns what is taken off each, in
+// powers of two.
+template <int D>
+__device__ __forceinline__ float settle(float16_t& s, float m, float c, const Seen& seen, Gathered<D>& g) {
+  if (!seen.all) {
+    const int half = __lane_id() >> 5, limit0 = seen.limit0 - 4 * half, limit1 = seen.limit1 - 4 * half;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      s[i] = 8 * ((i >> 2) & 1) + (i & 3) > (i < 8 ? limit0 : limit1) ? -INFINITY : s[i];
+    m = greatest(s);
+  }
   if (__any((m - g.top) * c > kLag)) {  // (a first score: infinitely above; none yet: NaN, no)
     const float top = fmaxf(m, g.top);
     const float carry = g.top == top ? 1.0f : __builtin_amdgcn_exp2f((g.top - top) * c);
@@ -294,32 +288,104 @@ __device__ __forceinline__ void attend_block(const Addresses<D>& at, const Queri
 #pragma unroll
     for (int b = 0; b < D / 32; ++b) g.sums[b] *= carry;
   }
-  const float base = g.top == -INFINITY ? 0.0f : g.top * c;
-  half8_t p[2];
+  return g.top == -INFINITY ? 0.0f : g.top * c;
+}
+
+// The weights of 32 scores as the values' second operand.
+struct Weights {
+  half8_t part[2];
   float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -base));
-    sum += w;
-    p[i >> 3][i & 7] = (_Float16)w;
+  // of scores 2 i and 2 i + 1
+  __device__ __forceinline__ void take(int i, const float16_t& s, float c, float base) {
+    const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i], c, -base));
+    const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i + 1], c, -base));
+    sum += w0 + w1;
+    part[i >> 2][2 * (i & 3)] = (_Float16)w0;
+    part[i >> 2][2 * (i & 3) + 1] = (_Float16)w1;
   }
-  g.sum += sum;
-  each<0, 2 * PARTS, 1>([&](auto ic) __attribute__((always_inline)) {
-    constexpr int i = decltype(ic)::value, step = i / PARTS, part = i % PARTS;
-    if constexpr (i > 0) read_values<V + 16 * step * T::ROW + 256 * part, T::ROW, N>(at.value, v);
-#pragma unroll
-    for (int b = 0; b < N; ++b)
-      g.sums[part * N + b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[b], p[step], g.sums[part * N + b], 0, 0, 0);
+};
+
+// The values of 32 keys, V bytes behind the lane's addresses, by their weights.  The first fragments `v` are on their
+// way; beside(i): vector instructions for after matrix instruction i.
+template <int D, int V>
+__device__ __forceinline__ void first_values(const Addresses<D>& at, half8_t (&v)[kAhead]) {
+  constexpr int N = 2 * (D / 32) < kAhead ? 2 * (D / 32) : kAhead;
+  each<0, N, 1>([&](auto ic) __attribute__((always_inline)) { v[decltype(ic)::value] = value_part<D, V, decltype(ic)::value>(at); });
+}
+template <int D, int V, typename Beside>
+__device__ __forceinline__ void gather(const Addresses<D>& at, half8_t (&v)[kAhead], const Weights& p, Gathered<D>& g,
+                                       Beside beside) {
+  each<0, 2 * (D / 32), 1>([&](auto ic) __attribute__((always_inline)) {
+    constexpr int i = decltype(ic)::value, step = i / (D / 32), b = i % (D / 32);
+    g.sums[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[i % kAhead], p.part[step], g.sums[b], 0, 0, 0);
+    if constexpr (i + kAhead < 2 * (D / 32)) v[i % kAhead] = value_part<D, V, i + kAhead>(at);
+    beside(ic);
+    in_order();
   });
-  while (__builtin_expect(strange != 0, 0)) {
-    const int k = __builtin_ctz(strange), in16 = k & 15;
+}
+
+// Scores, weights and values of one block after the other: keys K, values V bytes behind the lane's addresses.
+template <int D, int K, int V>
+__device__ __forceinline__ Weights attend_block(const Addresses<D>& at, const Queries<D>& q, float c, const Seen& seen,
+                                                Gathered<D>& g) {
+  half8_t v[kAhead];
+  float16_t s = scores_of<D, K>(at, q, [&](auto jc) __attribute__((always_inline)) {
+    if constexpr (decltype(jc)::value == D / 16 - 1) first_values<D, V>(at, v);
+  });
+  const float base = settle<D>(s, greatest(s), c, seen, g);
+  Weights p;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p.take(i, s, c, base);
+  g.sum += p.sum;
+  gather<D, V>(at, v, p, g, [](auto) __attribute__((always_inline)) {});
+  return p;
+}
+
+// The same, a block ahead with the scores: the weights of the block whose scores are `s`, with values V bytes behind the
+// lane's addresses, beside the products for the next block's scores (keys K bytes behind), and the greatest of
+// those, `m`, beside the products with the values.
+template <int D, int K, int V>
+__device__ __forceinline__ Weights attend_next(const Addresses<D>& at, const Queries<D>& q, float c, const Seen& seen,
+                                               float16_t& s, float& m, Gathered<D>& g) {
+  constexpr int N = D / 16, M = 2 * (D / 32);
+  half8_t v[kAhead];
+  Weights p;
+  const float base = settle<D>(s, m, c, seen, g);
+  in_order();
+  float16_t next = scores_of<D, K>(at, q, [&](auto jc) __attribute__((always_inline)) {
+    constexpr int j = decltype(jc)::value;
+    if constexpr (j == N - 1) first_values<D, V>(at, v);
+#pragma unroll
+    for (int i = 8 * j / N; i < 8 * (j + 1) / N; ++i) p.take(i, s, c, base);
+  });
+  g.sum += p.sum;
+  float most = -INFINITY;
+  gather<D, V>(at, v, p, g, [&](auto ic) __attribute__((always_inline)) {
+    constexpr int i = decltype(ic)::value;
+#pragma unroll
+    for (int n = 8 * i / M; n < 8 * (i + 1) / M; ++n) most = fmaxf(most, fmaxf(next[2 * n], next[2 * n + 1]));
+  });
+  s = next;
+  m = both_halves_max(most);
+  return p;
+}
+
+// The values that hide_strange took out of rows `strange` of the block, by their weights, to the rows that see them;
+// value_of(k): where row k of them is in the cache.
+template <int D, typename ValueOf>
+__device__ __forceinline__ void gather_strange(uint32_t strange, const Weights& p, const Seen& seen, ValueOf value_of,
+                                               Gathered<D>& g) {
+  const int lane = __lane_id(), row = lane & 31, half = lane >> 5;
+#pragma unroll 1
+  while (strange != 0) {
+    const int k = __builtin_ctz(strange);
     strange &= strange - 1;
     const int i8 = 4 * ((k >> 3) & 1) + (k & 3);  // of the eight weights of its 16 keys, in lane half (k / 4) % 2
     float w = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w = i == i8 + 8 * (k >> 4) ? (float)p[i >> 3][i & 7] : w;
+    for (int i = 0; i < 16; ++i) w = i == i8 + 8 * (k >> 4) ? (float)p.part[i >> 3][i & 7] : w;
     w = __shfl(w, row + 32 * ((k >> 2) & 1));
-    const bool sees = in16 <= (k < 16 ? seen.limit0 : seen.limit1);
+    const bool sees = (k & 15) <= (k < 16 ? seen.limit0 : seen.limit1);
     const _Float16* from = value_of(k) + 4 * half;
 #pragma unroll
     for (int b = 0; b < D / 32; ++b)

@@ -28,12 +28,12 @@ template <int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tiles_kernel(AttendArgs a, CacheArgs c, SeqArgs s, TileArgs x,
                                                                              Partials p) {
   using T = Tile<D>;
-  constexpr int KEYS = D == 256 ? 32 : 64;                  // of a stage
-  constexpr int LOADS = KEYS / 16 * T::LOADS / 4;           // of a wave and stage, of keys and of values each
-  constexpr int SLOT = KEYS * T::ROW;
-  __shared__ __attribute__((aligned(1024))) char ring[4 * SLOT];  // keys, then values, of two stages
+  // Blocks of 32 keys in a ring: where it has four, a block's scores are made beside the weights of the one before
+  // (matrix and vector instructions of one wave), with two blocks on their way; heads of 256 channels leave room for two.
+  constexpr int RING = D == 256 ? 2 : 4, LOADS = T::LOADS, SLOT = 32 * T::ROW;
+  __shared__ __attribute__((aligned(1024))) char ring[2 * RING * SLOT];  // keys, then values, of each
   __shared__ __attribute__((aligned(1024))) char queries[Queries<D>::BYTES ? 4 * Queries<D>::BYTES : 16];
-  __shared__ uint32_t strange[2][2];  // of a stage and the next
+  __shared__ uint32_t strange[2];  // of a block and the next
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = x.group;
   const float scale = a.scale * kLog2E;
 
@@ -80,19 +80,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tiles_kernel(Att
     key0 = a.shared;
     keys = rows.place0 + (min(rows.first + kTile, rows.total) - 1) / group + 1 - key0;
   }
-  const int stages = keys > 0 ? (keys + KEYS - 1) / KEYS : 0;
-  const int from = (int)((long long)stages * split / splits), to = (int)((long long)stages * (split + 1) / splits);
+  const int blocks = keys > 0 ? (keys + 31) / 32 : 0;
+  const int from = (int)((long long)blocks * split / splits), to = (int)((long long)blocks * (split + 1) / splits);
 
-  // least and greatest place of the workgroup's rows, then of the wave's
+  // least and greatest place of the workgroup's rows
   const int tile_least = shared ? a.shared - 1 : rows.place0 + rows.first / group;
   const int tile_most = key0 + keys - 1;
-  if (threadIdx.x < 4) strange[threadIdx.x >> 1][threadIdx.x & 1] = 0;
+  if (threadIdx.x < 2) strange[threadIdx.x] = 0;
   rows.first += 32 * wave;
   const bool live = rows.first < rows.total;
   const int mine = min(rows.first + (lane & 31), rows.total - 1) / group;
   const int place = shared ? a.shared - 1 : rows.place0 + mine;
   const int least = shared ? a.shared - 1 : rows.place0 + min(rows.first, rows.total - 1) / group;
-  const int most = !live ? -1 : shared ? a.shared - 1 : rows.place0 + (min(rows.first + 32, rows.total) - 1) / group;
 
   Queries<D> q;
   q.place((lds_char*)queries + wave * Queries<D>::BYTES);
@@ -100,64 +99,101 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tiles_kernel(Att
   Gathered<D> g;
   g.clear();
 
-  // this wave's loads of a stage: LOADS of keys and of values, all from one group of 16 keys
-  constexpr int PER = T::LOADS / LOADS;  // waves per 16 keys
-  static_assert(T::LOADS % LOADS == 0, "a wave's loads are of one group of keys");
-  const int sixteen = wave / PER, part = wave % PER;
-  const Sources<D> kept(lane, part * LOADS);
+  // this wave's loads of a block: of keys or of values, one group of 16 of them
+  const int sixteen = wave & 1, of_values = wave >> 1;
+  uint32_t lane_from[LOADS];
+  {
+    const Sources<D> sources(lane, 0);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) lane_from[i] = of_values ? sources.value(i) : sources.key(i);
+  }
   const Addresses<D> places((uint32_t)(uintptr_t)(lds_char*)ring, lane);
   Entries pages{s.tables + (int64_t)seq.index * s.width, nullptr, 0, s.width, 0, 0, 0};
-  auto load = [&](int stage, lds_char* slot) __attribute__((always_inline)) {
-    const int key = key0 + KEYS * stage;
-    if (stage == from || ((key + KEYS - 16) >> c.shift) - pages.first >= 64) pages.read(c, key >> c.shift);
+  auto load = [&](int block, int slot) __attribute__((always_inline)) {
+    const int key = key0 + 32 * block;
+    if (block == from || ((key + 16) >> c.shift) - pages.first >= 64) pages.read(c, key >> c.shift);
     const Keys16 source = keys16(pages, c, head, key + 16 * sixteen);
-    const char* k = reinterpret_cast<const char*>(c.k + source.at * D);
-    const char* v = reinterpret_cast<const char*>(c.v + source.at * D);
-    Sources<D> from_lane = kept;
-    asm volatile("" : "+v"(from_lane.keys[0]), "+v"(from_lane.values[0]));  // (each load's is formed here, not kept)
-    lds_char* to = slot + 16 * sixteen * T::ROW + 1024 * part * LOADS;
+    const char* base = reinterpret_cast<const char*>((of_values ? c.v : c.k) + source.at * D);
+    lds_char* to = (lds_char*)ring + (2 * slot + of_values) * SLOT + 16 * sixteen * T::ROW;
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) load_to_lds(k + from_lane.key(i), to + 1024 * i);
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) load_to_lds(v + from_lane.value(i), to + SLOT + 1024 * i);
+    for (int i = 0; i < LOADS; ++i) load_to_lds(base, lane_from[i], to + 1024 * i);
   };
-  auto step = [&](int stage, auto parity) __attribute__((always_inline)) {
-    constexpr int HERE = 2 * SLOT * decltype(parity)::value, NEXT = 2 * SLOT - HERE;
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  auto meet = [&]() __attribute__((always_inline)) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (stage + 1 < to) load(stage + 1, (lds_char*)ring + NEXT);
-    // past the least place of the workgroup's rows some values are not to be seen by some row
-    const int key = key0 + KEYS * stage;
-    const bool ragged = key + KEYS - 1 > tile_least;
-    if (ragged) {
-      const uint64_t met = hide_strange<D, KEYS>((lds_char*)ring + HERE + SLOT, threadIdx.x, 256, [&](int h, int& behind, int& upto) {
-        behind = tile_least - key - 16 * h;
-        upto = tile_most - key - 16 * h;
-      });
-      if ((uint32_t)met) atomicOr(&strange[stage & 1][0], (uint32_t)met);
-      if (met >> 32) atomicOr(&strange[stage & 1][1], (uint32_t)(met >> 32));
-      if (threadIdx.x < 2) strange[(stage + 1) & 1][threadIdx.x] = 0;
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-    }
-    each<0, KEYS / 32, 1>([&](auto bc) __attribute__((always_inline)) {
-      constexpr int b = decltype(bc)::value;
-      const int first = key + 32 * b;
-      if (first > most) return;
-      const Seen seen{place - first, place - first - 16, least - first >= 31};
-      const uint32_t odd = ragged ? __builtin_amdgcn_readfirstlane(strange[stage & 1][b]) : 0;
-      attend_block<D, HERE + 32 * b * T::ROW, HERE + SLOT + 32 * b * T::ROW>(places, q, scale, seen, odd, [&](int k) {
-        const int64_t number = page_number(c, pages.table[(first + k) >> c.shift]);
-        return c.v + (((number * c.heads + head) << c.shift) + ((first + k) & ((1 << c.shift) - 1))) * D;
-      }, g);
-    });
   };
-  if (from < to) load(from, (lds_char*)ring);
-  for (int stage = from; stage < to; stage += 2) {
-    step(stage, std::integral_constant<int, 0>{});
-    if (stage + 1 < to) step(stage + 1, std::integral_constant<int, 1>{});
+  // past the least place of the workgroup's rows some values are not to be seen by some row
+  auto hide = [&](int block, int slot) __attribute__((always_inline)) {
+    const int key = key0 + 32 * block;
+    if (key + 31 <= tile_least) return 0u;
+    const uint32_t met = (uint32_t)hide_strange<D, 32>((lds_char*)ring + (2 * slot + 1) * SLOT, threadIdx.x, 256,
+                                                       [&](int h, int& behind, int& upto) {
+                                                         behind = tile_least - key - 16 * h;
+                                                         upto = tile_most - key - 16 * h;
+                                                       });
+    if (met) atomicOr(&strange[block & 1], met);
+    if (threadIdx.x == 0) strange[(block + 1) & 1] = 0;
+    meet();
+    return (uint32_t)__builtin_amdgcn_readfirstlane(strange[block & 1]);
+  };
+  auto seen_of = [&](int block) __attribute__((always_inline)) {
+    const int key = key0 + 32 * block;
+    return Seen{place - key, place - key - 16, least - key >= 31};
+  };
+  auto finish = [&](int block, uint32_t odd, const Weights& p, const Seen& seen) __attribute__((always_inline)) {
+    if (__builtin_expect(odd != 0, 0))
+      gather_strange<D>(odd, p, seen, [&](int k) {
+        const int key = key0 + 32 * block + k;
+        const int64_t number = page_number(c, pages.table[key >> c.shift]);
+        return c.v + (((number * c.heads + head) << c.shift) + (key & ((1 << c.shift) - 1))) * D;
+      }, g);
+  };
+  if constexpr (RING == 4) {
+    float16_t s_now = float16_t(0.0f);
+    float m_now = 0.0f;
+    if (from < to) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) load(min(from + i, to - 1), i);
+      wait_loads<2 * LOADS>();
+      meet();
+      s_now = scores_of<D, 0>(places, q, [](auto) __attribute__((always_inline)) {});
+      m_now = greatest(s_now);
+    }
+    // One block: its scores are there, the next block's are made; the one after that may still be on its way, and the
+    // fourth takes the place of the last (past the end, the last block again: its scores count nothing).
+    auto step = [&](int block, auto slot) __attribute__((always_inline)) {
+      constexpr int HERE = decltype(slot)::value, NEXT = (HERE + 1) % 4;
+      wait_loads<LOADS>();
+      meet();
+      load(min(block + 3, to - 1), (HERE + 3) % 4);
+      const uint32_t odd = hide(block, HERE);
+      const Seen seen = seen_of(block);
+      const Weights p = attend_next<D, 2 * NEXT * SLOT, (2 * HERE + 1) * SLOT>(places, q, scale, seen, s_now, m_now, g);
+      finish(block, odd, p, seen);
+    };
+    for (int block = from; block < to; block += 4)
+      each<0, 4, 1>([&](auto slot) __attribute__((always_inline)) {
+        constexpr int i = decltype(slot)::value;
+        if (block + i < to) step(block + i, slot);
+      });
+    wait_loads<0>();  // (those past the end)
+  } else {
+    auto step = [&](int block, auto slot) __attribute__((always_inline)) {
+      constexpr int HERE = decltype(slot)::value;
+      wait_loads<0>();
+      meet();
+      if (block + 1 < to) load(block + 1, 1 - HERE);
+      const uint32_t odd = hide(block, HERE);
+      const Seen seen = seen_of(block);
+      const Weights p = attend_block<D, 2 * HERE * SLOT, (2 * HERE + 1) * SLOT>(places, q, scale, seen, g);
+      finish(block, odd, p, seen);
+    };
+    if (from < to) load(from, 0);
+    for (int block = from; block < to; block += 2) {
+      step(block, std::integral_constant<int, 0>{});
+      if (block + 1 < to) step(block + 1, std::integral_constant<int, 1>{});
+    }
   }
   if (live) write_rows(g, scale, a, p, rows, group, head, slice, nullptr, nullptr);
 }

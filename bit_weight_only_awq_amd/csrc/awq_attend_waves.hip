@@ -108,9 +108,9 @@ __global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(Atte
         const char* k = reinterpret_cast<const char*>(c.k + from.at * D);
         const char* v = reinterpret_cast<const char*>(c.v + from.at * D);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load_to_lds(k + from_lane.key(i), to + 16 * h * T::ROW + 1024 * i);
+        for (int i = 0; i < LOADS; ++i) load_to_lds(k, from_lane.key(i), to + 16 * h * T::ROW + 1024 * i);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load_to_lds(v + from_lane.value(i), to + SLOT + 16 * h * T::ROW + 1024 * i);
+        for (int i = 0; i < LOADS; ++i) load_to_lds(v, from_lane.value(i), to + SLOT + 16 * h * T::ROW + 1024 * i);
       }
     };
     auto step = [&](int block, auto parity) __attribute__((always_inline)) {
@@ -119,9 +119,9 @@ __global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(Atte
       place1 = next1;
       if (block + 1 < here) {
         load(block + 1, (lds_char*)ring + NEXT);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * LOADS) : "memory");
+        wait_loads<4 * LOADS>();
       } else {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        wait_loads<0>();
       }
       const Seen seen{place - place0, place - place1, least - place0 >= 15 && least - place1 >= 15};
       uint32_t strange = 0;
@@ -136,12 +136,14 @@ __global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(Atte
           strange = __builtin_amdgcn_readfirstlane(strange);
         }
       }
-      attend_block<D, HERE, HERE + SLOT>(places, q, scale, seen, strange, [&](int k) {
-        const int key = key0 + 32 * (block0 + block) + k;
-        const int page = list ? list[key >> c.shift] : key >> c.shift;
-        const int64_t number = page_number(c, pages.table[page]);
-        return c.v + (((number * c.heads + head) << c.shift) + (key & ((1 << c.shift) - 1))) * D;
-      }, g);
+      const Weights p = attend_block<D, HERE, HERE + SLOT>(places, q, scale, seen, g);
+      if (__builtin_expect(strange != 0, 0))
+        gather_strange<D>(strange, p, seen, [&](int k) {
+          const int key = key0 + 32 * (block0 + block) + k;
+          const int page = list ? list[key >> c.shift] : key >> c.shift;
+          const int64_t number = page_number(c, pages.table[page]);
+          return c.v + (((number * c.heads + head) << c.shift) + (key & ((1 << c.shift) - 1))) * D;
+        }, g);
     };
     load(0, (lds_char*)ring);
     for (int block = 0; block < here; block += 2) {
