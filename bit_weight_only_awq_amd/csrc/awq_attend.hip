@@ -65,8 +65,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
     const int blocks = a.list ? list_blocks(j.units, a.count) : key_blocks(j.units, seq.length);
     const int r = a.list ? g : (t - seq.row0) * group + g;
     const int before = a.list ? t * row_blocks(j.units, 1) : 0;
-    own_unit = first + ((before + (r >> 5)) * c.heads + head) * blocks;
-    own_row = r & 31;
+    const int nth = r / j.units.rows;
+    own_unit = first + ((before + nth) * c.heads + head) * blocks;
+    own_row = r - nth * j.units.rows;
     own_wave = own_unit / n.each;
     own_waves = (own_unit + blocks - 1) / n.each - own_wave + 1;
     if (own_waves == 1) {
@@ -79,8 +80,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
   }
   if (j.units.shared) {
     const int blocks = (j.units.shared_keys + 31) >> 5, r = (t - all_rows(s, 0).row0) * group + g;
-    shared_unit = ((r >> 5) * c.heads + head) * blocks;
-    shared_row = r & 31;
+    const int nth = r / j.units.rows;
+    shared_unit = (nth * c.heads + head) * blocks;
+    shared_row = r - nth * j.units.rows;
     shared_wave = shared_unit / n.each;
     shared_waves = (shared_unit + blocks - 1) / n.each - shared_wave + 1;
     if (shared_waves == 1) {
@@ -222,14 +224,18 @@ AttendPlan plan_of(int T, int B, int q_heads, int kv_heads, int dim, int page_si
   const int group = q_heads / kv_heads, stage = dim == 256 ? 32 : 64, slots = dim == 256 ? kUnits : 2 * kUnits;
   const int64_t rows = (int64_t)T * group;
   AttendPlan p{};
-  // (units of the waves: 32 rows, at least a block of them per sequence, times key heads and blocks of 32 keys)
-  const int64_t units = kv_heads * ((rows / 32 + B) * ((int64_t)width * page_size / 32 + 1) + (rows / 32 + 1) * (shared / 32 + 1));
+  // (units of the waves: 16 rows, at least a block of them per sequence, times key heads and blocks of 32 keys)
+  const int64_t units = kv_heads * ((rows / 16 + B) * ((int64_t)width * page_size / 32 + 1) + (rows / 16 + 1) * (shared / 32 + 1));
   p.own_few = list || (rows <= 32 * (int64_t)B && units < kMostUnits);
   p.prefix = shared == 0 ? 0 : p.own_few && rows <= 32 ? 1 : 2;
   p.waves = kUnits * (dim == 256 ? 2 : dim == 128 ? 5 : 6);
   p.least = 2;
   p.own_splits = p.prefix_splits = 1;
-  if (p.prefix == 2) p.prefix_splits = splits_of((rows + 127) / 128 * kv_heads, (shared + stage - 1) / stage, slots, 3.0);
+  p.rows = rows <= 16 * (int64_t)(list ? T : B) ? 16 : 32;
+  p.both = p.own_few && p.rows == 16 && p.prefix == 2 && dim < 256;
+  if (p.both) p.waves = kUnits * kWavesOfWorkgroup;  // (a unit's other workgroup makes row tiles)
+  if (p.prefix == 2)
+    p.prefix_splits = splits_of((rows + 127) / 128 * kv_heads, (shared + stage - 1) / stage, p.both ? kUnits : slots, 3.0);
   if (!p.own_few) {
     const int64_t keys = (int64_t)width * page_size - shared;
     p.own_splits = splits_of(((rows + 127) / 128 + B / 2) * kv_heads, (keys + stage - 1) / stage, slots, 3.0);
@@ -264,7 +270,7 @@ hipError_t launch_attend(const AttendArgs& a, const CacheArgs& c, const SeqArgs&
   const Partials p = partials(plan, (int64_t)s.T * a.q_heads, c.dim, workspace);
   hipError_t e = hipSuccess;
   if (plan.prefix == 2 || !plan.own_few) e = launch_attend_tiles(a, c, s, plan, p, stream);
-  if (e == hipSuccess && plan.own_few) e = launch_attend_waves(a, c, s, plan, p, stream);
+  if (e == hipSuccess && plan.own_few && !plan.both) e = launch_attend_waves(a, c, s, plan, p, stream);
   if (e != hipSuccess || (!plan.own_few && plan.slices() == 0)) return e;
   const JoinArgs j{unit_args(a, c, plan), plan.own_few, plan.own_slices(), plan.slices() - plan.own_slices()};
   if (c.dim == 64) launch_join<64>(a, c, s, j, p, stream);

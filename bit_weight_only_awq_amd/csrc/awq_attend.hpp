@@ -7,12 +7,15 @@
 namespace awq {
 
 constexpr int kUnits = 256;  // compute units
+constexpr int kWavesOfWorkgroup = 2;  // waves on their own of a workgroup, where it may be row tiles as well
 
-// Rows of 32 and keys of 32 of one wave (few), rows of 128 and splits of the keys (many).
+// Rows of 16 or 32 and keys of 32 of one wave (few), rows of 128 and splits of the keys (many).
 struct AttendPlan {
   bool own_few;       // a sequence's own keys: a wave per 32 rows, or a workgroup per 128
   int prefix;         // the shared keys: 0: none, 1: with the waves (and own_few), 2: with the workgroups
   int waves, least;   // waves of the first kind; key blocks that each takes at least
+  int rows;           // of theirs: 16 or 32
+  bool both;          // own_few and prefix 2, in one launch
   int own_splits, prefix_splits;  // of the second kind
   int own_slices() const { return own_few ? (prefix ? 1 : 0) : prefix || own_splits > 1 ? own_splits : 0; }
   int slices() const { return own_slices() + (prefix == 2 ? prefix_splits : prefix); }
@@ -20,7 +23,7 @@ struct AttendPlan {
 
 // Partial results: for each row's query head (numbered t * q_heads + head) and slice the maximum (in powers of two),
 // the sum and the values' sums: slice 0 (to own_splits - 1) the own keys, the rest the shared ones; and two of
-// those of 32 rows per wave, for a piece that starts within a segment and one that ends within one.
+// those of 32 rows per wave (or of its 16), for a piece that starts within a segment and one that ends within one.
 struct Partials {
   float2* stat;    // [slices][rows]
   float* sums;     // [slices][rows][dim]
@@ -49,7 +52,7 @@ hipError_t launch_attend_waves(const AttendArgs& a, const CacheArgs& c, const Se
 hipError_t launch_attend_tiles(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan,
                                const Partials& p, hipStream_t stream);
 
-// The units of work of the waves (32 rows, a key head, 32 keys), in order: the shared keys' (all rows together), then
+// The units of work of the waves (16 or 32 rows, a key head, 32 keys), in order: the shared keys' (all rows together), then
 // sequence after sequence; within one, rows, then key heads, then keys.  Every row has at least one.  Wave w takes the units
 // w * each .. w * each + each - 1.  (The host makes sure that their number stays below kMostUnits.)
 struct Units {
@@ -57,13 +60,14 @@ struct Units {
 };
 struct UnitArgs {
   int group, heads, shift, shared_keys, waves, least;
+  int rows;     // of a unit: 16 or 32
   bool shared;  // the shared keys are the waves' too
 };
 inline UnitArgs unit_args(const AttendArgs& a, const CacheArgs& c, const AttendPlan& plan) {
-  return UnitArgs{a.q_heads / c.heads, c.heads, c.shift, a.shared, plan.waves, plan.least, plan.prefix == 1};
+  return UnitArgs{a.q_heads / c.heads, c.heads, c.shift, a.shared, plan.waves, plan.least, plan.rows, plan.prefix == 1};
 }
 __device__ __forceinline__ int key_blocks(const UnitArgs& u, int length) { return max((length - u.shared_keys + 31) >> 5, 1); }
-__device__ __forceinline__ int row_blocks(const UnitArgs& u, int rows) { return (rows * u.group + 31) >> 5; }
+__device__ __forceinline__ int row_blocks(const UnitArgs& u, int rows) { return (rows * u.group + u.rows - 1) / u.rows; }
 __device__ __forceinline__ int units_of(const UnitArgs& u, const Sequence& q) {
   return q.rows ? row_blocks(u, q.rows) * u.heads * key_blocks(u, q.length) : 0;
 }
@@ -87,9 +91,9 @@ __device__ __forceinline__ int list_blocks(const UnitArgs& u, int count) { retur
 
 constexpr int64_t kMostUnits = 1 << 30;
 
-// 32 rows, numbered token after token, the key head's query heads within one: `first` is the number of the first,
+// Rows, numbered token after token, the key head's query heads within one: `first` is the number of the first,
 // `total` how many the sequence has; `place0` and `row0` are of its first token.
-struct Rows32 {
+struct Rows {
   int first, total, row0, place0;
 };
 
@@ -124,16 +128,16 @@ __device__ __forceinline__ Keys16 keys16(const Entries& e, const CacheArgs& c, i
                 page < 0 ? kNowhere : (page << c.shift) + slot};
 }
 
-// The queries of a wave's 32 rows.
-template <int D>
-__device__ __forceinline__ void read_queries(Queries<D>& q, const AttendArgs& a, const Rows32& r, int group, int head) {
-  const int lane = __lane_id(), row = r.first + (lane & 31), token = row / group;
+// The queries of a wave's R rows.
+template <int D, int R>
+__device__ __forceinline__ void read_queries(Queries<D, R>& q, const AttendArgs& a, const Rows& r, int group, int head) {
+  const int lane = __lane_id(), row = r.first + (lane & (R - 1)), token = row / group;
   const bool live = row < r.total;
   const _Float16* from = a.q + (live ? (r.row0 + token) * a.ldq + (int64_t)(head * group + row - token * group) * D : 0) +
-                         8 * (lane >> 5);
+                         8 * (lane / R);
 #pragma unroll
-  for (int j = 0; j < D / 16; ++j) {
-    half8_t v = *reinterpret_cast<const half8_t*>(from + 16 * j);
+  for (int j = 0; j < Queries<D, R>::PARTS; ++j) {
+    half8_t v = *reinterpret_cast<const half8_t*>(from + 512 / R * j);
     if (!live) v = half8_t((_Float16)0.0f);
     q.put(j, v);
   }
@@ -141,45 +145,41 @@ __device__ __forceinline__ void read_queries(Queries<D>& q, const AttendArgs& a,
 
 constexpr float kNoPlace = -1.0f;  // a sum that no row can have
 
-// Results of a wave's 32 rows: to y (`slice` below 0), or unfinished to a slice of the rows, or to `wave_stat` and
-// `wave_sums` of 32 rows.
-template <int D>
-__device__ __forceinline__ void write_rows(const Gathered<D>& g, float c, const AttendArgs& a, const Partials& p,
-                                           const Rows32& r, int group, int head, int slice, float2* wave_stat,
+// Results of a wave's R rows: to y (`slice` below 0), or unfinished to a slice of the rows, or to `wave_stat` and
+// `wave_sums` of R rows.
+template <int D, int R>
+__device__ __forceinline__ void write_rows(const Gathered<D, R>& g, float c, const AttendArgs& a, const Partials& p,
+                                           const Rows& r, int group, int head, int slice, float2* wave_stat,
                                            float* wave_sums) {
-  const int lane = __lane_id(), row = r.first + (lane & 31), token = row / group, half = lane >> 5;
+  const int lane = __lane_id(), row = r.first + (lane & (R - 1)), token = row / group, h = lane / R;
   if (row >= r.total) return;
-  const float sum = both_halves_sum(g.sum);
+  const float sum = row_sum<R>(g.sum);
   const int64_t t = r.row0 + token;
   const int at = head * group + row - token * group;
   if (slice < 0 && !wave_stat) {
     const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
-    _Float16* y = a.y + t * a.ldy + (int64_t)at * D + 4 * half;
+    _Float16* y = a.y + t * a.ldy + (int64_t)at * D + 4 * h;
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b)
+    for (int n = 0; n < Gathered<D, R>::QUADS; ++n) {
+      half4_t v;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        half4_t v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (_Float16)(sum == 0.0f ? 0.0f : g.sums[b][4 * n + i] * by);
-        *reinterpret_cast<half4_t*>(y + 32 * b + 8 * n) = v;
-      }
+      for (int i = 0; i < 4; ++i) v[i] = (_Float16)(sum == 0.0f ? 0.0f : g.get(n, i) * by);
+      *reinterpret_cast<half4_t*>(y + 256 / R * n) = v;
+    }
     return;
   }
-  const int64_t to = wave_stat ? lane & 31 : (int64_t)slice * p.rows + t * a.q_heads + at;
+  const int64_t to = wave_stat ? lane & (R - 1) : (int64_t)slice * p.rows + t * a.q_heads + at;
   // (a row without a place is marked: shared keys, which it does not have, must not count for it)
-  if (half == 0)
+  if (h == 0)
     (wave_stat ? wave_stat : p.stat)[to] = r.place0 + token < 0 ? float2{0.0f, kNoPlace} : float2{g.top * c, sum};
-  float* sums = (wave_stat ? wave_sums : p.sums) + to * D + 4 * half;
+  float* sums = (wave_stat ? wave_sums : p.sums) + to * D + 4 * h;
 #pragma unroll
-  for (int b = 0; b < D / 32; ++b)
+  for (int n = 0; n < Gathered<D, R>::QUADS; ++n) {
+    float4_t v;
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      float4_t v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = g.sums[b][4 * n + i];
-      *reinterpret_cast<float4_t*>(sums + 32 * b + 8 * n) = v;
-    }
+    for (int i = 0; i < 4; ++i) v[i] = g.get(n, i);
+    *reinterpret_cast<float4_t*>(sums + 256 / R * n) = v;
+  }
 }
 
 }  // namespace awq

@@ -1,16 +1,16 @@
-// Shared by the attention kernels: 32 rows of queries against 32 keys on the
-// matrix cores.
+// Shared by the attention kernels: 32 rows of queries (or 16, where there are no
+// more) against 32 keys on the matrix cores.
 //
 // Mathematics: a wave keeps, for each of its 32 rows, the running maximum m of the
 // scores, the sum l of the weights 2^((score - m) c) with c = scale log2(e), and
 // the weighted sum of the values, one pass over the keys.  Scores are formed
 // transposed, keys x queries, so that a lane holds 16 scores of one row (lane %
-// 32) and its partner 32 lanes away the other 16: maximum and sum need one
-// exchange, and a change of the maximum scales a lane's sums by a number it
-// has.  The weights, rounded to fp16 (relative 2^-11, as the values are), are then in
+// 32) and its partner 32 lanes away the other 16 (of 16 rows: 8, and three
+// partners): maximum and sum need one exchange (two), and a change of the maximum
+// scales a lane's sums by a number it has.  The weights, rounded to fp16 (relative 2^-11, as the values are), are then in
 // place as the second operand of the product with the values, whose first operand
 // comes out of LDS transposed; both follow the same order of keys (lane half h holds
-// keys 8 j + 4 h .. + 3), so nothing is exchanged.  Sums are fp32.
+// keys 8 j + 4 h .. + 3, lane quarter h of 16 rows keys 16 j + 4 h .. + 3), so nothing is exchanged.  Sums are fp32.
 //
 // The maximum lags: sums are rescaled only once a score passes it by a factor of
 // 2^8, which fp16 holds for weights and fp32 for sums.
@@ -32,7 +32,8 @@ constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLag = 8.0f;  // the maximum lags by at most this power of two
 
 // Rows of D halves in LDS, as 16-byte chunks: chunk c of row r is at chunk c ^ swizzle(r), so that what
-// one instruction reads lies in different banks (16 rows of one chunk for keys, 4 rows of 4 chunks for values).
+// half a wave reads in one instruction lies in different banks (16 rows of one chunk for keys; for values 4 rows of 4
+// chunks, or 8 rows of 2).
 template <int D>
 struct Tile {
   static constexpr int CHUNKS = D / 8, ROW = D * 2;
@@ -41,7 +42,8 @@ struct Tile {
     return D == 64 ? (r >> 1) & 7 : D == 96 ? (r >> 2) & 3 : r & 15;
   }
   static __device__ __forceinline__ int value_swizzle(int r) {
-    return D == 64 ? ((r >> 1) & 1) << 2 : D == 96 ? 0 : (r & 3) << 2;
+    const int fours = ((r >> 2) & 1) << 1;
+    return D == 64 ? ((r >> 1) & 1) << 2 | fours : D == 96 ? fours : (r & 3) << 2 | fours;
   }
 };
 
@@ -65,7 +67,8 @@ struct Sources {
     return D == 96 ? keys[i] : (keys[0] ^ (uint32_t)(16 * (D == 64 ? 4 * i : ROWS * i))) + 1024 * i;
   }
   __device__ __forceinline__ uint32_t value(int i) const {
-    return D == 96 ? values[i] : (values[0] ^ (uint32_t)(D == 256 ? 128 * (i & 1) : 0)) + 1024 * i;
+    return D == 96 ? values[i]
+                   : (values[0] ^ (uint32_t)(D == 256 ? 128 * (i & 1) + 16 * (i & 2) : D == 128 ? 32 * (i & 1) : 0)) + 1024 * i;
   }
 };
 
@@ -85,20 +88,58 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ float both_halves_max(float v) {
+// Greatest and sum over the lanes that share a row (R rows: lane % R).
+template <int R>
+__device__ __forceinline__ float row_max(float v) {
+  if constexpr (R == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false,
+                                                    false);
+    const uint32_t r0 = r[0], r1 = r[1];
+    v = fmaxf(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
+  }
   const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false,
                                                   false);
   const uint32_t r0 = r[0], r1 = r[1];
   return fmaxf(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
 }
-__device__ __forceinline__ float both_halves_sum(float v) { return swap_sum32(v, v); }
+template <int R>
+__device__ __forceinline__ float row_sum(float v) {
+  if constexpr (R == 16) v = swap_sum16(v, v);
+  return swap_sum32(v, v);
+}
 
-// What 32 rows have gathered: sums[b][i] is channel 32 b + 8 (i / 4) + 4 (lane /
-// 32) + i % 4 of row lane % 32; `sum` is the lane's share of l.
+// Scores of 32 keys and R rows, and what R rows gather: in a lane of row lane % R and part h = lane / R, scores 4 i .. 4
+// i + 3 are of keys (256 / R) i + 4 h .. + 3, sums 4 n .. 4 n + 3 of channels (256 / R) n + 4 h .. + 3.
+template <int R>
+struct Scores;
+template <>
+struct Scores<32> {
+  static constexpr int COUNT = 16;
+  float16_t s;
+  __device__ __forceinline__ float get(int i) const { return s[i]; }
+  __device__ __forceinline__ void put(int i, float v) { s[i] = v; }
+};
+template <>
+struct Scores<16> {
+  static constexpr int COUNT = 8;
+  float4_t s[2];
+  __device__ __forceinline__ float get(int i) const { return s[i >> 2][i & 3]; }
+  __device__ __forceinline__ void put(int i, float v) { s[i >> 2][i & 3] = v; }
+};
+
+template <int D, int R>
+struct Gathered;
 template <int D>
-struct Gathered {
+struct Gathered<D, 32> {
+  static constexpr int QUADS = D / 8;
   float16_t sums[D / 32];
-  float top, sum;
+  float top, sum;  // the maximum; the lane's share of l
+  __device__ __forceinline__ float get(int n, int i) const { return sums[n >> 2][4 * (n & 3) + i]; }
+  __device__ __forceinline__ void add(int n, int i, float v) { sums[n >> 2][4 * (n & 3) + i] += v; }
+  __device__ __forceinline__ void scale(float by) {
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) sums[b] *= by;
+  }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int b = 0; b < D / 32; ++b) sums[b] = float16_t(0.0f);
@@ -106,19 +147,38 @@ struct Gathered {
     sum = 0.0f;
   }
 };
-
-// Fragments of 32 rows' queries: row lane % 32, channels 16 j + 8 (lane / 32) .. + 7.  Where a head is 256 wide they
-// are in LDS, a wave's 64 times 16 bytes for each j (in registers with everything else, they would not all fit).
 template <int D>
+struct Gathered<D, 16> {
+  static constexpr int QUADS = D / 16;
+  float4_t sums[QUADS];
+  float top, sum;
+  __device__ __forceinline__ float get(int n, int i) const { return sums[n][i]; }
+  __device__ __forceinline__ void add(int n, int i, float v) { sums[n][i] += v; }
+  __device__ __forceinline__ void scale(float by) {
+#pragma unroll
+    for (int n = 0; n < QUADS; ++n) sums[n] *= by;
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int n = 0; n < QUADS; ++n) sums[n] = float4_t(0.0f);
+    top = -INFINITY;
+    sum = 0.0f;
+  }
+};
+
+// Fragments of R rows' queries: row lane % R, channels 8 (64 / R) j + 8 (lane / R) .. + 7.  Where a head is 256 wide,
+// those of 32 rows are in LDS, a wave's 64 times 16 bytes for each j (in registers with everything else, they would
+// not all fit).
+template <int D, int R>
 struct Queries {
-  static constexpr int BYTES = 0;  // of LDS, for a wave
-  half8_t part[D / 16];
+  static constexpr int BYTES = 0, PARTS = D * R / 512;  // of LDS, for a wave
+  half8_t part[PARTS];
   __device__ __forceinline__ void place(lds_char*) {}
   __device__ __forceinline__ void put(int j, half8_t v) { part[j] = v; }
 };
 template <>
-struct Queries<256> {
-  static constexpr int BYTES = 16 * 1024;
+struct Queries<256, 32> {
+  static constexpr int BYTES = 16 * 1024, PARTS = 16;
   lds_char* at;
   __device__ __forceinline__ void place(lds_char* to) { at = to + 16 * __lane_id(); }
   __device__ __forceinline__ void put(int j, half8_t v) { *(AWQ_LDS half8_t*)(at + 1024 * j) = v; }
@@ -162,22 +222,23 @@ __device__ __forceinline__ uint64_t hide_strange(lds_char* values, int id, int t
   return met;
 }
 
-// A lane's addresses in LDS: of its fragments of the keys (swizzling moves chunks within 16: the next 16 are 256 bytes
-// on) and of the values' 32 channels each, in a stage whose first byte is at `base`; another block or stage is an
-// offset in the instruction.
-template <int D>
+// A lane's addresses in LDS: of its fragments of the keys and of the values' channels (swizzling moves chunks within
+// 16: the next 16 are 256 bytes on), in a block whose first byte is at `base`; another block is an offset in the
+// instruction.
+template <int D, int R>
 struct Addresses {
   using T = Tile<D>;
-  static constexpr int KEYS = D < 128 ? D / 16 : 8, VALUES = D / 32 <= 4 ? D / 32 : 4;
+  static constexpr int WIDE = D < 128 ? D : 128, KEYS = WIDE * R / 512, VALUES = WIDE / R;
   uint32_t key[KEYS], value[VALUES];
   __device__ __forceinline__ Addresses(uint32_t base, int lane) {
-    const int row = lane & 31, half = lane >> 5, swz = T::key_swizzle(row) ^ half;
+    const int row = lane & (R - 1), h = lane / R, swz = T::key_swizzle(row) ^ h;
 #pragma unroll
-    for (int j = 0; j < KEYS; ++j) key[j] = base + row * T::ROW + 16 * ((2 * j) ^ swz);
-    const int l = lane & 15, chunk = 2 * ((lane >> 4) & 1) + ((l & 3) >> 1), vswz = T::value_swizzle(l >> 2);
+    for (int j = 0; j < KEYS; ++j) key[j] = base + row * T::ROW + 16 * ((64 / R * j) ^ swz);
+    // 16 lanes point to 4 rows of 16 channels: of 32 rows' values, the next 16 lanes to the next 16 channels
+    const int l = lane & 15, from = 4 * h + (l >> 2), chunk = (R == 32 ? 2 * ((lane >> 4) & 1) : 0) + ((l & 3) >> 1);
 #pragma unroll
     for (int b = 0; b < VALUES; ++b)
-      value[b] = base + (4 * half + (l >> 2)) * T::ROW + 8 * (l & 1) + 16 * ((4 * b + chunk) ^ vswz);
+      value[b] = base + from * T::ROW + 8 * (l & 1) + 16 * ((R / 8 * b + chunk) ^ T::value_swizzle(from));
   }
 };
 
@@ -195,13 +256,13 @@ __device__ __forceinline__ half8_t read16(uint32_t at) {
   return *(const AWQ_LDS half8_t*)(uintptr_t)(at + OFFSET);
 }
 // Four channels of a row per lane, swapped among 16 lanes: lane l of 16 points to channels 4 (l % 4) of key l / 4 and
-// gets channel l of the four keys; and of those 8 rows on.
-template <int OFFSET, int ROW>
+// gets channel l of the four keys; and of those APART bytes on.
+template <int OFFSET, int APART>
 __device__ __forceinline__ half8_t read_turned(uint32_t at) {
   typedef short short8_t __attribute__((ext_vector_type(8)));
   typedef AWQ_LDS short4_t* lds4;
   const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(uintptr_t)(at + OFFSET));
-  const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(uintptr_t)(at + OFFSET + 8 * ROW));
+  const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(uintptr_t)(at + OFFSET + APART));
   return __builtin_bit_cast(half8_t, short8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
 }
 
@@ -216,44 +277,51 @@ __device__ __forceinline__ void outlive(half8_t a, half8_t b) {
   asm volatile("" ::"v"(a), "v"(b));
 }
 
-// Fragment j of 32 keys, K bytes behind the lane's addresses, and of the queries.
-template <int D, int K, int J>
-__device__ __forceinline__ half8_t key_part(const Addresses<D>& at) {
-  return read16<K + 32 * (J / 8 * 8)>(at.key[J % 8]);
+// The products of a block, in order.  Scores: fragment J of the keys with fragment J % PARTS of the queries (of 16 rows,
+// the first 16 keys, then the others).  Values: I = (D / 32) (16 keys) + 32 channels; of 16 rows: 16 channels, all keys.
+template <int D, int R>
+struct Products {
+  static constexpr int SCORES = D / 16, VALUES = D / 16, PARTS = Queries<D, R>::PARTS;
+};
+template <int D, int R, int K, int J>
+__device__ __forceinline__ half8_t key_part(const Addresses<D, R>& at) {
+  constexpr int PARTS = Queries<D, R>::PARTS, KEYS = Addresses<D, R>::KEYS, j = J % PARTS;
+  return read16<K + J / PARTS * 16 * Tile<D>::ROW + 256 * (j / KEYS)>(at.key[j % KEYS]);
 }
-template <int D, int J>
-__device__ __forceinline__ half8_t query_part(const Queries<D>& q) {
-  if constexpr (Queries<D>::BYTES > 0) return read16<1024 * J>((uint32_t)(uintptr_t)q.at);
-  else return q.part[J];
+template <int D, int R, int J>
+__device__ __forceinline__ half8_t query_part(const Queries<D, R>& q) {
+  if constexpr (Queries<D, R>::BYTES > 0) return read16<1024 * J>((uint32_t)(uintptr_t)q.at);
+  else return q.part[J % Queries<D, R>::PARTS];
 }
-// Channels 32 b .. + 31 of 16 of 32 keys, V bytes behind the lane's addresses: I = (D / 32) (16 keys) + b.
-template <int D, int V, int I>
-__device__ __forceinline__ half8_t value_part(const Addresses<D>& at) {
-  constexpr int ROW = Tile<D>::ROW, step = I / (D / 32), b = I % (D / 32);
-  return read_turned<V + 16 * step * ROW + 256 * (b / 4), ROW>(at.value[b % 4]);
+template <int D, int R, int V, int I>
+__device__ __forceinline__ half8_t value_part(const Addresses<D, R>& at) {
+  constexpr int ROW = Tile<D>::ROW, VALUES = Addresses<D, R>::VALUES;
+  constexpr int b = R == 32 ? I % (D / 32) : I, rows = R == 32 ? 16 * (I / (D / 32)) : 0;
+  return read_turned<V + rows * ROW + 256 * (b / VALUES), (R == 32 ? 8 : 16) * ROW>(at.value[b % VALUES]);
 }
 
 constexpr int kAhead = 4;  // fragments on their way from LDS
 
-// Scores of 32 keys, K bytes behind the lane's addresses: lane (row, half) has keys 8 (i / 4) + 4 half + i % 4.
-// beside(j): vector instructions for after matrix instruction j.
-template <int D, int K, typename Beside>
-__device__ __forceinline__ float16_t scores_of(const Addresses<D>& at, const Queries<D>& q, Beside beside) {
-  float16_t s = float16_t(0.0f);
+// Scores of 32 keys, K bytes behind the lane's addresses.  beside(j): vector instructions for after matrix instruction j.
+template <int D, int R, int K, typename Beside>
+__device__ __forceinline__ Scores<R> scores_of(const Addresses<D, R>& at, const Queries<D, R>& q, Beside beside) {
+  using P = Products<D, R>;
+  Scores<R> s{};
   half8_t k[kAhead], x[kAhead];
   each<0, kAhead, 1>([&](auto jc) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value;
-    k[j] = key_part<D, K, j>(at);
-    x[j] = query_part<D, j>(q);
+    k[j] = key_part<D, R, K, j>(at);
+    x[j] = query_part<D, R, j>(q);
   });
   in_order();
-  each<0, D / 16, 1>([&](auto jc) __attribute__((always_inline)) {
+  each<0, P::SCORES, 1>([&](auto jc) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value, n = j % kAhead;
-    s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[n], x[n], s, 0, 0, 0);
-    if constexpr (j == 0) outlive(k[n], x[n]);
-    if constexpr (j + kAhead < D / 16) {
-      k[n] = key_part<D, K, j + kAhead>(at);
-      x[n] = query_part<D, j + kAhead>(q);
+    if constexpr (R == 32) s.s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[n], x[n], s.s, 0, 0, 0);
+    else s.s[j / P::PARTS] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[n], x[n], s.s[j / P::PARTS], 0, 0, 0);
+    if constexpr (j % P::PARTS == 0) outlive(k[n], x[n]);
+    if constexpr (j + kAhead < P::SCORES) {
+      k[n] = key_part<D, R, K, j + kAhead>(at);
+      x[n] = query_part<D, R, j + kAhead>(q);
     }
     beside(jc);
     in_order();
@@ -261,23 +329,26 @@ __device__ __forceinline__ float16_t scores_of(const Addresses<D>& at, const Que
   return s;
 }
 
-// Greatest of 32 scores, of lane and partner.
-__device__ __forceinline__ float greatest(const float16_t& s) {
-  float m = s[0];
+// Greatest of a row's 32 scores.
+template <int R>
+__device__ __forceinline__ float greatest(const Scores<R>& s) {
+  float m = s.get(0);
 #pragma unroll
-  for (int i = 1; i < 16; ++i) m = fmaxf(m, s[i]);
-  return both_halves_max(m);
+  for (int i = 1; i < Scores<R>::COUNT; ++i) m = fmaxf(m, s.get(i));
+  return row_max<R>(m);
 }
 
 // Masks 32 scores, whose greatest is `m` before that, and moves the maximum on; returns what is taken off each, in
 // powers of two.
-template <int D>
-__device__ __forceinline__ float settle(float16_t& s, float m, float c, const Seen& seen, Gathered<D>& g) {
+template <int D, int R>
+__device__ __forceinline__ float settle(Scores<R>& s, float m, float c, const Seen& seen, Gathered<D, R>& g) {
   if (!seen.all) {
-    const int half = __lane_id() >> 5, limit0 = seen.limit0 - 4 * half, limit1 = seen.limit1 - 4 * half;
+    const int h = __lane_id() / R, limit0 = seen.limit0 - 4 * h, limit1 = seen.limit1 - 4 * h;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      s[i] = 8 * ((i >> 2) & 1) + (i & 3) > (i < 8 ? limit0 : limit1) ? -INFINITY : s[i];
+    for (int i = 0; i < Scores<R>::COUNT; ++i) {
+      const int k = 256 / R * (i >> 2) + (i & 3);
+      s.put(i, (k & 15) > (k < 16 ? limit0 : limit1) ? -INFINITY : s.get(i));
+    }
     m = greatest(s);
   }
   if (__any((m - g.top) * c > kLag)) {  // (a first score: infinitely above; none yet: NaN, no)
@@ -285,20 +356,20 @@ __device__ __forceinline__ float settle(float16_t& s, float m, float c, const Se
     const float carry = g.top == top ? 1.0f : __builtin_amdgcn_exp2f((g.top - top) * c);
     g.top = top;
     g.sum *= carry;
-#pragma unroll
-    for (int b = 0; b < D / 32; ++b) g.sums[b] *= carry;
+    g.scale(carry);
   }
   return g.top == -INFINITY ? 0.0f : g.top * c;
 }
 
 // The weights of 32 scores as the values' second operand.
+template <int R>
 struct Weights {
-  half8_t part[2];
+  half8_t part[R / 16];
   float sum = 0.0f;
   // of scores 2 i and 2 i + 1
-  __device__ __forceinline__ void take(int i, const float16_t& s, float c, float base) {
-    const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i], c, -base));
-    const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i + 1], c, -base));
+  __device__ __forceinline__ void take(int i, const Scores<R>& s, float c, float base) {
+    const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s.get(2 * i), c, -base));
+    const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s.get(2 * i + 1), c, -base));
     sum += w0 + w1;
     part[i >> 2][2 * (i & 3)] = (_Float16)w0;
     part[i >> 2][2 * (i & 3) + 1] = (_Float16)w1;
@@ -307,98 +378,99 @@ struct Weights {
 
 // The values of 32 keys, V bytes behind the lane's addresses, by their weights.  The first fragments `v` are on their
 // way; beside(i): vector instructions for after matrix instruction i.
-template <int D, int V>
-__device__ __forceinline__ void first_values(const Addresses<D>& at, half8_t (&v)[kAhead]) {
-  constexpr int N = 2 * (D / 32) < kAhead ? 2 * (D / 32) : kAhead;
-  each<0, N, 1>([&](auto ic) __attribute__((always_inline)) { v[decltype(ic)::value] = value_part<D, V, decltype(ic)::value>(at); });
+template <int D, int R, int V>
+__device__ __forceinline__ void first_values(const Addresses<D, R>& at, half8_t (&v)[kAhead]) {
+  each<0, kAhead, 1>([&](auto ic) __attribute__((always_inline)) {
+    v[decltype(ic)::value] = value_part<D, R, V, decltype(ic)::value>(at);
+  });
 }
-template <int D, int V, typename Beside>
-__device__ __forceinline__ void gather(const Addresses<D>& at, half8_t (&v)[kAhead], const Weights& p, Gathered<D>& g,
-                                       Beside beside) {
-  each<0, 2 * (D / 32), 1>([&](auto ic) __attribute__((always_inline)) {
-    constexpr int i = decltype(ic)::value, step = i / (D / 32), b = i % (D / 32);
-    g.sums[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[i % kAhead], p.part[step], g.sums[b], 0, 0, 0);
-    if constexpr (i + kAhead < 2 * (D / 32)) v[i % kAhead] = value_part<D, V, i + kAhead>(at);
+template <int D, int R, int V, typename Beside>
+__device__ __forceinline__ void gather(const Addresses<D, R>& at, half8_t (&v)[kAhead], const Weights<R>& p,
+                                       Gathered<D, R>& g, Beside beside) {
+  each<0, Products<D, R>::VALUES, 1>([&](auto ic) __attribute__((always_inline)) {
+    constexpr int i = decltype(ic)::value, b = R == 32 ? i % (D / 32) : i, step = R == 32 ? i / (D / 32) : 0;
+    if constexpr (R == 32) g.sums[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[i % kAhead], p.part[step], g.sums[b], 0, 0, 0);
+    else g.sums[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[i % kAhead], p.part[step], g.sums[b], 0, 0, 0);
+    if constexpr (i + kAhead < Products<D, R>::VALUES) v[i % kAhead] = value_part<D, R, V, i + kAhead>(at);
     beside(ic);
     in_order();
   });
 }
 
 // Scores, weights and values of one block after the other: keys K, values V bytes behind the lane's addresses.
-template <int D, int K, int V>
-__device__ __forceinline__ Weights attend_block(const Addresses<D>& at, const Queries<D>& q, float c, const Seen& seen,
-                                                Gathered<D>& g) {
+template <int D, int R, int K, int V>
+__device__ __forceinline__ Weights<R> attend_block(const Addresses<D, R>& at, const Queries<D, R>& q, float c,
+                                                   const Seen& seen, Gathered<D, R>& g) {
   half8_t v[kAhead];
-  float16_t s = scores_of<D, K>(at, q, [&](auto jc) __attribute__((always_inline)) {
-    if constexpr (decltype(jc)::value == D / 16 - 1) first_values<D, V>(at, v);
+  Scores<R> s = scores_of<D, R, K>(at, q, [&](auto jc) __attribute__((always_inline)) {
+    if constexpr (decltype(jc)::value == Products<D, R>::SCORES - 1) first_values<D, R, V>(at, v);
   });
-  const float base = settle<D>(s, greatest(s), c, seen, g);
-  Weights p;
+  const float base = settle<D, R>(s, greatest(s), c, seen, g);
+  Weights<R> p;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) p.take(i, s, c, base);
+  for (int i = 0; i < Scores<R>::COUNT / 2; ++i) p.take(i, s, c, base);
   g.sum += p.sum;
-  gather<D, V>(at, v, p, g, [](auto) __attribute__((always_inline)) {});
+  gather<D, R, V>(at, v, p, g, [](auto) __attribute__((always_inline)) {});
   return p;
 }
 
 // The same, a block ahead with the scores: the weights of the block whose scores are `s`, with values V bytes behind the
 // lane's addresses, beside the products for the next block's scores (keys K bytes behind), and the greatest of
 // those, `m`, beside the products with the values.
-template <int D, int K, int V>
-__device__ __forceinline__ Weights attend_next(const Addresses<D>& at, const Queries<D>& q, float c, const Seen& seen,
-                                               float16_t& s, float& m, Gathered<D>& g) {
-  constexpr int N = D / 16, M = 2 * (D / 32);
+template <int D, int R, int K, int V>
+__device__ __forceinline__ Weights<R> attend_next(const Addresses<D, R>& at, const Queries<D, R>& q, float c,
+                                                  const Seen& seen, Scores<R>& s, float& m, Gathered<D, R>& g) {
+  constexpr int N = Products<D, R>::SCORES, M = Products<D, R>::VALUES, PAIRS = Scores<R>::COUNT / 2;
   half8_t v[kAhead];
-  Weights p;
-  const float base = settle<D>(s, m, c, seen, g);
+  Weights<R> p;
+  const float base = settle<D, R>(s, m, c, seen, g);
   in_order();
-  float16_t next = scores_of<D, K>(at, q, [&](auto jc) __attribute__((always_inline)) {
+  Scores<R> next = scores_of<D, R, K>(at, q, [&](auto jc) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value;
-    if constexpr (j == N - 1) first_values<D, V>(at, v);
+    if constexpr (j == N - 1) first_values<D, R, V>(at, v);
 #pragma unroll
-    for (int i = 8 * j / N; i < 8 * (j + 1) / N; ++i) p.take(i, s, c, base);
+    for (int i = PAIRS * j / N; i < PAIRS * (j + 1) / N; ++i) p.take(i, s, c, base);
   });
   g.sum += p.sum;
   float most = -INFINITY;
-  gather<D, V>(at, v, p, g, [&](auto ic) __attribute__((always_inline)) {
+  gather<D, R, V>(at, v, p, g, [&](auto ic) __attribute__((always_inline)) {
     constexpr int i = decltype(ic)::value;
 #pragma unroll
-    for (int n = 8 * i / M; n < 8 * (i + 1) / M; ++n) most = fmaxf(most, fmaxf(next[2 * n], next[2 * n + 1]));
+    for (int n = PAIRS * i / M; n < PAIRS * (i + 1) / M; ++n) most = fmaxf(most, fmaxf(next.get(2 * n), next.get(2 * n + 1)));
   });
   s = next;
-  m = both_halves_max(most);
+  m = row_max<R>(most);
   return p;
 }
 
 // The values that hide_strange took out of rows `strange` of the block, by their weights, to the rows that see them;
 // value_of(k): where row k of them is in the cache.
-template <int D, typename ValueOf>
-__device__ __forceinline__ void gather_strange(uint32_t strange, const Weights& p, const Seen& seen, ValueOf value_of,
-                                               Gathered<D>& g) {
-  const int lane = __lane_id(), row = lane & 31, half = lane >> 5;
+template <int D, int R, typename ValueOf>
+__device__ __forceinline__ void gather_strange(uint32_t strange, const Weights<R>& p, const Seen& seen, ValueOf value_of,
+                                               Gathered<D, R>& g) {
+  const int lane = __lane_id(), row = lane & (R - 1), h = lane / R;
 #pragma unroll 1
   while (strange != 0) {
     const int k = __builtin_ctz(strange);
     strange &= strange - 1;
-    const int i8 = 4 * ((k >> 3) & 1) + (k & 3);  // of the eight weights of its 16 keys, in lane half (k / 4) % 2
+    // its weight is number `at` of those in part `of` of the lanes
+    const int of = (k >> 2) & (64 / R - 1), at = R == 32 ? 4 * (k >> 3) + (k & 3) : 4 * (k >> 4) + (k & 3);
     float w = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w = i == i8 + 8 * (k >> 4) ? (float)p.part[i >> 3][i & 7] : w;
-    w = __shfl(w, row + 32 * ((k >> 2) & 1));
+    for (int i = 0; i < Scores<R>::COUNT; ++i) w = i == at ? (float)p.part[i >> 3][i & 7] : w;
+    w = __shfl(w, row + R * of);
     const bool sees = (k & 15) <= (k < 16 ? seen.limit0 : seen.limit1);
-    const _Float16* from = value_of(k) + 4 * half;
+    const _Float16* from = value_of(k) + 4 * h;
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b)
+    for (int n = 0; n < Gathered<D, R>::QUADS; ++n) {
+      const half4_t x = *reinterpret_cast<const half4_t*>(from + 256 / R * n);
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const half4_t x = *reinterpret_cast<const half4_t*>(from + 32 * b + 8 * n);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool gives = sees && !finite16(__builtin_bit_cast(uint16_t, (_Float16)x[i]));
-          g.sums[b][4 * n + i] += gives ? w * (float)x[i] : 0.0f;
-        }
-        __builtin_amdgcn_sched_barrier(0);
+      for (int i = 0; i < 4; ++i) {
+        const bool gives = sees && !finite16(__builtin_bit_cast(uint16_t, (_Float16)x[i]));
+        g.add(n, i, gives ? w * (float)x[i] : 0.0f);
       }
+      in_order();
+    }
   }
 }
 

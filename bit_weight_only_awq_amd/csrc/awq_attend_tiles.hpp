@@ -1,0 +1,229 @@
+// Attention of many rows (prompts, and the shared keys of a batch): workgroups of
+// 128 rows, four waves of 32, that share each stage of keys and values.
+//
+// Mathematics: awq_attend_block.hpp's.  A row is a token and a query head of one key
+// head, so the query heads of a group and, for the shared keys, the sequences of the
+// batch are rows of one product: the shared keys are read once per 128 rows, not
+// once per sequence.
+//
+// Bound: the matrix cores (4 D operations per row and key) beside the
+// exponentials.  A stage of keys and values goes straight to LDS while the one
+// before it is multiplied, with one barrier per stage.  Where the row tiles are
+// too few for the chip, the keys are split as well and the parts joined by a second
+// launch.
+#pragma once
+
+#include "awq_attend.hpp"
+
+namespace awq {
+
+constexpr int kTile = 128;  // rows of a workgroup
+
+// `shared_tiles` workgroup rows of the shared keys first, then the sequences' own.
+struct TileArgs {
+  int group, shared_tiles, shared_splits, own_tiles, own_splits, own_slice, shared_slice;
+  int descending;  // of the own tiles (per key head and split), those that come first, from the last rows up
+};
+
+template <int D>
+struct TileRing {
+  static constexpr int BLOCKS = D == 256 ? 2 : 4, BYTES = 2 * BLOCKS * 32 * Tile<D>::ROW;
+};
+
+// Workgroup number `index` of 256 threads; a ring of TileRing<D>::BYTES, room for the queries where they are in LDS, and
+// two words.
+template <int D>
+__device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const TileArgs& x,
+                                            const Partials& p, int index, lds_char* ring, lds_char* queries,
+                                            uint32_t* strange) {
+  using T = Tile<D>;
+  // Blocks of 32 keys in a ring: where it has four, a block's scores are made beside the weights of the one before
+  // (matrix and vector instructions of one wave), with two blocks on their way; heads of 256 channels leave room for two.
+  constexpr int RING = TileRing<D>::BLOCKS, LOADS = T::LOADS, SLOT = 32 * T::ROW;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = x.group;
+  const float scale = a.scale * kLog2E;
+
+  // the tile: key heads next to each other (one XCD keeps meeting the same); the last rows, which have the most keys,
+  // first, and where there are at most two workgroups per compute unit the second ones the other way around, so that
+  // each unit gets one with many keys and one with few
+  const int head = index % c.heads;
+  int nth = index / c.heads;
+  const bool shared = nth < x.shared_tiles * x.shared_splits;
+  int split, splits, slice, key0, keys;
+  Rows rows;  // of the workgroup, then of the wave
+  Sequence seq;
+  if (shared) {
+    split = nth / x.shared_tiles;
+    splits = x.shared_splits;
+    slice = x.shared_slice + split;
+    seq = all_rows(s, a.shared);
+    rows = Rows{kTile * (nth - split * x.shared_tiles), seq.rows * group, seq.row0, 0};
+    if (rows.first >= rows.total) return;
+    key0 = 0;
+    keys = a.shared;
+  } else {
+    nth -= x.shared_tiles * x.shared_splits;
+    split = nth / x.own_tiles;
+    splits = x.own_splits;
+    slice = x.own_slice < 0 ? -1 : x.own_slice + split;
+    const int turn = nth - split * x.own_tiles, wanted = turn < x.descending ? x.own_tiles - 1 - turn : turn - x.descending;
+    int seen = 0;
+    bool found = false;
+    for (int b0 = 0; b0 < s.B; b0 += 64) {
+      const Sequence q = sequence_at(s, c.shift, b0 + lane);
+      const int tiles = (q.rows * group + kTile - 1) / kTile, sum = seen + prefix_sum(tiles);
+      const unsigned long long owner = __ballot(sum > wanted && sum - tiles <= wanted);
+      if (owner != 0) {
+        const int l = __builtin_ctzll(owner);
+        seq = pick(q, l);
+        rows = Rows{kTile * (wanted - __builtin_amdgcn_readlane(sum - tiles, l)), seq.rows * group, seq.row0, seq.place0()};
+        found = true;
+        break;
+      }
+      seen = __builtin_amdgcn_readlane(sum, 63);
+    }
+    if (!found) return;
+    key0 = a.shared;
+    keys = rows.place0 + (min(rows.first + kTile, rows.total) - 1) / group + 1 - key0;
+  }
+  const int blocks = keys > 0 ? (keys + 31) / 32 : 0;
+  const int from = (int)((long long)blocks * split / splits), to = (int)((long long)blocks * (split + 1) / splits);
+
+  // least and greatest place of the workgroup's rows
+  const int tile_least = shared ? a.shared - 1 : rows.place0 + rows.first / group;
+  const int tile_most = key0 + keys - 1;
+  if (threadIdx.x < 2) strange[threadIdx.x] = 0;
+  rows.first += 32 * wave;
+  const bool live = rows.first < rows.total;
+  const int mine = min(rows.first + (lane & 31), rows.total - 1) / group;
+  const int place = shared ? a.shared - 1 : rows.place0 + mine;
+  const int least = shared ? a.shared - 1 : rows.place0 + min(rows.first, rows.total - 1) / group;
+
+  Queries<D, 32> q;
+  q.place(queries + wave * Queries<D, 32>::BYTES);
+  read_queries(q, a, rows, group, head);
+  Gathered<D, 32> g;
+  g.clear();
+
+  // this wave's loads of a block: of keys or of values, one group of 16 of them
+  const int sixteen = wave & 1, of_values = wave >> 1;
+  uint32_t lane_from[LOADS];
+  {
+    const Sources<D> sources(lane, 0);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) lane_from[i] = of_values ? sources.value(i) : sources.key(i);
+  }
+  const Addresses<D, 32> places((uint32_t)(uintptr_t)ring, lane);
+  Entries pages{s.tables + (int64_t)seq.index * s.width, nullptr, 0, s.width, 0, 0, 0};
+  auto load = [&](int block, int slot) __attribute__((always_inline)) {
+    const int key = key0 + 32 * block;
+    if (block == from || ((key + 16) >> c.shift) - pages.first >= 64) pages.read(c, key >> c.shift);
+    const Keys16 source = keys16(pages, c, head, key + 16 * sixteen);
+    const char* base = reinterpret_cast<const char*>((of_values ? c.v : c.k) + source.at * D);
+    lds_char* to = ring + (2 * slot + of_values) * SLOT + 16 * sixteen * T::ROW;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) load_to_lds(base, lane_from[i], to + 1024 * i);
+  };
+  auto meet = [&]() __attribute__((always_inline)) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  // past the least place of the workgroup's rows some values are not to be seen by some row
+  auto hide = [&](int block, int slot) __attribute__((always_inline)) {
+    const int key = key0 + 32 * block;
+    if (key + 31 <= tile_least) return 0u;
+    const uint32_t met = (uint32_t)hide_strange<D, 32>(ring + (2 * slot + 1) * SLOT, threadIdx.x, 256,
+                                                       [&](int h, int& behind, int& upto) {
+                                                         behind = tile_least - key - 16 * h;
+                                                         upto = tile_most - key - 16 * h;
+                                                       });
+    if (met) atomicOr(&strange[block & 1], met);
+    if (threadIdx.x == 0) strange[(block + 1) & 1] = 0;
+    meet();
+    return (uint32_t)__builtin_amdgcn_readfirstlane(strange[block & 1]);
+  };
+  auto seen_of = [&](int block) __attribute__((always_inline)) {
+    const int key = key0 + 32 * block;
+    return Seen{place - key, place - key - 16, least - key >= 31};
+  };
+  auto finish = [&](int block, uint32_t odd, const Weights<32>& p, const Seen& seen) __attribute__((always_inline)) {
+    if (__builtin_expect(odd != 0, 0))
+      gather_strange<D, 32>(odd, p, seen, [&](int k) {
+        const int key = key0 + 32 * block + k;
+        const int64_t number = page_number(c, pages.table[key >> c.shift]);
+        return c.v + (((number * c.heads + head) << c.shift) + (key & ((1 << c.shift) - 1))) * D;
+      }, g);
+  };
+  if constexpr (RING == 4) {
+    Scores<32> s_now{};
+    float m_now = 0.0f;
+    if (from < to) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) load(min(from + i, to - 1), i);
+      wait_loads<2 * LOADS>();
+      meet();
+      s_now = scores_of<D, 32, 0>(places, q, [](auto) __attribute__((always_inline)) {});
+      m_now = greatest(s_now);
+    }
+    // One block: its scores are there, the next block's are made; the one after that may still be on its way, and the
+    // fourth takes the place of the last (past the end, the last block again: its scores count nothing).
+    auto step = [&](int block, auto slot) __attribute__((always_inline)) {
+      constexpr int HERE = decltype(slot)::value, NEXT = (HERE + 1) % 4;
+      wait_loads<LOADS>();
+      meet();
+      load(min(block + 3, to - 1), (HERE + 3) % 4);
+      const uint32_t odd = hide(block, HERE);
+      const Seen seen = seen_of(block);
+      const Weights<32> p = attend_next<D, 32, 2 * NEXT * SLOT, (2 * HERE + 1) * SLOT>(places, q, scale, seen, s_now, m_now, g);
+      finish(block, odd, p, seen);
+    };
+    for (int block = from; block < to; block += 4)
+      each<0, 4, 1>([&](auto slot) __attribute__((always_inline)) {
+        constexpr int i = decltype(slot)::value;
+        if (block + i < to) step(block + i, slot);
+      });
+    wait_loads<0>();  // (those past the end)
+  } else {
+    auto step = [&](int block, auto slot) __attribute__((always_inline)) {
+      constexpr int HERE = decltype(slot)::value;
+      wait_loads<0>();
+      meet();
+      if (block + 1 < to) load(block + 1, 1 - HERE);
+      const uint32_t odd = hide(block, HERE);
+      const Seen seen = seen_of(block);
+      const Weights<32> p = attend_block<D, 32, 2 * HERE * SLOT, (2 * HERE + 1) * SLOT>(places, q, scale, seen, g);
+      finish(block, odd, p, seen);
+    };
+    if (from < to) load(from, 0);
+    for (int block = from; block < to; block += 2) {
+      step(block, std::integral_constant<int, 0>{});
+      if (block + 1 < to) step(block + 1, std::integral_constant<int, 1>{});
+    }
+  }
+  if (live) write_rows(g, scale, a, p, rows, group, head, slice, nullptr, nullptr);
+}
+
+// How a plan's row tiles are numbered.
+inline TileArgs tile_args(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan) {
+  const int group = a.q_heads / c.heads;
+  const int64_t rows = (int64_t)s.T * group, most = rows / kTile + s.B;  // (a ragged tile per sequence at most)
+  TileArgs x{group, 0, 1, 0, 1, plan.own_slices() > 0 ? 0 : -1, plan.own_slices(), 0};
+  if (plan.prefix == 2) {
+    x.shared_tiles = (int)((rows + kTile - 1) / kTile);
+    x.shared_splits = plan.prefix_splits;
+  }
+  if (!plan.own_few) {
+    x.own_tiles = (int)(most < rows ? most : rows);
+    x.own_splits = plan.own_splits;
+    const int first = (kUnits + c.heads - 1) / c.heads;
+    const bool twice = x.shared_tiles == 0 && x.own_splits == 1 && x.own_tiles > first && x.own_tiles <= 2 * first;
+    x.descending = twice && c.dim < 256 ? first : x.own_tiles;
+  }
+  return x;
+}
+inline unsigned tile_workgroups(const TileArgs& x, int heads) {
+  return (unsigned)((x.shared_tiles * x.shared_splits + x.own_tiles * x.own_splits) * heads);
+}
+
+}  // namespace awq

@@ -1,167 +1,30 @@
-// Attention of few rows per sequence (decoding): each wave on its own, 32 rows of
-// queries against an equal share of all keys.
-//
-// Mathematics: awq_attend_block.hpp's.  A unit of work is 32 keys for up to 32 rows
-// (tokens times query heads of one key head); all units of the batch, whatever the
-// lengths, are one list, and each of the `waves` waves takes an equal run of it, so
-// ragged batches and single long sequences fill the chip alike.  A wave that
-// takes a whole segment (rows, key head) writes its result; the pieces of the
-// others are joined by a second launch.
-//
-// Bound: HBM, each key and value once.  Keys and values go straight to LDS
-// (16 bytes per lane, whole rows), one block of 32 keys ahead of the products; a
-// workgroup is one wave, so nothing waits for a barrier.
-#include "awq_attend.hpp"
+// Attention of few rows per sequence on its own: a workgroup is one wave
+// (awq_attend_waves.hpp), so nothing waits for a barrier.
+#include "awq_attend_waves.hpp"
 
 namespace awq {
 namespace {
 
-template <int D, bool LIST>
-__global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(AttendArgs a, CacheArgs c, SeqArgs s, UnitArgs units, Partials p) {
-  using T = Tile<D>;
-  constexpr int LOADS = T::LOADS;
-  constexpr int SLOT = 32 * T::ROW;  // keys, then values, of a block; two blocks
-  __shared__ __attribute__((aligned(1024))) char ring[4 * SLOT];
-  __shared__ __attribute__((aligned(1024))) char queries[Queries<D>::BYTES ? Queries<D>::BYTES : 16];
-  const int lane = threadIdx.x, wave = blockIdx.x, group = units.group;
-  const float scale = a.scale * kLog2E;
+template <int D, int R, bool LIST>
+__global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(AttendArgs a, CacheArgs c, SeqArgs s,
+                                                                            UnitArgs units, Partials p) {
+  __shared__ __attribute__((aligned(1024))) char ring[wave_ring<D>()];
+  __shared__ __attribute__((aligned(1024))) char queries[Queries<D, R>::BYTES ? Queries<D, R>::BYTES : 16];
+  attend_wave<D, R, LIST>(a, c, s, units, p, blockIdx.x, (lds_char*)ring, (lds_char*)queries);
+}
 
-  const int list_rows = row_blocks(units, 1), of_list = LIST ? list_blocks(units, a.count) : 0;
-  const int per_token = c.heads * list_rows * of_list;
-  const Units n = LIST ? share_units(units, s.T * per_token, 0) : count_units(s, units);
-  int at = wave * n.each;
-  const int end = min(n.total, at + n.each);
-
-  const Sources<D> kept(lane, 0);
-  const Addresses<D> places((uint32_t)(uintptr_t)(lds_char*)ring, lane);
-
-  while (at < end) {
-    // the segment that unit `at` is in
-    Sequence seq{0, 0, 0, 0};
-    int nth, blocks, key0 = 0, count = 0;  // nth: of the sequence's units
-    const int* list = nullptr;
-    bool shared = false;
-    if constexpr (LIST) {
-      const int t = at / per_token;
-      nth = at - t * per_token;
-      blocks = of_list;
-      const Sequence of = sequence_of(s, c.shift, t);
-      if (of.rows == 0) {  // a row of no sequence
-        at += per_token - nth;
-        continue;
-      }
-      seq = Sequence{of.index, t, 1, t - of.row0 + of.place0() + 1};
-    } else if (at < n.shared) {
-      shared = true;
-      seq = all_rows(s, a.shared);
-      nth = at;
-      blocks = (a.shared + 31) >> 5;
-    } else {
-      int seen = n.shared;
-      for (int b0 = 0;; b0 += 64) {  // (some sequence holds it: at < total)
-        const Sequence q = sequence_at(s, c.shift, b0 + lane);
-        const int mine = units_of(units, q), sum = seen + prefix_sum(mine);
-        const unsigned long long owner = __ballot(sum > at && sum - mine <= at);
-        if (owner != 0) {
-          const int l = __builtin_ctzll(owner);
-          seq = pick(q, l);
-          nth = at - __builtin_amdgcn_readlane(sum - mine, l);
-          break;
-        }
-        seen = __builtin_amdgcn_readlane(sum, 63);
-      }
-      blocks = key_blocks(units, seq.length);
-      key0 = a.shared;
-    }
-    const int which = nth / blocks, block0 = nth - which * blocks;
-    const int row_block = which / c.heads, head = which - row_block * c.heads;
-    const int here = min(blocks - block0, end - at);
-    at += here;
-    const Rows32 rows{32 * row_block, seq.rows * group, seq.row0, seq.place0()};
-    // places of the rows: their own, and the least and greatest of them (past the shared keys: the last of these)
-    const int mine = (min(rows.first + (lane & 31), rows.total - 1)) / group;
-    const int place = shared ? a.shared - 1 : rows.place0 + mine;
-    const int least = shared ? a.shared - 1 : rows.place0 + rows.first / group;
-    const int most = shared ? a.shared - 1 : rows.place0 + (min(rows.first + 32, rows.total) - 1) / group;
-    if constexpr (LIST) {
-      list = a.list + ((int64_t)seq.row0 * c.heads + head) * a.count;
-      count = a.count;
-    }
-    Entries pages{s.tables + (int64_t)seq.index * s.width, list, count, s.width, 0, 0, 0};
-
-    Queries<D> q;
-    q.place((lds_char*)queries);
-    read_queries(q, a, rows, group, head);
-    Gathered<D> g;
-    g.clear();
-
-    int place0 = 0, place1 = 0, next0 = 0, next1 = 0;  // of the first of 16 keys
-    auto load = [&](int block, lds_char* to) __attribute__((always_inline)) {
-      const int key = key0 + 32 * (block0 + block);
-      if (block == 0 || ((key + 16) >> c.shift) - pages.first >= 64) pages.read(c, key >> c.shift);
-      Sources<D> from_lane = kept;
-      asm volatile("" : "+v"(from_lane.keys[0]), "+v"(from_lane.values[0]));  // (each load's is formed here, not kept)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const Keys16 from = keys16(pages, c, head, key + 16 * h);
-        (h ? next1 : next0) = from.place;
-        const char* k = reinterpret_cast<const char*>(c.k + from.at * D);
-        const char* v = reinterpret_cast<const char*>(c.v + from.at * D);
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) load_to_lds(k, from_lane.key(i), to + 16 * h * T::ROW + 1024 * i);
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) load_to_lds(v, from_lane.value(i), to + SLOT + 16 * h * T::ROW + 1024 * i);
-      }
-    };
-    auto step = [&](int block, auto parity) __attribute__((always_inline)) {
-      constexpr int HERE = 2 * SLOT * decltype(parity)::value, NEXT = 2 * SLOT - HERE;
-      place0 = next0;
-      place1 = next1;
-      if (block + 1 < here) {
-        load(block + 1, (lds_char*)ring + NEXT);
-        wait_loads<4 * LOADS>();
-      } else {
-        wait_loads<0>();
-      }
-      const Seen seen{place - place0, place - place1, least - place0 >= 15 && least - place1 >= 15};
-      uint32_t strange = 0;
-      if (!seen.all) {
-        const uint64_t met = hide_strange<D, 32>((lds_char*)ring + HERE + SLOT, lane, 64, [&](int h, int& behind, int& upto) {
-          behind = least - (h ? place1 : place0);
-          upto = most - (h ? place1 : place0);
-        });
-        if (__any(met != 0)) {
-          strange = (uint32_t)met;
-          for (int m = 1; m < 64; m <<= 1) strange |= (uint32_t)__shfl_xor((int)strange, m);
-          strange = __builtin_amdgcn_readfirstlane(strange);
-        }
-      }
-      const Weights p = attend_block<D, HERE, HERE + SLOT>(places, q, scale, seen, g);
-      if (__builtin_expect(strange != 0, 0))
-        gather_strange<D>(strange, p, seen, [&](int k) {
-          const int key = key0 + 32 * (block0 + block) + k;
-          const int page = list ? list[key >> c.shift] : key >> c.shift;
-          const int64_t number = page_number(c, pages.table[page]);
-          return c.v + (((number * c.heads + head) << c.shift) + (key & ((1 << c.shift) - 1))) * D;
-        }, g);
-    };
-    load(0, (lds_char*)ring);
-    for (int block = 0; block < here; block += 2) {
-      step(block, std::integral_constant<int, 0>{});
-      if (block + 1 < here) step(block + 1, std::integral_constant<int, 1>{});
-    }
-    const bool whole = here == blocks;
-    const int64_t slot = 2 * (int64_t)wave + (block0 > 0 ? 0 : 1);
-    write_rows(g, scale, a, p, rows, group, head, shared ? 1 : a.shared > 0 ? 0 : -1,
-               whole ? nullptr : p.wave_stat + slot * 32, p.wave_sums + slot * 32 * D);
-  }
+template <int D, int R>
+void launch_as(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan, const Partials& p,
+               const UnitArgs& u, hipStream_t stream) {
+  if (a.list) hipLaunchKernelGGL((attend_waves_kernel<D, R, true>), dim3(plan.waves), dim3(64), 0, stream, a, c, s, u, p);
+  else hipLaunchKernelGGL((attend_waves_kernel<D, R, false>), dim3(plan.waves), dim3(64), 0, stream, a, c, s, u, p);
 }
 
 template <int D>
 void launch(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan, const Partials& p,
             const UnitArgs& u, hipStream_t stream) {
-  if (a.list) hipLaunchKernelGGL((attend_waves_kernel<D, true>), dim3(plan.waves), dim3(64), 0, stream, a, c, s, u, p);
-  else hipLaunchKernelGGL((attend_waves_kernel<D, false>), dim3(plan.waves), dim3(64), 0, stream, a, c, s, u, p);
+  if (plan.rows == 16) launch_as<D, 16>(a, c, s, plan, p, u, stream);
+  else launch_as<D, 32>(a, c, s, plan, p, u, stream);
 }
 
 }  // namespace

@@ -156,7 +156,7 @@ int awq_attend_pages(const void* q, int32_t ldq, const int32_t* offsets, const i
   if (!stride_ok(ldq, row) || !stride_ok(ldy, row)) return AWQ_ERR_SHAPE;
   if (!(scale > 0.0f) || isinf(scale)) return AWQ_ERR_OPTION;
   if (count < 1 || (int64_t)count * page_size > ((int64_t)1 << 30) ||
-      (int64_t)T * kv_heads * ((q_heads / kv_heads + 31) / 32) * ((int64_t)count * page_size / 32 + 1) >= ((int64_t)1 << 30))
+      (int64_t)T * kv_heads * ((q_heads / kv_heads + 15) / 16) * ((int64_t)count * page_size / 32 + 1) >= ((int64_t)1 << 30))
     return AWQ_ERR_OPTION;
   st = check_pointers(q, k_pages, v_pages, y);
   if (st != AWQ_OK) return st;
