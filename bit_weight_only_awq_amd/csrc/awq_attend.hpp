@@ -91,41 +91,46 @@ __device__ __forceinline__ int list_blocks(const UnitArgs& u, int count) { retur
 
 constexpr int64_t kMostUnits = 1 << 30;
 
+constexpr int kNowhere = 1 << 30;  // a place behind every row's (subtracting it stays in 32 bits)
+
 // Rows, numbered token after token, the key head's query heads within one: `first` is the number of the first,
 // `total` how many the sequence has; `place0` and `row0` are of its first token.
 struct Rows {
   int first, total, row0, place0;
 };
 
-// The part of a segment's keys that a wave reads its page numbers for: 64 entries of a table or list, one per lane.
+// The pages of a segment's keys, 64 entries of its table or list at a time, one per lane: where the key head's part of
+// the page begins, and the place of its first token.
 struct Entries {
   const int* table;  // the sequence's
   const int* list;   // or NULL: every page of the table
   int count, width;  // of the list, of the table
-  int first;         // entry of lane 0
-  int page, number;  // the lane's page of the sequence (-1: none) and its number in the cache
+  int head;
+  int first;              // entry of lane 0
+  uint32_t at_lo, at_hi;  // row of the cache
+  int place;
 
   __device__ __forceinline__ void read(const CacheArgs& c, int from) {
     first = from;
     const int e = from + (int)__lane_id();
-    page = list ? (e < count ? list[e] : -1) : e;
+    int page = list ? (e < count ? list[e] : -1) : e;
     if (page < 0 || page >= width) page = -1;
-    number = page_number(c, page >= 0 ? table[page] : 0);
+    const uint64_t at = ((int64_t)page_number(c, page >= 0 ? table[page] : 0) * c.heads + head) << c.shift;
+    at_lo = (uint32_t)at;
+    at_hi = (uint32_t)(at >> 32);
+    place = page < 0 ? kNowhere : page << c.shift;
   }
 };
-
-constexpr int kNowhere = 1 << 30;  // a place behind every row's (subtracting it stays in 32 bits)
 
 // Where 16 keys are, and the place of the first of them in the sequence.
 struct Keys16 {
   int64_t at;  // row of the cache
   int place;
 };
-__device__ __forceinline__ Keys16 keys16(const Entries& e, const CacheArgs& c, int head, int key) {
+__device__ __forceinline__ Keys16 keys16(const Entries& e, const CacheArgs& c, int key) {
   const int lane = (key >> c.shift) - e.first, slot = key & ((1 << c.shift) - 1);
-  const int page = __builtin_amdgcn_readlane(e.page, lane), number = __builtin_amdgcn_readlane(e.number, lane);
-  return Keys16{(((int64_t)number * c.heads + head) << c.shift) + slot,
-                page < 0 ? kNowhere : (page << c.shift) + slot};
+  const uint32_t lo = __builtin_amdgcn_readlane(e.at_lo, lane), hi = __builtin_amdgcn_readlane(e.at_hi, lane);
+  return Keys16{(int64_t)((uint64_t)hi << 32 | (lo + slot)), __builtin_amdgcn_readlane(e.place, lane) + slot};
 }
 
 // The queries of a wave's R rows.

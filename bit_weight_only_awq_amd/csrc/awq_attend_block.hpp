@@ -72,15 +72,35 @@ struct Sources {
   }
 };
 
-// 16 bytes per lane from `base` + the lane's `offset` into LDS, lane after lane.  In assembly, so that the compiler does
-// not wait for it before it reads another part of the ring: the waits (vmcnt) stand where the stages change.  (Nothing
-// comes back into registers.  The ring's address goes in as well: to the compiler this writes to it.)
-__device__ __forceinline__ void load_to_lds(const char* base, uint32_t offset, lds_char* to) {
+// N times 64 times 16 bytes, from `base` + the lane's `offset`s, into LDS from `to` on, lane after lane.  In assembly, so
+// that the compiler does not wait for it before it reads another part of the ring: the waits (vmcnt) stand where the
+// blocks change.  (Nothing comes back into registers.  The ring's address goes in as well: to the compiler this writes
+// to it.)
+template <int N>
+__device__ __forceinline__ void load_to_lds(const char* base, const uint32_t (&offset)[N], lds_char* to) {
+  static_assert(N == 2 || N == 3 || N == 4, "loads of 16 rows, or half of them");
   uint32_t kept;
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
-               : "=&s"(kept)
-               : "s"(to), "v"(offset), "s"(base)
-               : "memory");
+  if constexpr (N == 2)
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %2\n\t"
+                 "s_add_u32 m0, m0, 1024\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(kept)
+                 : "s"(to), "s"(base), "v"(offset[0]), "v"(offset[1])
+                 : "memory", "scc");
+  if constexpr (N == 3)
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %2\n\t"
+                 "s_add_u32 m0, m0, 1024\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %2\n\t"
+                 "s_add_u32 m0, m0, 1024\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %5, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(kept)
+                 : "s"(to), "s"(base), "v"(offset[0]), "v"(offset[1]), "v"(offset[2])
+                 : "memory", "scc");
+  if constexpr (N == 4)
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %2\n\t"
+                 "s_add_u32 m0, m0, 1024\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %2\n\t"
+                 "s_add_u32 m0, m0, 1024\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %5, %2\n\t"
+                 "s_add_u32 m0, m0, 1024\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %6, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(kept)
+                 : "s"(to), "s"(base), "v"(offset[0]), "v"(offset[1]), "v"(offset[2]), "v"(offset[3])
+                 : "memory", "scc");
 }
 // (the count is of loads, in the order of their issue)
 template <int N>
@@ -302,17 +322,29 @@ __device__ __forceinline__ half8_t value_part(const Addresses<D, R>& at) {
 
 constexpr int kAhead = 4;  // fragments on their way from LDS
 
-// Scores of 32 keys, K bytes behind the lane's addresses.  beside(j): vector instructions for after matrix instruction j.
-template <int D, int R, int K, typename Beside>
-__device__ __forceinline__ Scores<R> scores_of(const Addresses<D, R>& at, const Queries<D, R>& q, Beside beside) {
-  using P = Products<D, R>;
-  Scores<R> s{};
+struct Fragments {
   half8_t k[kAhead], x[kAhead];
+};
+template <int D, int R, int K>
+__device__ __forceinline__ Fragments first_keys(const Addresses<D, R>& at, const Queries<D, R>& q) {
+  Fragments f;
   each<0, kAhead, 1>([&](auto jc) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value;
-    k[j] = key_part<D, R, K, j>(at);
-    x[j] = query_part<D, R, j>(q);
+    f.k[j] = key_part<D, R, K, j>(at);
+    f.x[j] = query_part<D, R, j>(q);
   });
+  return f;
+}
+
+// Scores of 32 keys, K bytes behind the lane's addresses, the first fragments on their way.  beside(j): vector
+// instructions for after matrix instruction j.
+template <int D, int R, int K, typename Beside>
+__device__ __forceinline__ Scores<R> scores_of(const Addresses<D, R>& at, const Queries<D, R>& q, Fragments& f,
+                                               Beside beside) {
+  using P = Products<D, R>;
+  Scores<R> s{};
+  auto& k = f.k;
+  auto& x = f.x;
   in_order();
   each<0, P::SCORES, 1>([&](auto jc) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value, n = j % kAhead;
@@ -402,7 +434,8 @@ template <int D, int R, int K, int V>
 __device__ __forceinline__ Weights<R> attend_block(const Addresses<D, R>& at, const Queries<D, R>& q, float c,
                                                    const Seen& seen, Gathered<D, R>& g) {
   half8_t v[kAhead];
-  Scores<R> s = scores_of<D, R, K>(at, q, [&](auto jc) __attribute__((always_inline)) {
+  Fragments f = first_keys<D, R, K>(at, q);
+  Scores<R> s = scores_of<D, R, K>(at, q, f, [&](auto jc) __attribute__((always_inline)) {
     if constexpr (decltype(jc)::value == Products<D, R>::SCORES - 1) first_values<D, R, V>(at, v);
   });
   const float base = settle<D, R>(s, greatest(s), c, seen, g);
@@ -415,19 +448,19 @@ __device__ __forceinline__ Weights<R> attend_block(const Addresses<D, R>& at, co
 }
 
 // The same, a block ahead with the scores: the weights of the block whose scores are `s`, with values V bytes behind the
-// lane's addresses, beside the products for the next block's scores (keys K bytes behind), and the greatest of
-// those, `m`, beside the products with the values.
+// lane's addresses, beside the products for the next block's scores (keys K bytes behind, the first fragments on their
+// way), and the greatest of those, `m`, beside the products with the values.
 template <int D, int R, int K, int V>
-__device__ __forceinline__ Weights<R> attend_next(const Addresses<D, R>& at, const Queries<D, R>& q, float c,
+__device__ __forceinline__ Weights<R> attend_next(const Addresses<D, R>& at, const Queries<D, R>& q, Fragments& f, float c,
                                                   const Seen& seen, Scores<R>& s, float& m, Gathered<D, R>& g) {
   constexpr int N = Products<D, R>::SCORES, M = Products<D, R>::VALUES, PAIRS = Scores<R>::COUNT / 2;
   half8_t v[kAhead];
   Weights<R> p;
   const float base = settle<D, R>(s, m, c, seen, g);
   in_order();
-  Scores<R> next = scores_of<D, R, K>(at, q, [&](auto jc) __attribute__((always_inline)) {
+  Scores<R> next = scores_of<D, R, K>(at, q, f, [&](auto jc) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value;
-    if constexpr (j == N - 1) first_values<D, R, V>(at, v);
+    if constexpr (j == N - 2) first_values<D, R, V>(at, v);
 #pragma unroll
     for (int i = PAIRS * j / N; i < PAIRS * (j + 1) / N; ++i) p.take(i, s, c, base);
   });

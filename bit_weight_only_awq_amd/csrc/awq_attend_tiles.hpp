@@ -107,22 +107,23 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
 
   // this wave's loads of a block: of keys or of values, one group of 16 of them
   const int sixteen = wave & 1, of_values = wave >> 1;
-  uint32_t lane_from[LOADS];
+  constexpr int PER = LOADS < 4 ? LOADS : 4;  // loads at once
+  uint32_t lane_from[LOADS / PER][PER];
   {
     const Sources<D> sources(lane, 0);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) lane_from[i] = of_values ? sources.value(i) : sources.key(i);
+    for (int i = 0; i < LOADS; ++i) lane_from[i / PER][i % PER] = of_values ? sources.value(i) : sources.key(i);
   }
   const Addresses<D, 32> places((uint32_t)(uintptr_t)ring, lane);
-  Entries pages{s.tables + (int64_t)seq.index * s.width, nullptr, 0, s.width, 0, 0, 0};
+  Entries pages{s.tables + (int64_t)seq.index * s.width, nullptr, 0, s.width, head, 0, 0, 0, 0};
   auto load = [&](int block, int slot) __attribute__((always_inline)) {
     const int key = key0 + 32 * block;
     if (block == from || ((key + 16) >> c.shift) - pages.first >= 64) pages.read(c, key >> c.shift);
-    const Keys16 source = keys16(pages, c, head, key + 16 * sixteen);
+    const Keys16 source = keys16(pages, c, key + 16 * sixteen);
     const char* base = reinterpret_cast<const char*>((of_values ? c.v : c.k) + source.at * D);
     lds_char* to = ring + (2 * slot + of_values) * SLOT + 16 * sixteen * T::ROW;
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) load_to_lds(base, lane_from[i], to + 1024 * i);
+    for (int i = 0; i < LOADS / PER; ++i) load_to_lds<PER>(base, lane_from[i], to + 1024 * PER * i);
   };
   auto meet = [&]() __attribute__((always_inline)) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -163,7 +164,8 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
       for (int i = 0; i < 3; ++i) load(min(from + i, to - 1), i);
       wait_loads<2 * LOADS>();
       meet();
-      s_now = scores_of<D, 32, 0>(places, q, [](auto) __attribute__((always_inline)) {});
+      Fragments f = first_keys<D, 32, 0>(places, q);
+      s_now = scores_of<D, 32, 0>(places, q, f, [](auto) __attribute__((always_inline)) {});
       m_now = greatest(s_now);
     }
     // One block: its scores are there, the next block's are made; the one after that may still be on its way, and the
@@ -172,10 +174,11 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
       constexpr int HERE = decltype(slot)::value, NEXT = (HERE + 1) % 4;
       wait_loads<LOADS>();
       meet();
+      Fragments f = first_keys<D, 32, 2 * NEXT * SLOT>(places, q);
       load(min(block + 3, to - 1), (HERE + 3) % 4);
       const uint32_t odd = hide(block, HERE);
       const Seen seen = seen_of(block);
-      const Weights<32> p = attend_next<D, 32, 2 * NEXT * SLOT, (2 * HERE + 1) * SLOT>(places, q, scale, seen, s_now, m_now, g);
+      const Weights<32> p = attend_next<D, 32, 2 * NEXT * SLOT, (2 * HERE + 1) * SLOT>(places, q, f, scale, seen, s_now, m_now, g);
       finish(block, odd, p, seen);
     };
     for (int block = from; block < to; block += 4)

@@ -25,7 +25,7 @@ template <int D, int R, bool LIST>
 __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const UnitArgs& units,
                                             const Partials& p, int wave, lds_char* ring, lds_char* queries) {
   using T = Tile<D>;
-  constexpr int LOADS = T::LOADS;
+  constexpr int LOADS = T::LOADS, PER = LOADS < 4 ? LOADS : 4;
   constexpr int SLOT = 32 * T::ROW;  // keys, then values, of a block
   const int lane = threadIdx.x & 63, group = units.group;
   const float scale = a.scale * kLog2E;
@@ -91,7 +91,7 @@ __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs
       list = a.list + ((int64_t)seq.row0 * c.heads + head) * a.count;
       count = a.count;
     }
-    Entries pages{s.tables + (int64_t)seq.index * s.width, list, count, s.width, 0, 0, 0};
+    Entries pages{s.tables + (int64_t)seq.index * s.width, list, count, s.width, head, 0, 0, 0, 0};
 
     Queries<D, R> q;
     q.place(queries);
@@ -107,14 +107,19 @@ __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs
       asm volatile("" : "+v"(from_lane.keys[0]), "+v"(from_lane.values[0]));  // (each load's is formed here, not kept)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const Keys16 from = keys16(pages, c, head, key + 16 * h);
+        const Keys16 from = keys16(pages, c, key + 16 * h);
         (h ? next1 : next0) = from.place;
-        const char* k = reinterpret_cast<const char*>(c.k + from.at * D);
-        const char* v = reinterpret_cast<const char*>(c.v + from.at * D);
+        each<0, LOADS, PER>([&](auto ic) __attribute__((always_inline)) {
+          constexpr int i = decltype(ic)::value;
+          uint32_t k[PER], v[PER];
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load_to_lds(k, from_lane.key(i), to + 16 * h * T::ROW + 1024 * i);
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) load_to_lds(v, from_lane.value(i), to + SLOT + 16 * h * T::ROW + 1024 * i);
+          for (int n = 0; n < PER; ++n) {
+            k[n] = from_lane.key(i + n);
+            v[n] = from_lane.value(i + n);
+          }
+          load_to_lds<PER>(reinterpret_cast<const char*>(c.k + from.at * D), k, to + 16 * h * T::ROW + 1024 * i);
+          load_to_lds<PER>(reinterpret_cast<const char*>(c.v + from.at * D), v, to + SLOT + 16 * h * T::ROW + 1024 * i);
+        });
       }
     };
     auto step = [&](int block, auto parity) __attribute__((always_inline)) {
