@@ -108,6 +108,10 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// The larger of two, NaN if either is: one instruction for three numbers, where the maximum that passes NaN over takes
+// one more for each.  (A row with a NaN among its scores is NaN, whatever its maximum.)
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // Greatest and sum over the lanes that share a row (R rows: lane % R).
 template <int R>
 __device__ __forceinline__ float row_max(float v) {
@@ -115,12 +119,12 @@ __device__ __forceinline__ float row_max(float v) {
     const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false,
                                                     false);
     const uint32_t r0 = r[0], r1 = r[1];
-    v = fmaxf(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
+    v = larger(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
   }
   const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false,
                                                   false);
   const uint32_t r0 = r[0], r1 = r[1];
-  return fmaxf(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
+  return larger(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
 }
 template <int R>
 __device__ __forceinline__ float row_sum(float v) {
@@ -366,7 +370,7 @@ template <int R>
 __device__ __forceinline__ float greatest(const Scores<R>& s) {
   float m = s.get(0);
 #pragma unroll
-  for (int i = 1; i < Scores<R>::COUNT; ++i) m = fmaxf(m, s.get(i));
+  for (int i = 1; i < Scores<R>::COUNT; ++i) m = larger(m, s.get(i));
   return row_max<R>(m);
 }
 
@@ -384,7 +388,7 @@ __device__ __forceinline__ float settle(Scores<R>& s, float m, float c, const Se
     m = greatest(s);
   }
   if (__any((m - g.top) * c > kLag)) {  // (a first score: infinitely above; none yet: NaN, no)
-    const float top = fmaxf(m, g.top);
+    const float top = m > g.top ? m : g.top;
     const float carry = g.top == top ? 1.0f : __builtin_amdgcn_exp2f((g.top - top) * c);
     g.top = top;
     g.sum *= carry;
@@ -469,7 +473,7 @@ __device__ __forceinline__ Weights<R> attend_next(const Addresses<D, R>& at, con
   gather<D, R, V>(at, v, p, g, [&](auto ic) __attribute__((always_inline)) {
     constexpr int i = decltype(ic)::value;
 #pragma unroll
-    for (int n = PAIRS * i / M; n < PAIRS * (i + 1) / M; ++n) most = fmaxf(most, fmaxf(next.get(2 * n), next.get(2 * n + 1)));
+    for (int n = PAIRS * i / M; n < PAIRS * (i + 1) / M; ++n) most = larger(larger(most, next.get(2 * n)), next.get(2 * n + 1));
   });
   s = next;
   m = row_max<R>(most);
