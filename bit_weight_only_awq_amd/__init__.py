@@ -809,51 +809,62 @@ def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 32, boun
     return KvCache(k, v, torch.empty((pages, kv_heads, 2, head_dim), dtype=torch.float16, device=device) if bounds else None)
 
 
+def _beside(t: Optional[torch.Tensor], shape, dtype, device: int, what: str) -> Optional[int]:
+    """Address of a contiguous tensor of a given shape and type on the GPU of the rows (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{what} must be a {str(dtype).split('.')[-1]} tensor of shape {tuple(shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must live on the GPU of the rows")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
 def _cache_call(x: torch.Tensor, cache: KvCache, seqs: Sequences, extra: int, what: str):
-    """(row address, row stride, the batch's arguments, those of the pages) of rows ``x`` that hold ``extra`` vectors
-    per key head beside the queries' (keys and values); everything on one device, which is the current one for the
-    call."""
+    """(device, row address, row stride, the batch's arguments, those of the pages) of rows ``x`` that hold ``extra``
+    vectors per key head beside the queries' (keys and values); everything on the rows' device, which is the current
+    one for the call."""
     k, v, bounds = cache
     offsets, lengths, tables = seqs
     pages, kv_heads, page_size, dim = shape = k.shape
-    if k.dtype is not _F16 or v.dtype is not _F16 or v.shape != shape:
+    if v.shape != shape:
         raise ValueError("the cache's keys and values must be float16 tensors [pages, kv_heads, page_size, head_dim]")
     if x.dim() != 2 or x.shape[1] % dim:
         raise ValueError(f"{what} must be a float16 tensor [T, heads * {dim}]")
-    heads = x.shape[1] // dim - extra * kv_heads
+    T, width = x.shape
+    heads = width // dim - extra * kv_heads
     if heads < 1 or heads % kv_heads:
         raise ValueError(f"{what} must hold a multiple of {kv_heads} query heads")
-    xp, ldx = _rows2d(x, None, x.shape[1], what)
-    B, device = lengths.shape[0], x.device
+    xp, ldx = _rows2d(x, None, width, what)
+    B, device = lengths.shape[0], x.get_device()
     if tables.dim() != 2:
         raise ValueError("seqs.tables must be an int32 tensor [B, width]")
-    if not (k.device == v.device == offsets.device == lengths.device == tables.device == device):
-        raise ValueError("the cache, the sequences and the rows must live on one GPU")
-    batch = (_flat(offsets, (B + 1,), _I32, "seqs.offsets"), _flat(lengths, (B,), _I32, "seqs.lengths"),
-             _flat(tables, (B, tables.shape[1]), _I32, "seqs.tables"), tables.shape[1], x.shape[0], B, heads, kv_heads,
-             dim)
-    return xp, ldx, batch, (_ptr(k), _ptr(v), pages, page_size)
+    columns = tables.shape[1]
+    batch = (_beside(offsets, (B + 1,), _I32, device, "seqs.offsets"),
+             _beside(lengths, (B,), _I32, device, "seqs.lengths"),
+             _beside(tables, (B, columns), _I32, device, "seqs.tables"), columns, T, B, heads, kv_heads, dim)
+    return device, xp, ldx, batch, (_beside(k, shape, _F16, device, "cache.k"),
+                                    _beside(v, shape, _F16, device, "cache.v"), pages, page_size)
 
 
-def _page_bounds(cache: KvCache) -> Optional[int]:
-    if cache.bounds is None:
-        return None
-    if cache.bounds.device != cache.k.device:
-        raise ValueError("the cache must live on one GPU")
+def _page_bounds(cache: KvCache, device: int) -> Optional[int]:
     pages, kv_heads, _, dim = cache.k.shape
-    return _flat(cache.bounds, (pages, kv_heads, 2, dim), _F16, "cache.bounds")
+    return _beside(cache.bounds, (pages, kv_heads, 2, dim), _F16, device, "cache.bounds")
 
 
-def _beside(t: Optional[torch.Tensor], x: torch.Tensor, what: str) -> None:
-    if t is not None and t.device != x.device:
-        raise ValueError(f"{what} must live on the GPU of the rows")
+def _workspace_beside(workspace: Optional[torch.Tensor], device: int) -> None:
+    if workspace is not None and workspace.get_device() != device:
+        raise ValueError("workspace must live on the GPU of the rows")
 
 
 def _output(y: Optional[torch.Tensor], x: torch.Tensor, width: int, what: str):
     if y is None:
         out = x.new_empty((x.shape[0], width))
         return out, out.data_ptr(), width
-    _beside(y, x, what)
+    if y.get_device() != x.get_device():
+        raise ValueError(f"{what} must live on the GPU of the rows")
     return (y, *_rows2d(y, x.shape[0], width, what))
 
 
@@ -867,21 +878,20 @@ def append_kv(qkv: torch.Tensor, cache: KvCache, seqs: Sequences, inv_freq: Opti
     sequence.  With several axes ``axes`` (int32 [R / 2]) says which one pair i turns by.  Pairs are channels
     (i, R / 2 + i), or (2 i, 2 i + 1) with ``interleaved``.  ``q`` may be the queries' columns of ``qkv``."""
     lib = _lib or load_library()
-    xp, ldx, batch, (kp, vp, pages, page_size) = _cache_call(qkv, cache, seqs, 2, "qkv")
-    bp = _page_bounds(cache)
+    device, xp, ldx, batch, (kp, vp, pages, page_size) = _cache_call(qkv, cache, seqs, 2, "qkv")
+    bp = _page_bounds(cache, device)
     width = batch[6] * batch[8]
     out, qp, ldq = _output(q, qkv, width, "q")
     T, count = qkv.shape[0], 1
     half = 0 if inv_freq is None else inv_freq.shape[0]
-    fp = _flat(inv_freq, (half,), _F32, "inv_freq")
-    if positions is not None:
-        count = 1 if positions.dim() == 1 else positions.shape[1]
-    pp = _flat(positions, (T,) if positions is not None and positions.dim() == 1 else (T, count), _I32, "positions")
-    ap = _flat(axes, (half,), _I32, "axes")
-    for t, what in ((inv_freq, "inv_freq"), (positions, "positions"), (axes, "axes")):
-        _beside(t, qkv, what)
+    shape = (T,)
+    if positions is not None and positions.dim() == 2:
+        shape = (T, count := positions.shape[1])
+    fp = _beside(inv_freq, (half,), _F32, device, "inv_freq")
+    pp = _beside(positions, shape, _I32, device, "positions")
+    ap = _beside(axes, (half,), _I32, device, "axes")
     if T > 0:
-        with _device_of(qkv):
+        with _device_of(device):
             st = lib.awq_append_kv(xp, ldx, *batch, fp, 2 * half, interleaved, pp, count, ap, qp, ldq, kp, vp, bp, pages,
                                    page_size, _handle(qkv))
         _check(st, "awq_append_kv")
@@ -899,22 +909,22 @@ class _Here:
 _HERE = _Here()
 
 
-def _device_of(t: torch.Tensor):
-    """The tensor's device as the current one, for a launch; nothing to do where it is already."""
-    return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+def _device_of(device: int):
+    """The device as the current one, for a launch; nothing to do where it is already."""
+    return _HERE if device == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _attend_rows(name: str, q, cache, seqs, scale, y, workspace, options, shape):
     """awq_attend and awq_attend_pages: ``options`` between the scale and the pages, ``shape`` of the workspace."""
     lib = _lib or load_library()
-    qp, ldq, batch, (kp, vp, pages, page_size) = _cache_call(q, cache, seqs, 0, "q")
-    _beside(workspace, q, "workspace")
+    device, qp, ldq, batch, (kp, vp, pages, page_size) = _cache_call(q, cache, seqs, 0, "q")
+    _workspace_beside(workspace, device)
     out, yp, ldy = _output(y, q, q.shape[1], "y")
     if scale is None:
         scale = batch[8] ** -0.5
     if q.shape[0] > 0:
         call, stream = getattr(lib, name), _handle(q)
-        with _device_of(q):
+        with _device_of(device):
             _with_workspace(
                 lambda ws, n: call(qp, ldq, *batch, scale, *options, kp, vp, pages, page_size, yp, ldy, ws, n, stream),
                 lambda: _bytes_of(name, *shape(batch, page_size)), name, workspace, q)
@@ -938,18 +948,18 @@ def select_pages(q: torch.Tensor, cache: KvCache, seqs: Sequences, count: int, f
     -1 past the last: all of them up to the token's place if they are at most ``count``, or else the ``first`` first,
     the ``recent`` last, and those between whose bounds allow the largest products with the queries."""
     lib = _lib or load_library()
-    qp, ldq, batch, (_, _, pages, page_size) = _cache_call(q, cache, seqs, 0, "q")
-    _beside(workspace, q, "workspace")
+    device, qp, ldq, batch, (_, _, pages, page_size) = _cache_call(q, cache, seqs, 0, "q")
+    _workspace_beside(workspace, device)
     if cache.bounds is None:
         raise ValueError("select_pages needs a cache with bounds")
-    bp = _page_bounds(cache)
+    bp = _page_bounds(cache, device)
     if not 1 <= count < 1 << 31:
         raise AwqError(AWQ_ERR_OPTION, "awq_select_pages")
     T, kv_heads = q.shape[0], batch[7]
     out = q.new_empty((T, kv_heads, count), dtype=_I32)
     if T > 0:
         stream = _handle(q)
-        with _device_of(q):
+        with _device_of(device):
             _with_workspace(
                 lambda ws, n: lib.awq_select_pages(qp, ldq, *batch, bp, pages, page_size, count, first, recent,
                                                    out.data_ptr(), ws, n, stream),
@@ -963,10 +973,9 @@ def attend_pages(q: torch.Tensor, cache: KvCache, seqs: Sequences, pages: torch.
     sequence's pages: each at most once, negative ones last), up to each token's place."""
     if pages.dim() != 3 or pages.shape[:2] != (q.shape[0], cache.k.shape[1]):
         raise ValueError("pages must be an int32 tensor [T, kv_heads, count]")
-    _beside(pages, q, "pages")
     count = pages.shape[2]
     return _attend_rows("awq_attend_pages", q, cache, seqs, scale, y, workspace,
-                        (_flat(pages, pages.shape, _I32, "pages"), count),
+                        (_beside(pages, pages.shape, _I32, q.get_device(), "pages"), count),
                         lambda b, size: (b[4], b[6], b[7], b[8], size, count))
 
 
