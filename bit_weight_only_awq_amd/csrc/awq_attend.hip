@@ -113,6 +113,20 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
         stat = p.stat[from];
       }
     }
+    // (the first values are on their way while the maxima are compared, and the next while some are added)
+    const int here = min(64, parts - i0);
+    float4_t v[AHEAD];
+    const auto load = [&](int k0) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const int of = k0 + k * GROUPS + lane / LANES, where = __shfl(from, of & 63);
+        v[k] = float4_t(0.0f);
+        if (of < here && live)
+          v[k] = *reinterpret_cast<const float4_t*>(
+              (where < 0 ? p.wave_sums + (int64_t)(-1 - where) * D : p.sums + (int64_t)where * D) + channel);
+      }
+    };
+    load(0);
     float m = stat.x;
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
@@ -126,22 +140,17 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
     total = total * carry + sum;
     if (i0 > 0) sums *= carry;
     top = m;
-    const int here = min(64, parts - i0);
     for (int k0 = 0; k0 < here; k0 += AHEAD * GROUPS) {
-      float4_t v[AHEAD];
-      float by[AHEAD];
+      float4_t w[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) w[k] = v[k];
+      if (k0 + AHEAD * GROUPS < here) load(k0 + AHEAD * GROUPS);
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
-        const int of = k0 + k * GROUPS + lane / LANES, where = __shfl(from, of & 63);
-        by[k] = __shfl(share, of & 63);
-        v[k] = float4_t(0.0f);
-        if (of >= here) by[k] = 0.0f;
-        else if (live)
-          v[k] = *reinterpret_cast<const float4_t*>(
-              (where < 0 ? p.wave_sums + (int64_t)(-1 - where) * D : p.sums + (int64_t)where * D) + channel);
+        const int of = k0 + k * GROUPS + lane / LANES;
+        const float by = __shfl(share, of & 63);
+        sums += w[k] * (of < here ? by : 0.0f);
       }
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k) sums += v[k] * by[k];
     }
   }
 #pragma unroll
