@@ -176,15 +176,23 @@ __global__ __launch_bounds__(256) void join_slices_kernel(AttendArgs a, SeqArgs 
   float4_t sums = float4_t(0.0f);
   float top = -INFINITY, total = 0.0f;
   bool placed = true;
+  float2 next_stat[AHEAD];
+  float4_t next_part[AHEAD];
+  const auto load = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {  // (past the last slice: the last again, counted as nothing)
+      const int64_t from = min(i0 + i, slices - 1) * p.rows + row;
+      next_stat[i] = p.stat[from];
+      next_part[i] = *reinterpret_cast<const float4_t*>(p.sums + from * D + channel);
+    }
+  };
+  load(0);
   for (int i0 = 0; i0 < slices; i0 += AHEAD) {
     float2 stat[AHEAD];
     float4_t part[AHEAD];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {  // (past the last slice: the last again, counted as nothing)
-      const int64_t from = min(i0 + i, slices - 1) * p.rows + row;
-      stat[i] = p.stat[from];
-      part[i] = *reinterpret_cast<const float4_t*>(p.sums + from * D + channel);
-    }
+    for (int i = 0; i < AHEAD; ++i) stat[i] = next_stat[i], part[i] = next_part[i];
+    if (i0 + AHEAD < slices) load(i0 + AHEAD);
     float m = top;
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {

@@ -151,6 +151,35 @@ struct Scores<16> {
   __device__ __forceinline__ void put(int i, float v) { s[i >> 2][i & 3] = v; }
 };
 
+// Where a head is 256 wide, the sums stay in the accumulator half of the registers, which only matrix instructions work
+// in: left to itself the compiler moves all of them to the other half and back for every block, because now and then
+// they are scaled.  `apart` stands between matrix instructions and those that touch single sums: it waits for the
+// former's results (at most 19 cycles after one of 16 passes) and for the latter's.
+template <int N, typename V>
+__device__ __forceinline__ void apart(V (&sums)[N]) {
+  if constexpr (N == 8)
+    asm volatile("s_nop 15\n\ts_nop 7"
+                 : "+a"(sums[0]), "+a"(sums[1]), "+a"(sums[2]), "+a"(sums[3]), "+a"(sums[4]), "+a"(sums[5]), "+a"(sums[6]),
+                   "+a"(sums[7]));
+  else {
+    static_assert(N == 16, "256 channels");
+    asm volatile("s_nop 15\n\ts_nop 7"
+                 : "+a"(sums[0]), "+a"(sums[1]), "+a"(sums[2]), "+a"(sums[3]), "+a"(sums[4]), "+a"(sums[5]), "+a"(sums[6]),
+                   "+a"(sums[7]), "+a"(sums[8]), "+a"(sums[9]), "+a"(sums[10]), "+a"(sums[11]), "+a"(sums[12]),
+                   "+a"(sums[13]), "+a"(sums[14]), "+a"(sums[15]));
+  }
+}
+__device__ __forceinline__ float scaled_apart(float sum, float by) {
+  float t;
+  asm("v_accvgpr_read_b32 %1, %0\n\tv_mul_f32 %1, %1, %2\n\tv_accvgpr_write_b32 %0, %1" : "+a"(sum), "=&v"(t) : "v"(by));
+  return sum;
+}
+__device__ __forceinline__ float added_apart(float sum, float x) {
+  float t;
+  asm("v_accvgpr_read_b32 %1, %0\n\tv_add_f32 %1, %1, %2\n\tv_accvgpr_write_b32 %0, %1" : "+a"(sum), "=&v"(t) : "v"(x));
+  return sum;
+}
+
 template <int D, int R>
 struct Gathered;
 template <int D>
@@ -159,10 +188,25 @@ struct Gathered<D, 32> {
   float16_t sums[D / 32];
   float top, sum;  // the maximum; the lane's share of l
   __device__ __forceinline__ float get(int n, int i) const { return sums[n >> 2][4 * (n & 3) + i]; }
-  __device__ __forceinline__ void add(int n, int i, float v) { sums[n >> 2][4 * (n & 3) + i] += v; }
+  __device__ __forceinline__ void pause() {
+    if constexpr (D == 256) apart(sums);
+  }
+  __device__ __forceinline__ void add(int n, int i, float v) {
+    const float sum = get(n, i);
+    sums[n >> 2][4 * (n & 3) + i] = D == 256 ? added_apart(sum, v) : sum + v;
+  }
   __device__ __forceinline__ void scale(float by) {
+    pause();
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b) sums[b] *= by;
+    for (int b = 0; b < D / 32; ++b) {
+      if constexpr (D < 256) {
+        sums[b] *= by;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sums[b][i] = scaled_apart(sums[b][i], by);
+      }
+    }
+    pause();
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -177,10 +221,24 @@ struct Gathered<D, 16> {
   float4_t sums[QUADS];
   float top, sum;
   __device__ __forceinline__ float get(int n, int i) const { return sums[n][i]; }
-  __device__ __forceinline__ void add(int n, int i, float v) { sums[n][i] += v; }
+  __device__ __forceinline__ void pause() {
+    if constexpr (D == 256) apart(sums);
+  }
+  __device__ __forceinline__ void add(int n, int i, float v) {
+    sums[n][i] = D == 256 ? added_apart(sums[n][i], v) : sums[n][i] + v;
+  }
   __device__ __forceinline__ void scale(float by) {
+    pause();
 #pragma unroll
-    for (int n = 0; n < QUADS; ++n) sums[n] *= by;
+    for (int n = 0; n < QUADS; ++n) {
+      if constexpr (D < 256) {
+        sums[n] *= by;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[n][i] = scaled_apart(sums[n][i], by);
+      }
+    }
+    pause();
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -191,21 +249,25 @@ struct Gathered<D, 16> {
 };
 
 // Fragments of R rows' queries: row lane % R, channels 8 (64 / R) j + 8 (lane / R) .. + 7.  Where a head is 256 wide,
-// those of 32 rows are in LDS, a wave's 64 times 16 bytes for each j (in registers with everything else, they would
-// not all fit).
+// all but the first four of 32 rows are in LDS, a wave's 64 times 16 bytes for each j (in registers with everything
+// else, they would not all fit; and with the four, there would not be room for three blocks of keys and values).
 template <int D, int R>
 struct Queries {
-  static constexpr int BYTES = 0, PARTS = D * R / 512;  // of LDS, for a wave
+  static constexpr int BYTES = 0, PARTS = D * R / 512, KEPT = PARTS;  // BYTES: of LDS, for a wave
   half8_t part[PARTS];
   __device__ __forceinline__ void place(lds_char*) {}
   __device__ __forceinline__ void put(int j, half8_t v) { part[j] = v; }
 };
 template <>
 struct Queries<256, 32> {
-  static constexpr int BYTES = 16 * 1024, PARTS = 16;
+  static constexpr int PARTS = 16, KEPT = 4, BYTES = 1024 * (PARTS - KEPT);
+  half8_t part[KEPT];
   lds_char* at;
   __device__ __forceinline__ void place(lds_char* to) { at = to + 16 * __lane_id(); }
-  __device__ __forceinline__ void put(int j, half8_t v) { *(AWQ_LDS half8_t*)(at + 1024 * j) = v; }
+  __device__ __forceinline__ void put(int j, half8_t v) {
+    if (j < KEPT) part[j] = v;
+    else *(AWQ_LDS half8_t*)(at + 1024 * (j - KEPT)) = v;
+  }
 };
 
 // Which of a block's keys the rows see: those of each 16 up to `limit` (the row's own place, less that of the first
@@ -314,8 +376,9 @@ __device__ __forceinline__ half8_t key_part(const Addresses<D, R>& at) {
 }
 template <int D, int R, int J>
 __device__ __forceinline__ half8_t query_part(const Queries<D, R>& q) {
-  if constexpr (Queries<D, R>::BYTES > 0) return read16<1024 * J>((uint32_t)(uintptr_t)q.at);
-  else return q.part[J % Queries<D, R>::PARTS];
+  constexpr int j = J % Queries<D, R>::PARTS, KEPT = Queries<D, R>::KEPT;
+  if constexpr (j >= KEPT) return read16<1024 * (j - KEPT)>((uint32_t)(uintptr_t)q.at);
+  else return q.part[j];
 }
 template <int D, int R, int V, int I>
 __device__ __forceinline__ half8_t value_part(const Addresses<D, R>& at) {
@@ -486,6 +549,7 @@ template <int D, int R, typename ValueOf>
 __device__ __forceinline__ void gather_strange(uint32_t strange, const Weights<R>& p, const Seen& seen, ValueOf value_of,
                                                Gathered<D, R>& g) {
   const int lane = __lane_id(), row = lane & (R - 1), h = lane / R;
+  g.pause();
 #pragma unroll 1
   while (strange != 0) {
     const int k = __builtin_ctz(strange);
@@ -509,6 +573,7 @@ __device__ __forceinline__ void gather_strange(uint32_t strange, const Weights<R
       in_order();
     }
   }
+  g.pause();
 }
 
 }  // namespace awq

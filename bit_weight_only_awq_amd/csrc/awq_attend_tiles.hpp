@@ -27,7 +27,7 @@ struct TileArgs {
 
 template <int D>
 struct TileRing {
-  static constexpr int BLOCKS = D == 256 ? 2 : 4, BYTES = 2 * BLOCKS * 32 * Tile<D>::ROW;
+  static constexpr int BLOCKS = D == 256 ? 3 : 4, BYTES = 2 * BLOCKS * 32 * Tile<D>::ROW;
 };
 
 // Workgroup number `index` of 256 threads; a ring of TileRing<D>::BYTES, room for the queries where they are in LDS, and
@@ -37,8 +37,8 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
                                             const Partials& p, int index, lds_char* ring, lds_char* queries,
                                             uint32_t* strange) {
   using T = Tile<D>;
-  // Blocks of 32 keys in a ring: where it has four, a block's scores are made beside the weights of the one before
-  // (matrix and vector instructions of one wave), with two blocks on their way; heads of 256 channels leave room for two.
+  // Blocks of 32 keys in a ring: a block's scores are made beside the weights of the one before (matrix and vector
+  // instructions of one wave), with two blocks on their way; heads of 256 channels leave room for one.
   constexpr int RING = TileRing<D>::BLOCKS, LOADS = T::LOADS, SLOT = 32 * T::ROW;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = x.group;
   const float scale = a.scale * kLog2E;
@@ -156,54 +156,37 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
         return c.v + (((number * c.heads + head) << c.shift) + (key & ((1 << c.shift) - 1))) * D;
       }, g);
   };
-  if constexpr (RING == 4) {
-    Scores<32> s_now{};
-    float m_now = 0.0f;
-    if (from < to) {
+  Scores<32> s_now{};
+  float m_now = 0.0f;
+  if (from < to) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) load(min(from + i, to - 1), i);
-      wait_loads<2 * LOADS>();
-      meet();
-      Fragments f = first_keys<D, 32, 0>(places, q);
-      s_now = scores_of<D, 32, 0>(places, q, f, [](auto) __attribute__((always_inline)) {});
-      m_now = greatest(s_now);
-    }
-    // One block: its scores are there, the next block's are made; the one after that may still be on its way, and the
-    // fourth takes the place of the last (past the end, the last block again: its scores count nothing).
-    auto step = [&](int block, auto slot) __attribute__((always_inline)) {
-      constexpr int HERE = decltype(slot)::value, NEXT = (HERE + 1) % 4;
-      wait_loads<LOADS>();
-      meet();
-      Fragments f = first_keys<D, 32, 2 * NEXT * SLOT>(places, q);
-      load(min(block + 3, to - 1), (HERE + 3) % 4);
-      const uint32_t odd = hide(block, HERE);
-      const Seen seen = seen_of(block);
-      const Weights<32> p = attend_next<D, 32, 2 * NEXT * SLOT, (2 * HERE + 1) * SLOT>(places, q, f, scale, seen, s_now, m_now, g);
-      finish(block, odd, p, seen);
-    };
-    for (int block = from; block < to; block += 4)
-      each<0, 4, 1>([&](auto slot) __attribute__((always_inline)) {
-        constexpr int i = decltype(slot)::value;
-        if (block + i < to) step(block + i, slot);
-      });
-    wait_loads<0>();  // (those past the end)
-  } else {
-    auto step = [&](int block, auto slot) __attribute__((always_inline)) {
-      constexpr int HERE = decltype(slot)::value;
-      wait_loads<0>();
-      meet();
-      if (block + 1 < to) load(block + 1, 1 - HERE);
-      const uint32_t odd = hide(block, HERE);
-      const Seen seen = seen_of(block);
-      const Weights<32> p = attend_block<D, 32, 2 * HERE * SLOT, (2 * HERE + 1) * SLOT>(places, q, scale, seen, g);
-      finish(block, odd, p, seen);
-    };
-    if (from < to) load(from, 0);
-    for (int block = from; block < to; block += 2) {
-      step(block, std::integral_constant<int, 0>{});
-      if (block + 1 < to) step(block + 1, std::integral_constant<int, 1>{});
-    }
+    for (int i = 0; i < RING - 1; ++i) load(min(from + i, to - 1), i);
+    wait_loads<(RING - 2) * LOADS>();
+    meet();
+    Fragments f = first_keys<D, 32, 0>(places, q);
+    s_now = scores_of<D, 32, 0>(places, q, f, [](auto) __attribute__((always_inline)) {});
+    m_now = greatest(s_now);
   }
+  // One block: its scores are there, the next block's are made; with a ring of four the one after that may still be on
+  // its way, and the last takes the place of the one before (past the end, the last block again: its scores count
+  // nothing).
+  auto step = [&](int block, auto slot) __attribute__((always_inline)) {
+    constexpr int HERE = decltype(slot)::value, NEXT = (HERE + 1) % RING;
+    wait_loads<(RING - 3) * LOADS>();
+    meet();
+    Fragments f = first_keys<D, 32, 2 * NEXT * SLOT>(places, q);
+    load(min(block + RING - 1, to - 1), (HERE + RING - 1) % RING);
+    const uint32_t odd = hide(block, HERE);
+    const Seen seen = seen_of(block);
+    const Weights<32> p = attend_next<D, 32, 2 * NEXT * SLOT, (2 * HERE + 1) * SLOT>(places, q, f, scale, seen, s_now, m_now, g);
+    finish(block, odd, p, seen);
+  };
+  for (int block = from; block < to; block += RING)
+    each<0, RING, 1>([&](auto slot) __attribute__((always_inline)) {
+      constexpr int i = decltype(slot)::value;
+      if (block + i < to) step(block + i, slot);
+    });
+  wait_loads<0>();  // (those past the end)
   if (live) write_rows(g, scale, a, p, rows, group, head, slice, nullptr, nullptr);
 }
 
