@@ -142,9 +142,8 @@ __device__ __forceinline__ void read_queries(Queries<D, R>& q, const AttendArgs&
                          8 * (lane / R);
 #pragma unroll
   for (int j = 0; j < Queries<D, R>::PARTS; ++j) {
-    half8_t v = *reinterpret_cast<const half8_t*>(from + 512 / R * j);
-    if (!live) v = half8_t((_Float16)0.0f);
-    q.put(j, v);
+    const half8_t v = *reinterpret_cast<const half8_t*>(from + 512 / R * j);
+    q.part[j] = live ? v : half8_t((_Float16)0.0f);
   }
 }
 

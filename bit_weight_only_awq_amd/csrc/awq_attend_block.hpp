@@ -248,26 +248,11 @@ struct Gathered<D, 16> {
   }
 };
 
-// Fragments of R rows' queries: row lane % R, channels 8 (64 / R) j + 8 (lane / R) .. + 7.  Where a head is 256 wide,
-// all but the first four of 32 rows are in LDS, a wave's 64 times 16 bytes for each j (in registers with everything
-// else, they would not all fit; and with the four, there would not be room for three blocks of keys and values).
+// Fragments of R rows' queries: row lane % R, channels 8 (64 / R) j + 8 (lane / R) .. + 7.
 template <int D, int R>
 struct Queries {
-  static constexpr int BYTES = 0, PARTS = D * R / 512, KEPT = PARTS;  // BYTES: of LDS, for a wave
+  static constexpr int PARTS = D * R / 512;
   half8_t part[PARTS];
-  __device__ __forceinline__ void place(lds_char*) {}
-  __device__ __forceinline__ void put(int j, half8_t v) { part[j] = v; }
-};
-template <>
-struct Queries<256, 32> {
-  static constexpr int PARTS = 16, KEPT = 4, BYTES = 1024 * (PARTS - KEPT);
-  half8_t part[KEPT];
-  lds_char* at;
-  __device__ __forceinline__ void place(lds_char* to) { at = to + 16 * __lane_id(); }
-  __device__ __forceinline__ void put(int j, half8_t v) {
-    if (j < KEPT) part[j] = v;
-    else *(AWQ_LDS half8_t*)(at + 1024 * (j - KEPT)) = v;
-  }
 };
 
 // Which of a block's keys the rows see: those of each 16 up to `limit` (the row's own place, less that of the first
@@ -374,12 +359,6 @@ __device__ __forceinline__ half8_t key_part(const Addresses<D, R>& at) {
   constexpr int PARTS = Queries<D, R>::PARTS, KEYS = Addresses<D, R>::KEYS, j = J % PARTS;
   return read16<K + J / PARTS * 16 * Tile<D>::ROW + 256 * (j / KEYS)>(at.key[j % KEYS]);
 }
-template <int D, int R, int J>
-__device__ __forceinline__ half8_t query_part(const Queries<D, R>& q) {
-  constexpr int j = J % Queries<D, R>::PARTS, KEPT = Queries<D, R>::KEPT;
-  if constexpr (j >= KEPT) return read16<1024 * (j - KEPT)>((uint32_t)(uintptr_t)q.at);
-  else return q.part[j];
-}
 template <int D, int R, int V, int I>
 __device__ __forceinline__ half8_t value_part(const Addresses<D, R>& at) {
   constexpr int ROW = Tile<D>::ROW, VALUES = Addresses<D, R>::VALUES;
@@ -390,15 +369,14 @@ __device__ __forceinline__ half8_t value_part(const Addresses<D, R>& at) {
 constexpr int kAhead = 4;  // fragments on their way from LDS
 
 struct Fragments {
-  half8_t k[kAhead], x[kAhead];
+  half8_t k[kAhead];
 };
 template <int D, int R, int K>
-__device__ __forceinline__ Fragments first_keys(const Addresses<D, R>& at, const Queries<D, R>& q) {
+__device__ __forceinline__ Fragments first_keys(const Addresses<D, R>& at) {
   Fragments f;
   each<0, kAhead, 1>([&](auto jc) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value;
     f.k[j] = key_part<D, R, K, j>(at);
-    f.x[j] = query_part<D, R, j>(q);
   });
   return f;
 }
@@ -411,17 +389,14 @@ __device__ __forceinline__ Scores<R> scores_of(const Addresses<D, R>& at, const 
   using P = Products<D, R>;
   Scores<R> s{};
   auto& k = f.k;
-  auto& x = f.x;
   in_order();
   each<0, P::SCORES, 1>([&](auto jc) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value, n = j % kAhead;
-    if constexpr (R == 32) s.s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[n], x[n], s.s, 0, 0, 0);
-    else s.s[j / P::PARTS] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[n], x[n], s.s[j / P::PARTS], 0, 0, 0);
-    if constexpr (j % P::PARTS == 0) outlive(k[n], x[n]);
-    if constexpr (j + kAhead < P::SCORES) {
-      k[n] = key_part<D, R, K, j + kAhead>(at);
-      x[n] = query_part<D, R, j + kAhead>(q);
-    }
+    const half8_t x = q.part[j % P::PARTS];
+    if constexpr (R == 32) s.s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[n], x, s.s, 0, 0, 0);
+    else s.s[j / P::PARTS] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[n], x, s.s[j / P::PARTS], 0, 0, 0);
+    if constexpr (j % P::PARTS == 0) outlive(k[n], x);
+    if constexpr (j + kAhead < P::SCORES) k[n] = key_part<D, R, K, j + kAhead>(at);
     beside(jc);
     in_order();
   });
@@ -501,7 +476,7 @@ template <int D, int R, int K, int V>
 __device__ __forceinline__ Weights<R> attend_block(const Addresses<D, R>& at, const Queries<D, R>& q, float c,
                                                    const Seen& seen, Gathered<D, R>& g) {
   half8_t v[kAhead];
-  Fragments f = first_keys<D, R, K>(at, q);
+  Fragments f = first_keys<D, R, K>(at);
   Scores<R> s = scores_of<D, R, K>(at, q, f, [&](auto jc) __attribute__((always_inline)) {
     if constexpr (decltype(jc)::value == Products<D, R>::SCORES - 1) first_values<D, R, V>(at, v);
   });

@@ -12,9 +12,8 @@ template <int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tiles_kernel(AttendArgs a, CacheArgs c, SeqArgs s, TileArgs x,
                                                                              Partials p) {
   __shared__ __attribute__((aligned(1024))) char ring[TileRing<D>::BYTES];
-  __shared__ __attribute__((aligned(1024))) char queries[Queries<D, 32>::BYTES ? 4 * Queries<D, 32>::BYTES : 16];
   __shared__ uint32_t strange[2];
-  attend_tile<D>(a, c, s, x, p, blockIdx.x, (lds_char*)ring, (lds_char*)queries, strange);
+  attend_tile<D>(a, c, s, x, p, blockIdx.x, (lds_char*)ring, strange);
 }
 
 // The first plan.waves / kWavesOfWorkgroup workgroups are waves on their own (as many of a workgroup's four as the ring
@@ -30,9 +29,9 @@ __global__ __launch_bounds__(256, 2) void attend_both_kernel(AttendArgs a, Cache
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave < kWavesOfWorkgroup)
       attend_wave<D, 16, false>(a, c, s, units, p, blockIdx.x * kWavesOfWorkgroup + wave,
-                            (lds_char*)ring + wave * wave_ring<D>(), nullptr);
+                            (lds_char*)ring + wave * wave_ring<D>());
   } else {
-    attend_tile<D>(a, c, s, x, p, blockIdx.x - first, (lds_char*)ring, nullptr, strange);
+    attend_tile<D>(a, c, s, x, p, blockIdx.x - first, (lds_char*)ring, strange);
   }
 }
 

@@ -27,18 +27,16 @@ struct TileArgs {
 
 template <int D>
 struct TileRing {
-  static constexpr int BLOCKS = D == 256 ? 3 : 4, BYTES = 2 * BLOCKS * 32 * Tile<D>::ROW;
+  static constexpr int BLOCKS = 4, BYTES = 2 * BLOCKS * 32 * Tile<D>::ROW;
 };
 
-// Workgroup number `index` of 256 threads; a ring of TileRing<D>::BYTES, room for the queries where they are in LDS, and
-// two words.
+// Workgroup number `index` of 256 threads; a ring of TileRing<D>::BYTES and two words.
 template <int D>
 __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const TileArgs& x,
-                                            const Partials& p, int index, lds_char* ring, lds_char* queries,
-                                            uint32_t* strange) {
+                                            const Partials& p, int index, lds_char* ring, uint32_t* strange) {
   using T = Tile<D>;
   // Blocks of 32 keys in a ring: a block's scores are made beside the weights of the one before (matrix and vector
-  // instructions of one wave), with two blocks on their way; heads of 256 channels leave room for one.
+  // instructions of one wave), with two blocks on their way.
   constexpr int RING = TileRing<D>::BLOCKS, LOADS = T::LOADS, SLOT = 32 * T::ROW;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = x.group;
   const float scale = a.scale * kLog2E;
@@ -100,7 +98,6 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
   const int least = shared ? a.shared - 1 : rows.place0 + min(rows.first, rows.total - 1) / group;
 
   Queries<D, 32> q;
-  q.place(queries + wave * Queries<D, 32>::BYTES);
   read_queries(q, a, rows, group, head);
   Gathered<D, 32> g;
   g.clear();
@@ -163,18 +160,17 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
     for (int i = 0; i < RING - 1; ++i) load(min(from + i, to - 1), i);
     wait_loads<(RING - 2) * LOADS>();
     meet();
-    Fragments f = first_keys<D, 32, 0>(places, q);
+    Fragments f = first_keys<D, 32, 0>(places);
     s_now = scores_of<D, 32, 0>(places, q, f, [](auto) __attribute__((always_inline)) {});
     m_now = greatest(s_now);
   }
-  // One block: its scores are there, the next block's are made; with a ring of four the one after that may still be on
-  // its way, and the last takes the place of the one before (past the end, the last block again: its scores count
-  // nothing).
+  // One block: its scores are there, the next block's are made; the one after that may still be on its way, and the
+  // fourth takes the place of the last (past the end, the last block again: its scores count nothing).
   auto step = [&](int block, auto slot) __attribute__((always_inline)) {
     constexpr int HERE = decltype(slot)::value, NEXT = (HERE + 1) % RING;
     wait_loads<(RING - 3) * LOADS>();
     meet();
-    Fragments f = first_keys<D, 32, 2 * NEXT * SLOT>(places, q);
+    Fragments f = first_keys<D, 32, 2 * NEXT * SLOT>(places);
     load(min(block + RING - 1, to - 1), (HERE + RING - 1) % RING);
     const uint32_t odd = hide(block, HERE);
     const Seen seen = seen_of(block);

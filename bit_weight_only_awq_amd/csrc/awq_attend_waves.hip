@@ -9,8 +9,7 @@ template <int D, int R, bool LIST>
 __global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(AttendArgs a, CacheArgs c, SeqArgs s,
                                                                             UnitArgs units, Partials p) {
   __shared__ __attribute__((aligned(1024))) char ring[wave_ring<D>()];
-  __shared__ __attribute__((aligned(1024))) char queries[Queries<D, R>::BYTES ? Queries<D, R>::BYTES : 16];
-  attend_wave<D, R, LIST>(a, c, s, units, p, blockIdx.x, (lds_char*)ring, (lds_char*)queries);
+  attend_wave<D, R, LIST>(a, c, s, units, p, blockIdx.x, (lds_char*)ring);
 }
 
 template <int D, int R>

@@ -20,10 +20,10 @@ namespace awq {
 template <int D>
 constexpr int wave_ring() { return 4 * 32 * Tile<D>::ROW; }  // bytes: keys and values of two blocks
 
-// Wave number `wave`; its own ring of wave_ring<D>() bytes, and room for its queries where they are in LDS.
+// Wave number `wave`; its own ring of wave_ring<D>() bytes.
 template <int D, int R, bool LIST>
 __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const UnitArgs& units,
-                                            const Partials& p, int wave, lds_char* ring, lds_char* queries) {
+                                            const Partials& p, int wave, lds_char* ring) {
   using T = Tile<D>;
   constexpr int LOADS = T::LOADS, PER = LOADS < 4 ? LOADS : 4;
   constexpr int SLOT = 32 * T::ROW;  // keys, then values, of a block
@@ -94,7 +94,6 @@ __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs
     Entries pages{s.tables + (int64_t)seq.index * s.width, list, count, s.width, head, 0, 0, 0, 0};
 
     Queries<D, R> q;
-    q.place(queries);
     read_queries(q, a, rows, group, head);
     Gathered<D, R> g;
     g.clear();
