@@ -22,7 +22,7 @@ constexpr int kTile = 128;  // rows of a workgroup
 // `shared_tiles` workgroup rows of the shared keys first, then the sequences' own.
 struct TileArgs {
   int group, shared_tiles, shared_splits, own_tiles, own_splits, own_slice, shared_slice;
-  int descending;  // of the own tiles (per key head and split), those that come first, from the last rows up
+  int descending;  // of the own tiles (per key head), those that come first, from the last rows up
 };
 
 template <int D>
@@ -43,7 +43,8 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
 
   // the tile: key heads next to each other (one XCD keeps meeting the same); the last rows, which have the most keys,
   // first, and where there are at most two workgroups per compute unit the second ones the other way around, so that
-  // each unit gets one with many keys and one with few
+  // each unit gets one with many keys and one with few; numbers that no rows have (the host knows a bound only) all at
+  // one end, so that the XCDs, which take workgroups in turn, get equally many that have some
   const int head = index % c.heads;
   int nth = index / c.heads;
   const bool shared = nth < x.shared_tiles * x.shared_splits;
@@ -61,10 +62,10 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
     keys = a.shared;
   } else {
     nth -= x.shared_tiles * x.shared_splits;
-    split = nth / x.own_tiles;
     splits = x.own_splits;
+    split = nth % splits;
     slice = x.own_slice < 0 ? -1 : x.own_slice + split;
-    const int turn = nth - split * x.own_tiles, wanted = turn < x.descending ? x.own_tiles - 1 - turn : turn - x.descending;
+    const int turn = nth / splits, wanted = turn < x.descending ? x.own_tiles - 1 - turn : turn - x.descending;
     int seen = 0;
     bool found = false;
     for (int b0 = 0; b0 < s.B; b0 += 64) {
