@@ -68,8 +68,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
     const int nth = r / j.units.rows;
     own_unit = first + ((before + nth) * c.heads + head) * blocks;
     own_row = r - nth * j.units.rows;
-    own_wave = own_unit / n.each;
-    own_waves = (own_unit + blocks - 1) / n.each - own_wave + 1;
+    // (within the waves that there are, also where sequences overlap and the units are too many to count)
+    own_wave = min(max(own_unit / n.each, 0), j.units.waves - 1);
+    own_waves = min((own_unit + blocks - 1) / n.each, j.units.waves - 1) - own_wave + 1;
     if (own_waves == 1) {
       if (j.own_slices == 0) return;  // the result is in place
       own_waves = 0;

@@ -62,7 +62,8 @@ __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs
       blocks = (a.shared + 31) >> 5;
     } else {
       int seen = n.shared;
-      for (int b0 = 0;; b0 += 64) {  // (some sequence holds it: at < total)
+      nth = 0;
+      for (int b0 = 0; b0 < s.B; b0 += 64) {
         const Sequence q = sequence_at(s, c.shift, b0 + lane);
         const int mine = units_of(units, q), sum = seen + prefix_sum(mine);
         const unsigned long long owner = __ballot(sum > at && sum - mine <= at);
@@ -74,6 +75,7 @@ __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs
         }
         seen = __builtin_amdgcn_readlane(sum, 63);
       }
+      if (seq.rows == 0) return;  // (some sequence holds it, at < total, unless the numbers changed meanwhile)
       blocks = key_blocks(units, seq.length);
       key0 = a.shared;
     }

@@ -16,7 +16,8 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 constexpr int32_t kMaxDim = 1 << 21;   // row strides
 constexpr int32_t kMaxSeqs = 1 << 16;
 constexpr int32_t kMaxHeads = 1024;
-constexpr int32_t kMaxRows = 1 << 24;  // tokens times query heads: launch grids and row tiles in 32 bits
+constexpr int32_t kMaxRows = 1 << 24;  // tokens times query heads, below it: launches of less than 2^32 threads
+constexpr int32_t kMaxChosen = 1 << 22;  // tokens times key heads of a selection, likewise
 constexpr int32_t kMaxAxes = 16;
 
 bool dim_known(int32_t dim) { return dim == 64 || dim == 96 || dim == 128 || dim == 256; }
@@ -25,7 +26,7 @@ bool page_known(int32_t size) { return size >= 16 && size <= 256 && (size & (siz
 // Token and head counts and the tables' width; then the page size, so that places stay within 30 bits.
 bool counts_ok(int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t width, int32_t page_size) {
   return T >= 1 && B >= 1 && B <= kMaxSeqs && kv_heads >= 1 && q_heads >= kv_heads && q_heads <= kMaxHeads &&
-         q_heads % kv_heads == 0 && (int64_t)T * q_heads <= kMaxRows && width >= 1 && page_known(page_size) &&
+         q_heads % kv_heads == 0 && (int64_t)T * q_heads < kMaxRows && width >= 1 && page_known(page_size) &&
          (int64_t)width * page_size <= ((int64_t)1 << 30);
 }
 
@@ -114,7 +115,7 @@ int awq_attend(const void* q, int32_t ldq, const int32_t* offsets, const int32_t
 }
 
 size_t awq_select_pages_workspace_bytes(int32_t T, int32_t kv_heads, int32_t width, int32_t count) {
-  if (T < 1 || kv_heads < 1 || (int64_t)T * kv_heads > kMaxRows || width < 1 || count < 1) return 0;
+  if (T < 1 || kv_heads < 1 || (int64_t)T * kv_heads >= kMaxChosen || width < 1 || count < 1) return 0;
   return awq::select_workspace_bytes(T, kv_heads, width, count);
 }
 
@@ -124,7 +125,7 @@ int awq_select_pages(const void* q, int32_t ldq, const int32_t* offsets, const i
                      int32_t* chosen, void* workspace, size_t workspace_bytes, void* stream) {
   int st = check_cache(offsets, lengths, tables, width, T, B, q_heads, kv_heads, head_dim, pages, page_size);
   if (st != AWQ_OK) return st;
-  if (!stride_ok(ldq, (int64_t)q_heads * head_dim)) return AWQ_ERR_SHAPE;
+  if (!stride_ok(ldq, (int64_t)q_heads * head_dim) || (int64_t)T * kv_heads >= kMaxChosen) return AWQ_ERR_SHAPE;
   if (count < 1 || first < 0 || recent < 1 || (int64_t)first + recent > count ||
       (int64_t)T * kv_heads * count >= ((int64_t)1 << 31))
     return AWQ_ERR_OPTION;

@@ -292,7 +292,10 @@ void launch_score(const SelectArgs& a, const CacheArgs& c, const SeqArgs& s, uin
   constexpr int PAGES = Score<D>::PAGES;
   // a wave's pages: one batch where that fills the chip, more where the queries' sums would be formed too often
   const int64_t all = (int64_t)s.T * c.heads * ((s.width + PAGES - 1) / PAGES), want = all / kScoreWaves;
-  const int batches = want < 1 ? 1 : want > 8 ? 8 : (int)want, pages = 4 * batches * PAGES;
+  int batches = want < 1 ? 1 : want > 8 ? 8 : (int)want;
+  constexpr int kMostGroups = 65535;  // (of a launch in y)
+  batches = max(batches, s.width / (4 * PAGES) / kMostGroups + 1);
+  const int pages = 4 * batches * PAGES;
   hipLaunchKernelGGL((score_kernel<D>), dim3(s.T * c.heads, (s.width + pages - 1) / pages), dim3(256), 0, stream, a, c, s,
                      batches, keys);
 }

@@ -437,7 +437,7 @@ size_t awq_combine_experts_workspace_bytes(int32_t T, int32_t top_k, int32_t E, 
  * page out of range nothing is written.  A new token whose place is negative (more
  * rows than length) is not appended, and its attention is 0.
  * q_heads is a multiple of kv_heads: key head h serves query heads h * G .. h * G
- * + G - 1, G = q_heads / kv_heads.  1 <= B <= 2^16, T * q_heads <= 2^24, q_heads
+ * + G - 1, G = q_heads / kv_heads.  1 <= B <= 2^16, T * q_heads < 2^24, q_heads
  * <= 1024.  Row strides as everywhere (multiples of 8, at most 2^21).
  *
  * awq_append_kv - new tokens into the cache, rotated on the way.
@@ -499,8 +499,10 @@ size_t awq_attend_workspace_bytes(int32_t T, int32_t B, int32_t q_heads, int32_t
  * between, the ones with the largest
  *   score(page) = sum over the key head's query heads and the channels of max(q lo, q hi),
  * lo and hi the page's bounds (the largest q . k that keys within them could have): q hi
- * where q > 0, q lo where q < 0, nothing where q = 0; the lower page first among equal scores.  Scores are fp64 sums; NaN counts as the lowest.
- * first >= 0, recent >= 1, first + recent <= count (AWQ_ERR_OPTION).  Deterministic.
+ * where q > 0, q lo where q < 0, nothing where q = 0; the lower page first among equal
+ * scores.  Scores are fp64 sums; NaN counts as the lowest.
+ * first >= 0, recent >= 1, first + recent <= count (AWQ_ERR_OPTION).  T * kv_heads < 2^22.
+ * Deterministic.
  * workspace: awq_select_pages_workspace_bytes() bytes (a score per token, key head and
  * page of the tables), as awq_attend's.
  */
