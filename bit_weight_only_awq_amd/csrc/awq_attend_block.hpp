@@ -78,8 +78,13 @@ struct Sources {
 // to it.)
 template <int N>
 __device__ __forceinline__ void load_to_lds(const char* base, const uint32_t (&offset)[N], lds_char* to) {
-  static_assert(N == 2 || N == 3 || N == 4, "loads of 16 rows, or half of them");
+  static_assert(N >= 1 && N <= 4, "loads of 16 rows, or some of them");
   uint32_t kept;
+  if constexpr (N == 1)
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(kept)
+                 : "s"(to), "s"(base), "v"(offset[0])
+                 : "memory");
   if constexpr (N == 2)
     asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %2\n\t"
                  "s_add_u32 m0, m0, 1024\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %2\n\ts_mov_b32 m0, %0"
@@ -491,10 +496,11 @@ __device__ __forceinline__ Weights<R> attend_block(const Addresses<D, R>& at, co
 
 // The same, a block ahead with the scores: the weights of the block whose scores are `s`, with values V bytes behind the
 // lane's addresses, beside the products for the next block's scores (keys K bytes behind, the first fragments on their
-// way), and the greatest of those, `m`, beside the products with the values.
-template <int D, int R, int K, int V>
+// way), and the greatest of those, `m`, beside the products with the values, as well as beside(i), after every other of
+// them.
+template <int D, int R, int K, int V, typename Beside>
 __device__ __forceinline__ Weights<R> attend_next(const Addresses<D, R>& at, const Queries<D, R>& q, Fragments& f, float c,
-                                                  const Seen& seen, Scores<R>& s, float& m, Gathered<D, R>& g) {
+                                                  const Seen& seen, Scores<R>& s, float& m, Gathered<D, R>& g, Beside beside) {
   constexpr int N = Products<D, R>::SCORES, M = Products<D, R>::VALUES, PAIRS = Scores<R>::COUNT / 2;
   half8_t v[kAhead];
   Weights<R> p;
@@ -512,6 +518,7 @@ __device__ __forceinline__ Weights<R> attend_next(const Addresses<D, R>& at, con
     constexpr int i = decltype(ic)::value;
 #pragma unroll
     for (int n = PAIRS * i / M; n < PAIRS * (i + 1) / M; ++n) most = larger(larger(most, next.get(2 * n)), next.get(2 * n + 1));
+    if constexpr (i % 2 == 0) beside(std::integral_constant<int, i / 2>{});
   });
   s = next;
   m = row_max<R>(most);

@@ -105,24 +105,20 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
 
   // this wave's loads of a block: of keys or of values, one group of 16 of them
   const int sixteen = wave & 1, of_values = wave >> 1;
-  constexpr int PER = LOADS < 4 ? LOADS : 4;  // loads at once
-  uint32_t lane_from[LOADS / PER][PER];
+  uint32_t lane_from[LOADS];
   {
     const Sources<D> sources(lane, 0);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) lane_from[i / PER][i % PER] = of_values ? sources.value(i) : sources.key(i);
+    for (int i = 0; i < LOADS; ++i) lane_from[i] = of_values ? sources.value(i) : sources.key(i);
   }
   const Addresses<D, 32> places((uint32_t)(uintptr_t)ring, lane);
   Entries pages{s.tables + (int64_t)seq.index * s.width, nullptr, 0, s.width, head, 0, 0, 0, 0};
-  auto load = [&](int block, int slot) __attribute__((always_inline)) {
+  auto source_of = [&](int block) __attribute__((always_inline)) {
     const int key = key0 + 32 * block;
     if (block == from || ((key + 16) >> c.shift) - pages.first >= 64) pages.read(c, key >> c.shift);
-    const Keys16 source = keys16(pages, c, key + 16 * sixteen);
-    const char* base = reinterpret_cast<const char*>((of_values ? c.v : c.k) + source.at * D);
-    lds_char* to = ring + (2 * slot + of_values) * SLOT + 16 * sixteen * T::ROW;
-#pragma unroll
-    for (int i = 0; i < LOADS / PER; ++i) load_to_lds<PER>(base, lane_from[i], to + 1024 * PER * i);
+    return reinterpret_cast<const char*>((of_values ? c.v : c.k) + keys16(pages, c, key + 16 * sixteen).at * D);
   };
+  lds_char* const own = ring + of_values * SLOT + 16 * sixteen * T::ROW;
   auto meet = [&]() __attribute__((always_inline)) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -158,7 +154,11 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
   float m_now = 0.0f;
   if (from < to) {
 #pragma unroll
-    for (int i = 0; i < RING - 1; ++i) load(min(from + i, to - 1), i);
+    for (int i = 0; i < RING - 1; ++i) {
+      const char* base = source_of(min(from + i, to - 1));
+#pragma unroll
+      for (int n = 0; n < LOADS; ++n) load_to_lds<1>(base, {lane_from[n]}, own + 2 * SLOT * i + 1024 * n);
+    }
     wait_loads<(RING - 2) * LOADS>();
     meet();
     Fragments f = first_keys<D, 32, 0>(places);
@@ -172,10 +172,15 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
     wait_loads<(RING - 3) * LOADS>();
     meet();
     Fragments f = first_keys<D, 32, 2 * NEXT * SLOT>(places);
-    load(min(block + RING - 1, to - 1), (HERE + RING - 1) % RING);
+    const char* base = source_of(min(block + RING - 1, to - 1));
     const uint32_t odd = hide(block, HERE);
     const Seen seen = seen_of(block);
-    const Weights<32> p = attend_next<D, 32, 2 * NEXT * SLOT, (2 * HERE + 1) * SLOT>(places, q, f, scale, seen, s_now, m_now, g);
+    const Weights<32> p = attend_next<D, 32, 2 * NEXT * SLOT, (2 * HERE + 1) * SLOT>(
+        places, q, f, scale, seen, s_now, m_now, g, [&](auto n) __attribute__((always_inline)) {
+          constexpr int i = decltype(n)::value;
+          static_assert(Products<D, 32>::VALUES == 2 * LOADS, "a load for every other of them");
+          load_to_lds<1>(base, {lane_from[i]}, own + 2 * SLOT * ((HERE + RING - 1) % RING) + 1024 * i);
+        });
     finish(block, odd, p, seen);
   };
   for (int block = from; block < to; block += RING)
