@@ -14,8 +14,7 @@ namespace {
 
 struct JoinArgs {
   UnitArgs units;
-  bool own_few;
-  int own_slices, shared_slices;
+  int slices;  // the own keys' (where there are shared keys) and theirs
 };
 
 // Where waves made the parts of the own keys: a wave per row (token and query
@@ -34,10 +33,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
   // the row's sequence and, among the waves' units, the first of it
   Sequence seq{0, 0, 0, 0};
   int first = 0;
-  Units n{0, 0, 1};
+  Units n{0, 1};
   if (!a.list) {
-    const int shared = j.units.shared ? row_blocks(j.units, all_rows(s, 0).rows) * c.heads * ((j.units.shared_keys + 31) >> 5) : 0;
-    int seen = shared;
+    int seen = 0;
     for (int b0 = 0; b0 < s.B; b0 += 64) {
       const Sequence q = sequence_at(s, c.shift, b0 + lane);
       const int mine = units_of(j.units, q), sum = seen + prefix_sum(mine);
@@ -49,51 +47,28 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
       }
       seen = __builtin_amdgcn_readlane(sum, 63);
     }
-    n = share_units(j.units, seen, shared);
+    n = share_units(seen);
   } else {
     seq = sequence_of(s, c.shift, t);
-    n = share_units(j.units, s.T * c.heads * row_blocks(j.units, 1) * list_blocks(j.units, a.count), 0);
+    n = share_units(s.T * c.heads * row_blocks(j.units, 1) * list_blocks(j.units, a.count));
   }
   if (seq.rows == 0) return;  // a row of no sequence stays as it is
 
-  // The row's parts: own_waves pieces of waves from `own_wave` on and shared_waves from `shared_wave` on, then slices.
-  // (A row without a place has parts as well: those of its own keys, all empty, and those of shared keys, not its.)
-  int own_unit = 0, own_wave = 0, own_waves = 0, own_row = 0, shared_unit = 0, shared_wave = 0, shared_waves = 0,
-      shared_row = 0, slice0 = 0, slices = 0;
+  // The row's parts: `pieces` of waves from `wave0` on, then slices: slice 0, the own keys, if a wave had them all, and the
+  // shared keys'.  (A row without a place has parts as well: those of its own keys, all empty, and those of shared
+  // keys, not its.)
   const bool placed = t - seq.row0 + seq.place0() >= 0;
-  {
-    const int blocks = a.list ? list_blocks(j.units, a.count) : key_blocks(j.units, seq.length);
-    const int r = a.list ? g : (t - seq.row0) * group + g;
-    const int before = a.list ? t * row_blocks(j.units, 1) : 0;
-    const int nth = r / j.units.rows;
-    own_unit = first + ((before + nth) * c.heads + head) * blocks;
-    own_row = r - nth * j.units.rows;
-    // (within the waves that there are, also where sequences overlap and the units are too many to count)
-    own_wave = min(max(own_unit / n.each, 0), j.units.waves - 1);
-    own_waves = min((own_unit + blocks - 1) / n.each, j.units.waves - 1) - own_wave + 1;
-    if (own_waves == 1) {
-      if (j.own_slices == 0) return;  // the result is in place
-      own_waves = 0;
-      slices = 1;
-    } else {
-      slice0 = j.own_slices;
-    }
+  const int blocks = a.list ? list_blocks(j.units, a.count) : key_blocks(j.units, seq.length);
+  const int r = a.list ? g : (t - seq.row0) * group + g, nth = r / j.units.rows, own_row = r - nth * j.units.rows;
+  const int unit = first + (((a.list ? t * row_blocks(j.units, 1) : 0) + nth) * c.heads + head) * blocks;
+  // (within the waves that there are, also where sequences overlap and the units are too many to count)
+  const int wave0 = min(max(unit / n.each, 0), kWaves - 1);
+  int pieces = min((unit + blocks - 1) / n.each, kWaves - 1) - wave0 + 1, slice0 = 1;
+  if (pieces == 1) {
+    if (j.slices == 0) return;  // the result is in place
+    pieces = slice0 = 0;
   }
-  if (j.units.shared) {
-    const int blocks = (j.units.shared_keys + 31) >> 5, r = (t - all_rows(s, 0).row0) * group + g;
-    const int nth = r / j.units.rows;
-    shared_unit = (nth * c.heads + head) * blocks;
-    shared_row = r - nth * j.units.rows;
-    shared_wave = shared_unit / n.each;
-    shared_waves = (shared_unit + blocks - 1) / n.each - shared_wave + 1;
-    if (shared_waves == 1) {
-      shared_waves = 0;
-      slices = 2 - slice0;  // (slice 0: the own keys, 1: the shared)
-    }
-  } else {
-    slices += j.shared_slices;
-  }
-  const int parts = placed ? own_waves + shared_waves + slices : 0;
+  const int parts = placed ? pieces + max(j.slices - slice0, 0) : 0;
 
   float4_t sums = float4_t(0.0f);
   float top = -INFINITY, total = 0.0f;
@@ -104,13 +79,12 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
     int i = i0 + lane, from = 0;
     float2 stat{-INFINITY, 0.0f};
     if (i < parts) {
-      if (i < own_waves + shared_waves) {
-        const bool own = i < own_waves;
-        const int w = own ? own_wave + i : shared_wave + i - own_waves;
-        from = -1 - ((2 * w + (w * n.each > (own ? own_unit : shared_unit) ? 0 : 1)) * 32 + (own ? own_row : shared_row));
+      if (i < pieces) {
+        const int w = wave0 + i;
+        from = -1 - ((2 * w + (w * n.each > unit ? 0 : 1)) * 32 + own_row);
         stat = p.wave_stat[-1 - from];
       } else {
-        from = (int)((slice0 + i - own_waves - shared_waves) * p.rows) + row;
+        from = (int)((slice0 + i - pieces) * p.rows) + row;
         stat = p.stat[from];
       }
     }
@@ -242,18 +216,15 @@ AttendPlan plan_of(int T, int B, int q_heads, int kv_heads, int dim, int page_si
   const int group = q_heads / kv_heads, stage = dim == 256 ? 32 : 64, slots = dim == 256 ? kUnits : 2 * kUnits;
   const int64_t rows = (int64_t)T * group;
   AttendPlan p{};
+  p.shared = shared > 0;
   // (units of the waves: 16 rows, at least a block of them per sequence, times key heads and blocks of 32 keys)
-  const int64_t units = kv_heads * ((rows / 16 + B) * ((int64_t)width * page_size / 32 + 1) + (rows / 16 + 1) * (shared / 32 + 1));
+  const int64_t units = kv_heads * (rows / 16 + B) * ((int64_t)width * page_size / 32 + 1);
   p.own_few = list || (rows <= 32 * (int64_t)B && units < kMostUnits);
-  p.prefix = shared == 0 ? 0 : p.own_few && rows <= 32 ? 1 : 2;
-  p.waves = kUnits * (dim == 256 ? 2 : dim == 128 ? 5 : 6);
-  p.least = 2;
-  p.own_splits = p.prefix_splits = 1;
   p.rows = rows <= 16 * (int64_t)(list ? T : B) ? 16 : 32;
-  p.both = p.own_few && p.rows == 16 && p.prefix == 2 && dim < 256;
-  if (p.both) p.waves = kUnits * kWavesOfWorkgroup;  // (a unit's other workgroup makes row tiles)
-  if (p.prefix == 2)
-    p.prefix_splits = splits_of((rows + 127) / 128 * kv_heads, (shared + stage - 1) / stage, p.both ? kUnits : slots, 3.0);
+  p.both = p.own_few && p.shared && p.rows == 16;
+  p.own_splits = p.shared_splits = 1;
+  if (p.shared)
+    p.shared_splits = splits_of((rows + 127) / 128 * kv_heads, (shared + stage - 1) / stage, p.both ? kUnits : slots, 3.0);
   if (!p.own_few) {
     const int64_t keys = (int64_t)width * page_size - shared;
     p.own_splits = splits_of(((rows + 127) / 128 + B / 2) * kv_heads, (keys + stage - 1) / stage, slots, 3.0);
@@ -262,15 +233,15 @@ AttendPlan plan_of(int T, int B, int q_heads, int kv_heads, int dim, int page_si
 }
 
 template <int D>
-void launch_join(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const JoinArgs& j, const Partials& p,
-                 hipStream_t stream) {
+void launch_join(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, bool own_few, const JoinArgs& j,
+                 const Partials& p, hipStream_t stream) {
   const int64_t rows = (int64_t)s.T * a.q_heads;
   constexpr int ROWS = 256 / (D <= 64 ? 16 : D <= 128 ? 32 : 64);  // of a workgroup
-  if (j.own_few)
+  if (own_few)
     hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, c, s, j, p);
   else
     hipLaunchKernelGGL((join_slices_kernel<D>), dim3((unsigned)((rows + ROWS - 1) / ROWS)), dim3(256), 0, stream, a, s,
-                       j.own_slices + j.shared_slices, p);
+                       j.slices, p);
 }
 
 }  // namespace
@@ -287,14 +258,16 @@ hipError_t launch_attend(const AttendArgs& a, const CacheArgs& c, const SeqArgs&
   const AttendPlan plan = plan_of(s.T, s.B, a.q_heads, c.heads, c.dim, 1 << c.shift, list ? a.count : s.width, a.shared, list);
   const Partials p = partials(plan, (int64_t)s.T * a.q_heads, c.dim, workspace);
   hipError_t e = hipSuccess;
-  if (plan.prefix == 2 || !plan.own_few) e = launch_attend_tiles(a, c, s, plan, p, stream);
+  if (plan.shared || !plan.own_few) e = launch_attend_tiles(a, c, s, plan, p, stream);
   if (e == hipSuccess && plan.own_few && !plan.both) e = launch_attend_waves(a, c, s, plan, p, stream);
   if (e != hipSuccess || (!plan.own_few && plan.slices() == 0)) return e;
-  const JoinArgs j{unit_args(a, c, plan), plan.own_few, plan.own_slices(), plan.slices() - plan.own_slices()};
-  if (c.dim == 64) launch_join<64>(a, c, s, j, p, stream);
-  else if (c.dim == 96) launch_join<96>(a, c, s, j, p, stream);
-  else if (c.dim == 128) launch_join<128>(a, c, s, j, p, stream);
-  else launch_join<256>(a, c, s, j, p, stream);
+  const JoinArgs j{unit_args(a, c, plan), plan.slices()};
+#define AWQ_JOIN(D) launch_join<D>(a, c, s, plan.own_few, j, p, stream)
+  if (c.dim == 64) AWQ_JOIN(64);
+  else if (c.dim == 96) AWQ_JOIN(96);
+  else if (c.dim == 128) AWQ_JOIN(128);
+  else AWQ_JOIN(256);
+#undef AWQ_JOIN
   return hipGetLastError();
 }
 

@@ -7,18 +7,21 @@
 namespace awq {
 
 constexpr int kUnits = 256;  // compute units
-constexpr int kWavesOfWorkgroup = 2;  // waves on their own of a workgroup, where it may be row tiles as well
+// Waves on their own of a unit, each with a ring of two blocks.  (With five a unit's LDS is full, and HBM serves their
+// many streams less well: 1 token of 8191 40.5 us, with two 32.4; 48 tokens 103, 96, with four 93.4; 32 tokens on chosen
+// pages 102, 92; 1 token of 30000 46, 36.  Rings of three or four blocks: the same or slower.)
+constexpr int kWavesOfUnit = 2, kWaves = kUnits * kWavesOfUnit;
+constexpr int kLeastUnits = 2;  // key blocks that a wave takes at least
 
-// Rows of 16 or 32 and keys of 32 of one wave (few), rows of 128 and splits of the keys (many).
+// Rows of 16 or 32 and keys of 32 of one wave (few), rows of 128 and splits of the keys (many, and all shared keys).
 struct AttendPlan {
-  bool own_few;       // a sequence's own keys: a wave per 32 rows, or a workgroup per 128
-  int prefix;         // the shared keys: 0: none, 1: with the waves (and own_few), 2: with the workgroups
-  int waves, least;   // waves of the first kind; key blocks that each takes at least
-  int rows;           // of theirs: 16 or 32
-  bool both;          // own_few and prefix 2, in one launch
-  int own_splits, prefix_splits;  // of the second kind
-  int own_slices() const { return own_few ? (prefix ? 1 : 0) : prefix || own_splits > 1 ? own_splits : 0; }
-  int slices() const { return own_slices() + (prefix == 2 ? prefix_splits : prefix); }
+  bool own_few;  // a sequence's own keys: with the waves, or with the workgroups
+  bool shared;   // there are shared keys
+  int rows;      // of a wave: 16 or 32
+  bool both;     // waves and workgroups in one launch
+  int own_splits, shared_splits;  // of the workgroups
+  int own_slices() const { return own_few ? shared : shared || own_splits > 1 ? own_splits : 0; }
+  int slices() const { return own_slices() + (shared ? shared_splits : 0); }
 };
 
 // Partial results: for each row's query head (numbered t * q_heads + head) and slice the maximum (in powers of two),
@@ -34,7 +37,7 @@ struct Partials {
 
 inline Partials partials(const AttendPlan& p, int64_t rows, int dim, void* workspace) {
   Partials x;
-  const int64_t waves = p.own_few ? 64 * (int64_t)p.waves : 0;
+  const int64_t waves = p.own_few ? 64 * kWaves : 0;
   x.rows = rows;
   x.sums = static_cast<float*>(workspace);
   x.wave_sums = x.sums + p.slices() * rows * dim;
@@ -43,7 +46,7 @@ inline Partials partials(const AttendPlan& p, int64_t rows, int dim, void* works
   return x;
 }
 inline size_t partial_bytes(const AttendPlan& p, int64_t rows, int dim) {
-  const int64_t all = p.slices() * rows + (p.own_few ? 64 * (int64_t)p.waves : 0);
+  const int64_t all = p.slices() * rows + (p.own_few ? 64 * kWaves : 0);
   return ((size_t)all * (dim * 4 + 8) + 15) & ~(size_t)15;
 }
 
@@ -52,39 +55,32 @@ hipError_t launch_attend_waves(const AttendArgs& a, const CacheArgs& c, const Se
 hipError_t launch_attend_tiles(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan,
                                const Partials& p, hipStream_t stream);
 
-// The units of work of the waves (16 or 32 rows, a key head, 32 keys), in order: the shared keys' (all rows together), then
-// sequence after sequence; within one, rows, then key heads, then keys.  Every row has at least one.  Wave w takes the units
-// w * each .. w * each + each - 1.  (The host makes sure that their number stays below kMostUnits.)
+// The units of work of the waves (16 or 32 rows, a key head, 32 keys), in order: sequence after sequence; within one, rows,
+// then key heads, then keys.  Every row has at least one.  Wave w takes the units w * each .. w * each + each - 1.  (The
+// host makes sure that their number stays below kMostUnits.)
 struct Units {
-  int total, shared, each;
+  int total, each;
 };
 struct UnitArgs {
-  int group, heads, shift, shared_keys, waves, least;
-  int rows;     // of a unit: 16 or 32
-  bool shared;  // the shared keys are the waves' too
+  int group, heads, shift, shared_keys;
+  int rows;  // of a unit: 16 or 32
 };
 inline UnitArgs unit_args(const AttendArgs& a, const CacheArgs& c, const AttendPlan& plan) {
-  return UnitArgs{a.q_heads / c.heads, c.heads, c.shift, a.shared, plan.waves, plan.least, plan.rows, plan.prefix == 1};
+  return UnitArgs{a.q_heads / c.heads, c.heads, c.shift, a.shared, plan.rows};
 }
 __device__ __forceinline__ int key_blocks(const UnitArgs& u, int length) { return max((length - u.shared_keys + 31) >> 5, 1); }
 __device__ __forceinline__ int row_blocks(const UnitArgs& u, int rows) { return (rows * u.group + u.rows - 1) / u.rows; }
 __device__ __forceinline__ int units_of(const UnitArgs& u, const Sequence& q) {
   return q.rows ? row_blocks(u, q.rows) * u.heads * key_blocks(u, q.length) : 0;
 }
-// All rows of the batch as one sequence that ends with the shared keys.
-__device__ __forceinline__ Sequence all_rows(const SeqArgs& s, int shared_keys) {
-  const int from = min(max(s.offsets[0], 0), s.T);
-  return Sequence{0, from, max(min(s.offsets[s.B], s.T) - from, 0), shared_keys};
-}
-__device__ __forceinline__ Units share_units(const UnitArgs& u, int total, int shared) {
-  return Units{total, shared, max((total + u.waves - 1) / u.waves, u.least)};
+__device__ __forceinline__ Units share_units(int total) {
+  return Units{total, max((total + kWaves - 1) / kWaves, kLeastUnits)};
 }
 __device__ __forceinline__ Units count_units(const SeqArgs& s, const UnitArgs& u) {
-  const int shared = u.shared ? row_blocks(u, all_rows(s, 0).rows) * u.heads * ((u.shared_keys + 31) >> 5) : 0;
-  int total = shared;
+  int total = 0;
   for (int b0 = 0; b0 < s.B; b0 += 64)
     total += __builtin_amdgcn_readlane(prefix_sum(units_of(u, sequence_at(s, u.shift, b0 + __lane_id()))), 63);
-  return share_units(u, total, shared);
+  return share_units(total);
 }
 // For a list of pages per token: units of a token.
 __device__ __forceinline__ int list_blocks(const UnitArgs& u, int count) { return ((count << u.shift) + 31) >> 5; }

@@ -16,22 +16,20 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_tiles_kernel(Att
   attend_tile<D>(a, c, s, x, p, blockIdx.x, (lds_char*)ring, strange);
 }
 
-// The first plan.waves / kWavesOfWorkgroup workgroups are waves on their own (as many of a workgroup's four as the ring
-// has room for), the others row tiles of the shared keys.
+// The first kUnits workgroups are waves on their own (kWavesOfUnit of a workgroup's four: as many as the ring has room
+// for), the others row tiles of the shared keys.
 template <int D>
-__global__ __launch_bounds__(256, 2) void attend_both_kernel(AttendArgs a, CacheArgs c, SeqArgs s, UnitArgs units, TileArgs x,
-                                                             Partials p) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_both_kernel(AttendArgs a, CacheArgs c, SeqArgs s,
+                                                                            UnitArgs units, TileArgs x, Partials p) {
   __shared__ __attribute__((aligned(1024))) char ring[TileRing<D>::BYTES];
   __shared__ uint32_t strange[2];
-  const int first = units.waves / kWavesOfWorkgroup;
-  if ((int)blockIdx.x < first) {
-    static_assert(kWavesOfWorkgroup * wave_ring<D>() <= TileRing<D>::BYTES, "the waves' rings fit");
+  if ((int)blockIdx.x < kUnits) {
+    static_assert(kWavesOfUnit * wave_ring<D>() <= TileRing<D>::BYTES, "the waves' rings fit");
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wave < kWavesOfWorkgroup)
-      attend_wave<D, 16, false>(a, c, s, units, p, blockIdx.x * kWavesOfWorkgroup + wave,
-                            (lds_char*)ring + wave * wave_ring<D>());
+    if (wave < kWavesOfUnit)
+      attend_wave<D, 16, false>(a, c, s, units, p, blockIdx.x * kWavesOfUnit + wave, (lds_char*)ring + wave * wave_ring<D>());
   } else {
-    attend_tile<D>(a, c, s, x, p, blockIdx.x - first, (lds_char*)ring, strange);
+    attend_tile<D>(a, c, s, x, p, blockIdx.x - kUnits, (lds_char*)ring, strange);
   }
 }
 
@@ -40,13 +38,11 @@ void launch(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const Att
             hipStream_t stream) {
   const TileArgs x = tile_args(a, c, s, plan);
   const unsigned grid = tile_workgroups(x, c.heads);
-  if constexpr (D < 256)
-    if (plan.both) {
-      hipLaunchKernelGGL((attend_both_kernel<D>), dim3(plan.waves / kWavesOfWorkgroup + grid), dim3(256), 0, stream, a, c, s,
-                         unit_args(a, c, plan), x, p);
-      return;
-    }
-  hipLaunchKernelGGL((attend_tiles_kernel<D>), dim3(grid), dim3(256), 0, stream, a, c, s, x, p);
+  if (plan.both)
+    hipLaunchKernelGGL((attend_both_kernel<D>), dim3(kUnits + grid), dim3(256), 0, stream, a, c, s, unit_args(a, c, plan), x,
+                       p);
+  else
+    hipLaunchKernelGGL((attend_tiles_kernel<D>), dim3(grid), dim3(256), 0, stream, a, c, s, x, p);
 }
 
 }  // namespace

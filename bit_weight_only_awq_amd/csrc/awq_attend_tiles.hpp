@@ -30,6 +30,12 @@ struct TileRing {
   static constexpr int BLOCKS = 4, BYTES = 2 * BLOCKS * 32 * Tile<D>::ROW;
 };
 
+// All rows of the batch as one sequence that ends with the shared keys.
+__device__ __forceinline__ Sequence all_rows(const SeqArgs& s, int shared_keys) {
+  const int from = min(max(s.offsets[0], 0), s.T);
+  return Sequence{0, from, max(min(s.offsets[s.B], s.T) - from, 0), shared_keys};
+}
+
 // Workgroup number `index` of 256 threads; a ring of TileRing<D>::BYTES and two words.
 template <int D>
 __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const TileArgs& x,
@@ -197,9 +203,9 @@ inline TileArgs tile_args(const AttendArgs& a, const CacheArgs& c, const SeqArgs
   const int group = a.q_heads / c.heads;
   const int64_t rows = (int64_t)s.T * group, most = rows / kTile + s.B;  // (a ragged tile per sequence at most)
   TileArgs x{group, 0, 1, 0, 1, plan.own_slices() > 0 ? 0 : -1, plan.own_slices(), 0};
-  if (plan.prefix == 2) {
+  if (plan.shared) {
     x.shared_tiles = (int)((rows + kTile - 1) / kTile);
-    x.shared_splits = plan.prefix_splits;
+    x.shared_splits = plan.shared_splits;
   }
   if (!plan.own_few) {
     x.own_tiles = (int)(most < rows ? most : rows);

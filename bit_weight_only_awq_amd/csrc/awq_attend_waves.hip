@@ -15,8 +15,8 @@ __global__ __launch_bounds__(64, D == 256 ? 1 : 2) void attend_waves_kernel(Atte
 template <int D, int R>
 void launch_as(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan, const Partials& p,
                const UnitArgs& u, hipStream_t stream) {
-  if (a.list) hipLaunchKernelGGL((attend_waves_kernel<D, R, true>), dim3(plan.waves), dim3(64), 0, stream, a, c, s, u, p);
-  else hipLaunchKernelGGL((attend_waves_kernel<D, R, false>), dim3(plan.waves), dim3(64), 0, stream, a, c, s, u, p);
+  if (a.list) hipLaunchKernelGGL((attend_waves_kernel<D, R, true>), dim3(kWaves), dim3(64), 0, stream, a, c, s, u, p);
+  else hipLaunchKernelGGL((attend_waves_kernel<D, R, false>), dim3(kWaves), dim3(64), 0, stream, a, c, s, u, p);
 }
 
 template <int D>

@@ -3,7 +3,7 @@
 //
 // Mathematics: awq_attend_block.hpp's.  A unit of work is 32 keys for up to R rows
 // (tokens times query heads of one key head); all units of the batch, whatever the
-// lengths, are one list, and each of the `waves` waves takes an equal run of it, so
+// lengths, are one list, and each of kWaves waves takes an equal run of it, so
 // ragged batches and single long sequences fill the chip alike.  A wave that
 // takes a whole segment (rows, key head) writes its result; the pieces of the
 // others are joined by a second launch.
@@ -32,7 +32,7 @@ __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs
 
   const int list_rows = row_blocks(units, 1), of_list = LIST ? list_blocks(units, a.count) : 0;
   const int per_token = c.heads * list_rows * of_list;
-  const Units n = LIST ? share_units(units, s.T * per_token, 0) : count_units(s, units);
+  const Units n = LIST ? share_units(s.T * per_token) : count_units(s, units);
   int at = wave * n.each;
   const int end = min(n.total, at + n.each);
 
@@ -44,7 +44,6 @@ __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs
     Sequence seq{0, 0, 0, 0};
     int nth, blocks, key0 = 0, count = 0;  // nth: of the sequence's units
     const int* list = nullptr;
-    bool shared = false;
     if constexpr (LIST) {
       const int t = at / per_token;
       nth = at - t * per_token;
@@ -55,13 +54,8 @@ __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs
         continue;
       }
       seq = Sequence{of.index, t, 1, t - of.row0 + of.place0() + 1};
-    } else if (at < n.shared) {
-      shared = true;
-      seq = all_rows(s, a.shared);
-      nth = at;
-      blocks = (a.shared + 31) >> 5;
     } else {
-      int seen = n.shared;
+      int seen = 0;
       nth = 0;
       for (int b0 = 0; b0 < s.B; b0 += 64) {
         const Sequence q = sequence_at(s, c.shift, b0 + lane);
@@ -84,11 +78,10 @@ __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs
     const int here = min(blocks - block0, end - at);
     at += here;
     const Rows rows{R * row_block, seq.rows * group, seq.row0, seq.place0()};
-    // places of the rows: their own, and the least and greatest of them (past the shared keys: the last of these)
+    // places of the rows: their own, and the least and greatest of them
     const int mine = (min(rows.first + (lane & (R - 1)), rows.total - 1)) / group;
-    const int place = shared ? a.shared - 1 : rows.place0 + mine;
-    const int least = shared ? a.shared - 1 : rows.place0 + rows.first / group;
-    const int most = shared ? a.shared - 1 : rows.place0 + (min(rows.first + R, rows.total) - 1) / group;
+    const int place = rows.place0 + mine, least = rows.place0 + rows.first / group;
+    const int most = rows.place0 + (min(rows.first + R, rows.total) - 1) / group;
     if constexpr (LIST) {
       list = a.list + ((int64_t)seq.row0 * c.heads + head) * a.count;
       count = a.count;
@@ -162,7 +155,7 @@ __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs
     }
     const bool whole = here == blocks;
     const int64_t slot = 2 * (int64_t)wave + (block0 > 0 ? 0 : 1);
-    write_rows(g, scale, a, p, rows, group, head, shared ? 1 : a.shared > 0 ? 0 : -1,
+    write_rows(g, scale, a, p, rows, group, head, a.shared > 0 ? 0 : -1,
                whole ? nullptr : p.wave_stat + slot * 32, p.wave_sums + slot * 32 * D);
   }
 }
