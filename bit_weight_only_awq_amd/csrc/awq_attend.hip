@@ -2,11 +2,13 @@
 // batch takes, and the launch that joins parts.
 //
 // Few rows per sequence go to independent waves (awq_attend_waves.hip), many to
-// workgroups of 128 rows (awq_attend_tiles.hip); shared keys to whichever suits the
+// workgroups of 128 rows (awq_attend_tiles.hip), and shared keys to these, with the
 // rows of all sequences together.
 //
 // Joining: with m the greatest of the parts' maxima, y = sum_i 2^(m_i - m) o_i / sum_i
-// 2^(m_i - m) l_i over the parts, in a fixed order, in fp32.
+// 2^(m_i - m) l_i over the parts, in a fixed order, in fp32.  Bound: a launch and the
+// chain offsets -> which parts -> parts (4.6-6.7 us); 16 to 30 MB of parts of many rows
+// 14 us.
 #include "awq_attend.hpp"
 
 namespace awq {
@@ -18,9 +20,8 @@ struct JoinArgs {
 };
 
 // Where waves made the parts of the own keys: a wave per row (token and query
-// head), 64 parts at a time, a lane holding each
-// part's maximum and sum, then LANES lanes their share of the channels and 64 /
-// LANES groups of lanes every such part.
+// head), 64 parts at a time, a lane holding each part's maximum and sum, then LANES
+// lanes their share of the channels and 64 / LANES groups of lanes every such part.
 template <int D>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, SeqArgs s, JoinArgs j, Partials p) {
   constexpr int LANES = D <= 64 ? 16 : D <= 128 ? 32 : 64, GROUPS = 64 / LANES, AHEAD = 8;
@@ -194,7 +195,6 @@ __global__ __launch_bounds__(256) void join_slices_kernel(AttendArgs a, SeqArgs 
   *reinterpret_cast<half4_t*>(a.y + t * a.ldy + (int64_t)at * D + channel) = v;
 }
 
-
 // The keys' splits over which `tiles` workgroups take the least time, in rounds of two per compute unit (one where
 // a head is 256 wide), a stage being the unit, what a workgroup does besides costing `extra` of them, and writing and
 // reading the parts of a tile 0.0085 (128 rows of fp32 sums, there and back).
@@ -212,6 +212,14 @@ int splits_of(int64_t tiles, int64_t stages, int slots, double extra) {
   return best;
 }
 
+// Which kernels, measured on both sides (us; sequences x new tokens x query heads of a key head):
+// Up to 32 rows per sequence on average (a row: a token and a query head of one key head) the waves, which share ragged
+// batches out evenly; past that they would read the keys twice.  8 x 4 x 8, 4000 before: waves 34.9, row tiles 38.5;
+// 48 x 1 x 8, 7 to 4000 before: 96, 111; 8 x 5 x 8: 45, 33.3.  (Many key heads with several tokens each, 30 x 16 x 1 of 32
+// heads: 102, 85: the join's rows.)
+// Up to 16 rows the waves' products are of 16: 8 x 2 x 8 32.0, of 32 32.4; 8 x 4 x 8 43.1, 33.9.
+// Shared keys always by row tiles: 1 x 1 x 8 after 8192 19.0, by waves 30.9; 16 x 1 x 8 26.1, 61.4; with up to 16 rows per
+// sequence in one launch with the waves: 16 x 1 x 8 25.9, in two 38.2; 61 x 1 x 8 47, 68.
 AttendPlan plan_of(int T, int B, int q_heads, int kv_heads, int dim, int page_size, int width, int shared, bool list) {
   const int group = q_heads / kv_heads, stage = dim == 256 ? 32 : 64, slots = dim == 256 ? kUnits : 2 * kUnits;
   const int64_t rows = (int64_t)T * group;
