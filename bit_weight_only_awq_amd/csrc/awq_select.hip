@@ -17,7 +17,8 @@
 // pages, 95 MB: 26 us, 3.7 TB/s, 10 of them fp64 instructions; 1 token of 6251
 // pages, 26 MB: 9.0); the second finds the wanted number of largest scores by their
 // bits, 8 at a time from the highest in which they differ, one workgroup per token and
-// key head: a chain of reads and rounds (8.5 us in both cases).
+// key head: a chain of reads and rounds (8.5 us in both cases).  Narrow tables take
+// both steps in one launch.
 #include "awq_cache.hpp"
 
 namespace awq {
@@ -65,23 +66,19 @@ struct Score {
   static constexpr int CHUNKS = D / 4, L = CHUNKS <= 16 ? 16 : CHUNKS <= 32 ? 32 : 64, ROWS = 64 / L, PAGES = 16 * ROWS;
 };
 
-template <int D>
-__global__ __launch_bounds__(256) void score_kernel(SelectArgs a, CacheArgs c, SeqArgs s, int batches,
-                                                    uint64_t* __restrict__ keys) {
+// Scores of pages p0 .. p0 + PAGES - 1, then of those `step` further, below p1, by one wave, of token t and a key head:
+// put(page - span.from, score).
+template <int D, typename Put>
+__device__ __forceinline__ void score_pages(const SelectArgs& a, const CacheArgs& c, const SeqArgs& s, const Sequence& q,
+                                            int t, int head, int p0, int step, int p1, int from, Put put) {
   using P = Score<D>;
   constexpr int L = P::L;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = blockIdx.x / c.heads, head = blockIdx.x % c.heads;
-  Sequence q;
-  const Span span = span_of(a, s, c.shift, t, q);
-  int p0 = span.from + (int)(blockIdx.y * 4 + wave) * batches * P::PAGES;
-  if (p0 >= span.to) return;
-  const int p1 = min(span.to, p0 + batches * P::PAGES);
-  const int chunk = lane & (L - 1), row = lane / L;
+  const int lane = threadIdx.x & 63, chunk = lane & (L - 1), row = lane / L;
   const bool high = chunk >= D / 8, live = chunk < P::CHUNKS;
   const int group = a.q_heads / c.heads, channel = 8 * (high ? chunk - D / 8 : chunk);
   // the pages' numbers, one per lane, while the queries arrive
   const int* table = s.tables + (int64_t)q.index * s.width;
-  auto number_of = [&](int from) { return page_number(c, table[min(from + min(lane, P::PAGES - 1), p1 - 1)]); };
+  auto number_of = [&](int at) { return page_number(c, table[min(at + min(lane, P::PAGES - 1), p1 - 1)]); };
   int number = number_of(p0);
   double w[8];
 #pragma unroll
@@ -112,16 +109,15 @@ __global__ __launch_bounds__(256) void score_kernel(SelectArgs a, CacheArgs c, S
   u32x4 used;
 #pragma unroll
   for (int i = 0; i < 4; ++i) used[i] = (w[2 * i] != 0.0 ? 0xFFFFu : 0u) | (w[2 * i + 1] != 0.0 ? 0xFFFF0000u : 0u);
-  uint64_t* out = keys + ((int64_t)t * c.heads + head) * s.width;
 #pragma unroll 1
-  for (; p0 < p1; p0 += P::PAGES) {
+  for (; p0 < p1; p0 += step) {
     u32x4 raw[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const int64_t page = __shfl(number, j * P::ROWS + row);
       raw[j] = *reinterpret_cast<const u32x4*>(c.bounds + (page * c.heads + head) * 2 * D + (live ? 8 * chunk : 0));
     }
-    if (p0 + P::PAGES < p1) number = number_of(p0 + P::PAGES);
+    if (p0 + step < p1) number = number_of(p0 + step);
     double sum[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -136,19 +132,33 @@ __global__ __launch_bounds__(256) void score_kernel(SelectArgs a, CacheArgs c, S
 #pragma unroll
     for (int m = 16; m < L; m <<= 1) total += swap_lanes(total, m);
     const int page = p0 + (lane & 15) * P::ROWS + row;
-    if (chunk < 16 && page < p1) out[page - span.from] = ordered(total);
+    if (chunk < 16 && page < p1) put(page - from, ordered(total));
   }
+}
+
+template <int D>
+__global__ __launch_bounds__(256) void score_kernel(SelectArgs a, CacheArgs c, SeqArgs s, int batches,
+                                                    uint64_t* __restrict__ keys) {
+  constexpr int PAGES = Score<D>::PAGES;
+  const int wave = threadIdx.x >> 6, t = blockIdx.x / c.heads, head = blockIdx.x % c.heads;
+  Sequence q;
+  const Span span = span_of(a, s, c.shift, t, q);
+  const int p0 = span.from + (int)(blockIdx.y * 4 + wave) * batches * PAGES;
+  if (p0 >= span.to) return;
+  uint64_t* out = keys + ((int64_t)t * c.heads + head) * s.width;
+  score_pages<D>(a, c, s, q, t, head, p0, PAGES, min(span.to, p0 + batches * PAGES), span.from,
+                 [&](int i, uint64_t score) { out[i] = score; });
 }
 
 constexpr int kScoreWaves = 4096;  // four per SIMD
 
-constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kKept = 8;  // scores that a thread holds at a time: numbers tid, tid + 1024, ... of 8192
+constexpr int kKept = 8;  // scores that a thread holds at a time: of 1024 threads numbers tid, tid + 1024, ... of 8192
 
 // The place of each flagged score among all flagged ones before it, `placed` so far.
 struct Places {
   unsigned at[kKept];
 };
+template <int WAVES>
 __device__ __forceinline__ Places places_of(const bool (&flag)[kKept], unsigned* part, unsigned& placed) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   Places p;
@@ -156,53 +166,57 @@ __device__ __forceinline__ Places places_of(const bool (&flag)[kKept], unsigned*
   for (int k = 0; k < kKept; ++k) {
     const unsigned long long all = __ballot(flag[k]);
     p.at[k] = __popcll(all & ((1ull << lane) - 1));
-    if (lane == 0) part[k * kWaves + wave] = __popcll(all);
+    if (lane == 0) part[k * WAVES + wave] = __popcll(all);
   }
   __syncthreads();
-  if (wave == 0) {  // (128 counts, two per lane)
-    static_assert(kKept * kWaves == 128, "two counts per lane");
-    const unsigned x = part[2 * lane], y = part[2 * lane + 1], upto = prefix_sum((int)(x + y));
-    part[2 * lane] = upto - x - y;
-    part[2 * lane + 1] = upto - y;
-    if (lane == 63) part[128] = upto;
+  constexpr int COUNTS = kKept * WAVES, EACH = COUNTS / 64;
+  static_assert(EACH == 1 || EACH == 2, "one or two counts per lane");
+  if (wave == 0) {
+    const unsigned x = part[EACH * lane], y = EACH == 2 ? part[EACH * lane + 1] : 0, upto = prefix_sum((int)(x + y));
+    part[EACH * lane] = upto - x - y;
+    if (EACH == 2) part[EACH * lane + 1] = upto - y;
+    if (lane == 63) part[COUNTS] = upto;
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kKept; ++k) p.at[k] += placed + part[k * kWaves + wave];
-  placed += part[128];
+  for (int k = 0; k < kKept; ++k) p.at[k] += placed + part[k * WAVES + wave];
+  placed += part[COUNTS];
   __syncthreads();
   return p;
 }
 
-__global__ __launch_bounds__(kThreads) void choose_kernel(SelectArgs a, CacheArgs c, SeqArgs s,
-                                                          const uint64_t* __restrict__ keys) {
-  __shared__ unsigned count[256], part[130], found[3];
-  __shared__ uint64_t bits[kWaves];
-  const int t = blockIdx.x / c.heads, head = blockIdx.x % c.heads, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  Sequence q;
-  const Span span = span_of(a, s, c.shift, t, q);
-  int* out = a.pages + ((int64_t)t * c.heads + head) * a.count;
-  if (q.rows == 0) return;  // rows of no sequence stay as they are
+// The pages of a token and key head that are chosen whatever the scores; whether that is all.
+template <int THREADS>
+__device__ __forceinline__ bool choose_fixed(const SelectArgs& a, const Span& span, int* out) {
+  const int tid = threadIdx.x;
   if (span.have <= a.count) {
-    for (int i = tid; i < a.count; i += kThreads) out[i] = i < span.have ? i : -1;
-    return;
+    for (int i = tid; i < a.count; i += THREADS) out[i] = i < span.have ? i : -1;
+    return true;
   }
-  for (int i = tid; i < a.first; i += kThreads) out[i] = i;
-  for (int i = tid; i < a.recent; i += kThreads) out[a.count - a.recent + i] = span.to + i;
-  const uint64_t* in = keys + ((int64_t)t * c.heads + head) * s.width;
-  const int n = span.to - span.from, rounds = (n + kKept * kThreads - 1) / (kKept * kThreads);
-  int wanted = a.count - a.first - a.recent;  // 0 <= wanted < n
-  if (wanted == 0) return;
+  for (int i = tid; i < a.first; i += THREADS) out[i] = i;
+  for (int i = tid; i < a.recent; i += THREADS) out[a.count - a.recent + i] = span.to + i;
+  return a.count == a.first + a.recent;
+}
+
+// Of scores in[0 .. span.to - span.from - 1] the largest, by a workgroup.
+template <int THREADS>
+__device__ __forceinline__ void choose(const SelectArgs& a, const Span& span, int* out, const uint64_t* in) {
+  constexpr int WAVES = THREADS / 64;
+  __shared__ unsigned count[256], part[kKept * WAVES + 1], found[3];
+  __shared__ uint64_t bits[WAVES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = span.to - span.from, rounds = (n + kKept * THREADS - 1) / (kKept * THREADS);
+  int wanted = a.count - a.first - a.recent;  // 0 < wanted < n
 
   uint64_t kept[kKept];
   auto read = [&](int round) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < kKept; ++k) {
-      const int i = (round * kKept + k) * kThreads + tid;
+      const int i = (round * kKept + k) * THREADS + tid;
       kept[k] = i < n ? in[i] : 0;
     }
   };
-  auto number = [&](int round, int k) __attribute__((always_inline)) { return (round * kKept + k) * kThreads + tid; };
+  auto number = [&](int round, int k) __attribute__((always_inline)) { return (round * kKept + k) * THREADS + tid; };
 
   // the highest bit in which the scores differ
   const uint64_t one = in[0];
@@ -222,7 +236,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectArgs a, CacheArg
   __syncthreads();
   differ = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) differ |= bits[w];
+  for (int w = 0; w < WAVES; ++w) differ |= bits[w];
   const int top = differ ? 64 - __builtin_clzll(differ) : 0;  // bits 0 .. top - 1 differ
   // the wanted-th largest: its bits from `top` down, 8 at a time, until no more scores share those found than are
   // wanted of them
@@ -274,7 +288,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectArgs a, CacheArg
       bool equal[kKept];
 #pragma unroll
       for (int k = 0; k < kKept; ++k) equal[k] = number(r, k) < n && kept[k] == edge;
-      const Places p = places_of(equal, part, tied);
+      const Places p = places_of<WAVES>(equal, part, tied);
 #pragma unroll
       for (int k = 0; k < kKept; ++k)
         take[k] = number(r, k) < n && (kept[k] > edge || (equal[k] && p.at[k] < (unsigned)wanted));
@@ -282,11 +296,43 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectArgs a, CacheArg
 #pragma unroll
       for (int k = 0; k < kKept; ++k) take[k] = number(r, k) < n && kept[k] >= edge;
     }
-    const Places p = places_of(take, part, placed);
+    const Places p = places_of<WAVES>(take, part, placed);
 #pragma unroll
     for (int k = 0; k < kKept; ++k)
       if (take[k]) out[p.at[k]] = span.from + number(r, k);
   }
+}
+
+__global__ __launch_bounds__(1024) void choose_kernel(SelectArgs a, CacheArgs c, SeqArgs s, const uint64_t* __restrict__ keys) {
+  const int t = blockIdx.x / c.heads, head = blockIdx.x % c.heads;
+  Sequence q;
+  const Span span = span_of(a, s, c.shift, t, q);
+  int* out = a.pages + ((int64_t)t * c.heads + head) * a.count;
+  if (q.rows == 0) return;  // rows of no sequence stay as they are
+  if (choose_fixed<1024>(a, span, out)) return;
+  choose<1024>(a, span, out, keys + ((int64_t)t * c.heads + head) * s.width);
+}
+
+// Both in one launch, the scores in LDS, where the tables are so narrow that one workgroup reads a row's bounds in the
+// time of a launch (17 tokens of 30 key heads, 24 pages: select and attend 66.6 us, in two launches 76; 1 token of 8 pages of
+// 128 channels 31.3, 36; but 13 tokens of one head, 950 pages of 256 channels 50.5, 37.5).
+constexpr int kAlone = 512;  // pages
+
+template <int D>
+__global__ __launch_bounds__(512) void select_kernel(SelectArgs a, CacheArgs c, SeqArgs s) {
+  __shared__ uint64_t keys[kAlone];
+  const int t = blockIdx.x / c.heads, head = blockIdx.x % c.heads;
+  Sequence q;
+  const Span span = span_of(a, s, c.shift, t, q);
+  int* out = a.pages + ((int64_t)t * c.heads + head) * a.count;
+  if (q.rows == 0) return;
+  if (choose_fixed<512>(a, span, out)) return;  // (the same for the whole workgroup)
+  constexpr int PAGES = Score<D>::PAGES;
+  const int p0 = span.from + (int)(threadIdx.x >> 6) * PAGES;
+  if (p0 < span.to)
+    score_pages<D>(a, c, s, q, t, head, p0, 8 * PAGES, span.to, span.from, [&](int i, uint64_t score) { keys[i] = score; });
+  __syncthreads();
+  choose<512>(a, span, out, keys);
 }
 
 template <int D>
@@ -305,20 +351,21 @@ void launch_score(const SelectArgs& a, const CacheArgs& c, const SeqArgs& s, uin
 }  // namespace
 
 size_t select_workspace_bytes(int T, int kv_heads, int width, int count) {
-  return width > count ? ((size_t)T * kv_heads * width * 8 + 15) & ~(size_t)15 : 0;
+  return width > count && width > kAlone ? ((size_t)T * kv_heads * width * 8 + 15) & ~(size_t)15 : 0;
 }
 
 hipError_t launch_select(const SelectArgs& a, const CacheArgs& c, const SeqArgs& s, void* workspace, hipStream_t stream) {
   uint64_t* keys = static_cast<uint64_t*>(workspace);
-  if (s.width > a.count) {  // (otherwise no sequence has more pages than are wanted)
-#define AWQ_SCORE(D) launch_score<D>(a, c, s, keys, stream)
-    if (c.dim == 64) AWQ_SCORE(64);
-    else if (c.dim == 96) AWQ_SCORE(96);
-    else if (c.dim == 128) AWQ_SCORE(128);
-    else AWQ_SCORE(256);
-#undef AWQ_SCORE
-  }
-  hipLaunchKernelGGL(choose_kernel, dim3(s.T * c.heads), dim3(kThreads), 0, stream, a, c, s, keys);
+#define AWQ_SELECT(D)                                                                                       \
+  if (s.width <= kAlone) hipLaunchKernelGGL((select_kernel<D>), dim3(s.T * c.heads), dim3(512), 0, stream, a, c, s); \
+  else if (s.width > a.count) launch_score<D>(a, c, s, keys, stream)
+  if (c.dim == 64) { AWQ_SELECT(64); }
+  else if (c.dim == 96) { AWQ_SELECT(96); }
+  else if (c.dim == 128) { AWQ_SELECT(128); }
+  else { AWQ_SELECT(256); }
+#undef AWQ_SELECT
+  if (s.width > kAlone)  // (with no more pages than are wanted there are no scores, and none are looked at)
+    hipLaunchKernelGGL(choose_kernel, dim3(s.T * c.heads), dim3(1024), 0, stream, a, c, s, keys);
   return hipGetLastError();
 }
 

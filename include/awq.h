@@ -504,7 +504,7 @@ size_t awq_attend_workspace_bytes(int32_t T, int32_t B, int32_t q_heads, int32_t
  * first >= 0, recent >= 1, first + recent <= count (AWQ_ERR_OPTION).  T * kv_heads < 2^22.
  * Deterministic.
  * workspace: awq_select_pages_workspace_bytes() bytes (a score per token, key head and
- * page of the tables), as awq_attend's.
+ * page of the tables; 0 for narrow ones), as awq_attend's.
  */
 int awq_select_pages(const void* q, int32_t ldq, const int32_t* offsets, const int32_t* lengths, const int32_t* tables,
                      int32_t width, int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,

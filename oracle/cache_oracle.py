@@ -58,8 +58,9 @@ def attend_row(q, k, v, scale):
 def scores(q, bounds):
     """q [G, D], bounds [pages, 2, D] -> a score per page."""
     q = q.astype(np.float64)[None]
-    b = bounds.astype(np.float64)
-    return np.maximum(q * b[:, None, 0], q * b[:, None, 1]).sum((1, 2))
+    lo, hi = (bounds.astype(np.float64)[:, None, i] for i in (0, 1))
+    with np.errstate(invalid="ignore"):  # (the side that a channel does not use may be anything)
+        return np.where(q == 0, 0.0, np.where(q > 0, q * hi, q * lo)).sum((1, 2))
 
 
 def select(q, bounds, have, count, first, recent):

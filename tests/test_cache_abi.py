@@ -124,9 +124,11 @@ def test_pages_refusals(lib):
         assert selecting(lib, **{name: 0}) == awq.AWQ_ERR_NULL, name
     for name, at in (("q", P[0] + 8), ("bounds", P[11] + 8), ("chosen", P[12] + 2)):
         assert selecting(lib, **{name: at}) == awq.AWQ_ERR_ALIGN, name
-    need = lib.awq_select_pages_workspace_bytes(4, 2, 8, 4)
+    need = lib.awq_select_pages_workspace_bytes(4, 2, 5000, 4)
     assert need > 0 and lib.awq_select_pages_workspace_bytes(4, 2, 8, 8) == 0
-    assert selecting(lib, wsb=need - 1) == awq.AWQ_ERR_WORKSPACE and selecting(lib, ws=0) == awq.AWQ_ERR_NULL
+    assert lib.awq_select_pages_workspace_bytes(4, 2, 512, 4) == 0 and lib.awq_select_pages_workspace_bytes(4, 2, 513, 4) > 0
+    assert selecting(lib, width=5000, wsb=need - 1) == awq.AWQ_ERR_WORKSPACE
+    assert selecting(lib, width=5000, ws=0, wsb=need) == awq.AWQ_ERR_NULL
     for bad in ((0, 2, 8, 4), (4, 0, 8, 4), (4, 2, 0, 4), (4, 2, 8, 0), (1 << 24, 2, 8, 4)):
         assert lib.awq_select_pages_workspace_bytes(*bad) == 0, bad
     for kw in (dict(count=0), dict(count=1 << 29)):

@@ -54,6 +54,24 @@ def test_first_and_recent(count, first, recent):
     check(batch([1, 1, 3], [1600, 16 * 89, 20], 8, 2, 128, 16, pad=1), count, first, recent)
 
 
+@pytest.mark.parametrize("width", [512, 513])  # scores in one launch and in two
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+def test_wide_tables(D, width):
+    for pages in (1, 3, 17, 64, 400, 512):
+        b = batch([1, 2], [pages * 16 - 1, max(0, pages * 16 - 40)], 8, 2, D, 16, width=width, seed=pages)
+        for count, first, recent in ((2, 1, 1), (9, 0, 1), (16, 3, 4), (6, 2, 4)):
+            check(b, count, first, recent)
+    b = batch([1], [500 * 16 - 1], 8, 1, D, 16, width=width)
+    b.bounds[:] = 1.0  # all equal
+    check(b, 50)
+    b.bounds[::3] = 2.0
+    check(b, 300)
+    check(b, 150)
+    b.bounds[::5, :, 0, 3] = np.nan
+    b.bounds[::7, :, 1, 4] = np.inf
+    check(b, 100)
+
+
 def test_many_pages():
     check(batch([1], [16 * 9000], 8, 1, 64, 16), 128, 1, 2)
     check(batch([1], [16 * 20001], 2, 1, 64, 16), 5, 1, 2)
