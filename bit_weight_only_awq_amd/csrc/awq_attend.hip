@@ -218,8 +218,8 @@ int splits_of(int64_t tiles, int64_t stages, int slots, double extra) {
 // 48 x 1 x 8, 7 to 4000 before: 96, 111; 8 x 5 x 8: 45, 33.3.  (Many key heads with several tokens each, 30 x 16 x 1 of 32
 // heads: 102, 85: the join's rows.)
 // Up to 16 rows the waves' products are of 16: 8 x 2 x 8 32.0, of 32 32.4; 8 x 4 x 8 43.1, 33.9.
-// Shared keys always by row tiles: 1 x 1 x 8 after 8192 19.0, by waves 30.9; 16 x 1 x 8 26.1, 61.4; with up to 16 rows per
-// sequence in one launch with the waves: 16 x 1 x 8 25.9, in two 38.2; 61 x 1 x 8 47, 68.
+// Shared keys always by row tiles: 1 x 1 x 8 after 8192 19.0, by waves 30.9; 16 x 1 x 8 26.1, 61.4; and in one launch with
+// the waves, whose products are of 16 rows there: 16 x 1 x 8 25.9, in two 38.2; 61 x 1 x 8 47, 68; 1 x 6 x 3 after 1600 18, 23.
 AttendPlan plan_of(int T, int B, int q_heads, int kv_heads, int dim, int page_size, int width, int shared, bool list) {
   const int group = q_heads / kv_heads, stage = dim == 256 ? 32 : 64, slots = dim == 256 ? kUnits : 2 * kUnits;
   const int64_t rows = (int64_t)T * group;
@@ -228,11 +228,10 @@ AttendPlan plan_of(int T, int B, int q_heads, int kv_heads, int dim, int page_si
   // (units of the waves: 16 rows, at least a block of them per sequence, times key heads and blocks of 32 keys)
   const int64_t units = kv_heads * (rows / 16 + B) * ((int64_t)width * page_size / 32 + 1);
   p.own_few = list || (rows <= 32 * (int64_t)B && units < kMostUnits);
-  p.rows = rows <= 16 * (int64_t)(list ? T : B) ? 16 : 32;
-  p.both = p.own_few && p.shared && p.rows == 16;
+  p.rows = p.shared || rows <= 16 * (int64_t)(list ? T : B) ? 16 : 32;
   p.own_splits = p.shared_splits = 1;
   if (p.shared)
-    p.shared_splits = splits_of((rows + 127) / 128 * kv_heads, (shared + stage - 1) / stage, p.both ? kUnits : slots, 3.0);
+    p.shared_splits = splits_of((rows + 127) / 128 * kv_heads, (shared + stage - 1) / stage, p.both() ? kUnits : slots, 3.0);
   if (!p.own_few) {
     const int64_t keys = (int64_t)width * page_size - shared;
     p.own_splits = splits_of(((rows + 127) / 128 + B / 2) * kv_heads, (keys + stage - 1) / stage, slots, 3.0);
@@ -267,7 +266,7 @@ hipError_t launch_attend(const AttendArgs& a, const CacheArgs& c, const SeqArgs&
   const Partials p = partials(plan, (int64_t)s.T * a.q_heads, c.dim, workspace);
   hipError_t e = hipSuccess;
   if (plan.shared || !plan.own_few) e = launch_attend_tiles(a, c, s, plan, p, stream);
-  if (e == hipSuccess && plan.own_few && !plan.both) e = launch_attend_waves(a, c, s, plan, p, stream);
+  if (e == hipSuccess && plan.own_few && !plan.both()) e = launch_attend_waves(a, c, s, plan, p, stream);
   if (e != hipSuccess || (!plan.own_few && plan.slices() == 0)) return e;
   const JoinArgs j{unit_args(a, c, plan), plan.slices()};
 #define AWQ_JOIN(D) launch_join<D>(a, c, s, plan.own_few, j, p, stream)

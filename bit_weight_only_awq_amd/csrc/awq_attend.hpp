@@ -18,8 +18,8 @@ struct AttendPlan {
   bool own_few;  // a sequence's own keys: with the waves, or with the workgroups
   bool shared;   // there are shared keys
   int rows;      // of a wave: 16 or 32
-  bool both;     // waves and workgroups in one launch
   int own_splits, shared_splits;  // of the workgroups
+  bool both() const { return own_few && shared; }  // in one launch
   int own_slices() const { return own_few ? shared : shared || own_splits > 1 ? own_splits : 0; }
   int slices() const { return own_slices() + (shared ? shared_splits : 0); }
 };

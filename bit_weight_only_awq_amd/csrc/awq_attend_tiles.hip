@@ -39,7 +39,7 @@ void launch(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const Att
             hipStream_t stream) {
   const TileArgs x = tile_args(a, c, s, plan);
   const unsigned grid = tile_workgroups(x, c.heads);
-  if (plan.both)
+  if (plan.both())
     hipLaunchKernelGGL((attend_both_kernel<D>), dim3(kUnits + grid), dim3(256), 0, stream, a, c, s, unit_args(a, c, plan), x,
                        p);
   else
