@@ -417,19 +417,21 @@ __device__ __forceinline__ float greatest(const Scores<R>& s) {
   return row_max<R>(m);
 }
 
-// Masks 32 scores, whose greatest is `m` before that, and moves the maximum on; returns what is taken off each, in
-// powers of two.
-template <int D, int R>
-__device__ __forceinline__ float settle(Scores<R>& s, float m, float c, const Seen& seen, Gathered<D, R>& g) {
-  if (!seen.all) {
-    const int h = __lane_id() / R, limit0 = seen.limit0 - 4 * h, limit1 = seen.limit1 - 4 * h;
+// Masks 32 scores; returns their greatest.
+template <int R>
+__device__ __forceinline__ float mask(Scores<R>& s, const Seen& seen) {
+  const int h = __lane_id() / R, limit0 = seen.limit0 - 4 * h, limit1 = seen.limit1 - 4 * h;
 #pragma unroll
-    for (int i = 0; i < Scores<R>::COUNT; ++i) {
-      const int k = 256 / R * (i >> 2) + (i & 3);
-      s.put(i, (k & 15) > (k < 16 ? limit0 : limit1) ? -INFINITY : s.get(i));
-    }
-    m = greatest(s);
+  for (int i = 0; i < Scores<R>::COUNT; ++i) {
+    const int k = 256 / R * (i >> 2) + (i & 3);
+    s.put(i, (k & 15) > (k < 16 ? limit0 : limit1) ? -INFINITY : s.get(i));
   }
+  return greatest(s);
+}
+
+// Moves the maximum on to that of 32 scores, whose greatest is `m`; returns what is taken off each, in powers of two.
+template <int D, int R>
+__device__ __forceinline__ float settle(float m, float c, Gathered<D, R>& g) {
   if (__any((m - g.top) * c > kLag)) {  // (a first score: infinitely above; none yet: NaN, no)
     const float top = m > g.top ? m : g.top;
     const float carry = g.top == top ? 1.0f : __builtin_amdgcn_exp2f((g.top - top) * c);
@@ -444,12 +446,12 @@ __device__ __forceinline__ float settle(Scores<R>& s, float m, float c, const Se
 template <int R>
 struct Weights {
   half8_t part[R / 16];
-  float sum = 0.0f;
+  float pair[R / 4];  // sums of two
   // of scores 2 i and 2 i + 1
   __device__ __forceinline__ void take(int i, const Scores<R>& s, float c, float base) {
     const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s.get(2 * i), c, -base));
     const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s.get(2 * i + 1), c, -base));
-    sum += w0 + w1;
+    pair[i] = w0 + w1;
     part[i >> 2][2 * (i & 3)] = (_Float16)w0;
     part[i >> 2][2 * (i & 3) + 1] = (_Float16)w1;
   }
@@ -485,11 +487,12 @@ __device__ __forceinline__ Weights<R> attend_block(const Addresses<D, R>& at, co
   Scores<R> s = scores_of<D, R, K>(at, q, f, [&](auto jc) __attribute__((always_inline)) {
     if constexpr (decltype(jc)::value == Products<D, R>::SCORES - 1) first_values<D, R, V>(at, v);
   });
-  const float base = settle<D, R>(s, greatest(s), c, seen, g);
+  const float base = settle<D, R>(seen.all ? greatest(s) : mask(s, seen), c, g);
   Weights<R> p;
 #pragma unroll
   for (int i = 0; i < Scores<R>::COUNT / 2; ++i) p.take(i, s, c, base);
-  g.sum += p.sum;
+#pragma unroll
+  for (int i = 0; i < Scores<R>::COUNT / 2; ++i) g.sum += p.pair[i];
   gather<D, R, V>(at, v, p, g, [](auto) __attribute__((always_inline)) {});
   return p;
 }
@@ -504,7 +507,8 @@ __device__ __forceinline__ Weights<R> attend_next(const Addresses<D, R>& at, con
   constexpr int N = Products<D, R>::SCORES, M = Products<D, R>::VALUES, PAIRS = Scores<R>::COUNT / 2;
   half8_t v[kAhead];
   Weights<R> p;
-  const float base = settle<D, R>(s, m, c, seen, g);
+  if (!seen.all) m = mask(s, seen);
+  const float base = settle<D, R>(m, c, g);
   in_order();
   Scores<R> next = scores_of<D, R, K>(at, q, f, [&](auto jc) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value;
@@ -512,14 +516,17 @@ __device__ __forceinline__ Weights<R> attend_next(const Addresses<D, R>& at, con
 #pragma unroll
     for (int i = PAIRS * j / N; i < PAIRS * (j + 1) / N; ++i) p.take(i, s, c, base);
   });
-  g.sum += p.sum;
   float most = -INFINITY;
   gather<D, R, V>(at, v, p, g, [&](auto ic) __attribute__((always_inline)) {
     constexpr int i = decltype(ic)::value;
 #pragma unroll
-    for (int n = PAIRS * i / M; n < PAIRS * (i + 1) / M; ++n) most = larger(larger(most, next.get(2 * n)), next.get(2 * n + 1));
+    for (int n = PAIRS * i / M; n < PAIRS * (i + 1) / M; ++n) {
+      most = larger(larger(most, next.get(2 * n)), next.get(2 * n + 1));
+      g.sum += p.pair[n];
+    }
     if constexpr (i % 2 == 0) beside(std::integral_constant<int, i / 2>{});
   });
+  asm volatile("" : "+v"(g.sum));  // (here, beside the matrix instructions, and not after them)
   s = next;
   m = row_max<R>(most);
   return p;

@@ -136,7 +136,7 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
   // past the least place of the workgroup's rows some values are not to be seen by some row
   auto hide = [&](int block, int slot) __attribute__((always_inline)) {
     const int key = key0 + 32 * block;
-    if (key + 31 <= tile_least) return 0u;
+    if (key + 31 <= tile_least) return 0u;  // (the same for the whole workgroup)
     const uint32_t met = (uint32_t)hide_strange<D, 32>(ring + (2 * slot + 1) * SLOT, threadIdx.x, 256,
                                                        [&](int h, int& behind, int& upto) {
                                                          behind = tile_least - key - 16 * h;
@@ -176,26 +176,39 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
   }
   // One block: its scores are there, the next block's are made; the one after that may still be on its way, and the
   // fourth takes the place of the last (past the end, the last block again: its scores count nothing).
-  auto step = [&](int block, auto slot) __attribute__((always_inline)) {
+  auto step = [&](int block, auto slot, auto plain) __attribute__((always_inline)) {
+    asm volatile("" : "+v"(s_now.s));  // (keeps the scores of both loops below in the same two sets of registers)
     constexpr int HERE = decltype(slot)::value, NEXT = (HERE + 1) % RING;
     wait_loads<(RING - 3) * LOADS>();
     meet();
     Fragments f = first_keys<D, 32, 2 * NEXT * SLOT>(places);
     const char* base = source_of(min(block + RING - 1, to - 1));
-    const uint32_t odd = hide(block, HERE);
-    const Seen seen = seen_of(block);
+    uint32_t odd = 0;
+    Seen seen{0, 0, true};
+    if constexpr (!decltype(plain)::value) {
+      odd = hide(block, HERE);
+      seen = seen_of(block);
+    }
     const Weights<32> p = attend_next<D, 32, 2 * NEXT * SLOT, (2 * HERE + 1) * SLOT>(
         places, q, f, scale, seen, s_now, m_now, g, [&](auto n) __attribute__((always_inline)) {
           constexpr int i = decltype(n)::value;
           static_assert(Products<D, 32>::VALUES == 2 * LOADS, "a load for every other of them");
           load_to_lds<1>(base, {lane_from[i]}, own + 2 * SLOT * ((HERE + RING - 1) % RING) + 1024 * i);
         });
-    finish(block, odd, p, seen);
+    if constexpr (!decltype(plain)::value) finish(block, odd, p, seen);
   };
-  for (int block = from; block < to; block += RING)
+  // Blocks that all rows see whole, four at a time, without a thought for what some must not see (with both in one loop
+  // the scores are copied for every block).
+  const int whole = max(tile_least - key0 + 1, 0) / 32;
+  int block = from;
+  for (; block + RING <= min(whole, to); block += RING)
+    each<0, RING, 1>([&](auto slot) __attribute__((always_inline)) {
+      step(block + decltype(slot)::value, slot, std::true_type{});
+    });
+  for (; block < to; block += RING)
     each<0, RING, 1>([&](auto slot) __attribute__((always_inline)) {
       constexpr int i = decltype(slot)::value;
-      if (block + i < to) step(block + i, slot);
+      if (block + i < to) step(block + i, slot, std::false_type{});
     });
   wait_loads<0>();  // (those past the end)
   if (live) write_rows(g, scale, a, p, rows, group, head, slice, nullptr, nullptr);
