@@ -1,7 +1,7 @@
 // Attention of many rows (awq_attend_tiles.hpp), and of many rows of shared keys
 // together with few rows per sequence (awq_attend_waves.hpp): the first is bound by
 // the matrix cores, the second by HBM, and in one launch each compute unit holds a
-// workgroup of either kind (61 tokens of 64 query heads after 8192: 37 us; one launch
+// workgroup of either kind (61 tokens of 64 query heads after 8192: 34 us; one launch
 // after the other, with their joins, 68 us for 47).
 #include "awq_attend_tiles.hpp"
 #include "awq_attend_waves.hpp"

@@ -7,9 +7,9 @@
 // once per sequence.
 //
 // Bound: the matrix cores (4 D operations per row and key) beside the
-// exponentials: 13 questions after 16384 shared tokens 552-572 us, 0.87-0.90 PFLOP/s
+// exponentials: 13 questions after 16384 shared tokens 522-539 us, 0.92-0.95 PFLOP/s
 // with two workgroups per unit at the power limit; a wave that has its SIMD to
-// itself takes 0.9 us per block (a prompt of 2000, whose last tiles see 64 of them: 56
+// itself takes 0.8 us per block (a prompt of 2000, whose last tiles see 64 of them: 53
 // us).  A block of keys and values goes straight to LDS while the one before it is
 // multiplied, with one barrier per block.  Where the row tiles are
 // too few for the chip, the keys are split as well and the parts joined by a second
