@@ -82,7 +82,7 @@ def run(b, R, interleaved=False, positions=None, axes=None, bounds=True, in_plac
     return q, cache
 
 
-@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (32, 32), (8, 1), (14, 2), (64, 8), (7, 7)])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (36, 36), (8, 1), (14, 2), (64, 8), (7, 7)])
 @pytest.mark.parametrize("D", [64, 96, 128, 256])
 def test_heads(Hq, Hkv, D):
     run(Batch([1, 2, 5], [0, 15, 33], Hq, Hkv, D, 16, pad=2, seed=Hq), D)
@@ -101,7 +101,7 @@ def test_batches(B):
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("D,R", [(64, 32), (96, 16), (128, 0), (128, 64), (128, 112), (256, 128)])
 def test_part_of_the_channels(D, R, interleaved):
-    run(Batch([3, 20], [9, 0], 8, 2, D, 16), R, interleaved)
+    run(Batch([3, 20], [9, 0], 6, 2, D, 16), R, interleaved)
 
 
 @pytest.mark.parametrize("interleaved", [False, True])

@@ -11,7 +11,7 @@ from tests._cache import Batch
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
-HEADS = [(1, 1), (4, 4), (8, 1), (10, 2), (14, 2), (16, 1), (32, 1), (40, 1), (64, 8)]
+HEADS = [(1, 1), (4, 4), (8, 1), (10, 2), (14, 2), (16, 1), (36, 1), (40, 1), (64, 8)]
 
 
 def attend(b, **kw):
