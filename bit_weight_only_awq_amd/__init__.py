@@ -986,7 +986,10 @@ def attention(x: torch.Tensor, qkv: PackedWeight, o: PackedWeight, cache: KvCach
               axes: Optional[torch.Tensor] = None, interleaved: bool = False) -> torch.Tensor:
     """A decoder block's attention for new tokens ``x`` [T, K]: the fused q/k/v layer (``pack_fused([q, k, v])``,
     ``bias`` its own), the tokens' keys and values appended, attention over the cache, the output layer, plus
-    ``residual``.  With ``pages`` above 0 each token attends to that many pages only (``select_pages``)."""
+    ``residual``.  With ``pages`` above 0 each token attends to that many pages only (``select_pages``); these come from
+    the token's own table, so ``shared`` must be 0."""
+    if pages and shared:
+        raise ValueError("chosen pages are of each sequence's own table: with pages, shared must be 0")
     rows = linear_fused(x, qkv, bias=bias)
     q = append_kv(rows, cache, seqs, inv_freq, positions, axes, interleaved)
     if pages:

@@ -160,6 +160,11 @@ def test_binding_refusals():
         awq.attend_pages(q, cache, seqs, torch.zeros((4, 3, 5), dtype=torch.int32))
 
 
+def test_attention_refuses_chosen_pages_of_a_shared_prefix():
+    with pytest.raises(ValueError, match="shared must be 0"):
+        awq.attention(torch.zeros((1, 64), dtype=torch.float16), None, None, None, None, shared=16, pages=4)
+
+
 def test_oracle_by_hand():
     q = np.array([1.0, -2.0])
     k, v = np.array([[0.0, 0.0], [np.log(3.0), 0.0]]), np.array([[4.0, 0.0], [0.0, 8.0]])

@@ -232,3 +232,52 @@ def test_a_block_in_a_graph(mode):
         for got, want in zip(*caches):
             assert torch.equal(got, want)
         lengths += 1
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("new,past,shared", [(3, 200, 0), (6, 200, 0), (20, 200, 0), (150, 400, 0), (3, 200, 64), (40, 30, 160)])
+def test_values_that_are_not_finite_reach_their_rows_only(new, past, shared, D):
+    """An infinity and a NaN among the new tokens' values: rows before them are as without, rows from them on have them in
+    their channels and nothing else."""
+    awq = G.lib()
+    b = Batch([new, 1], [past, 9], 8, 2, D, 16, shared=shared, seed=new)
+    p = shared + past + new // 2
+    page, slot = b.tables[0, p // 16], p % 16
+    b.v[page, 1, slot, 5], b.v[page, 0, slot, D - 3] = np.inf, np.nan
+    cache, seqs = b.device()
+    q = G.dev_f16(b.q)
+    results = [awq.attend(q, cache, seqs, shared=shared)]
+    if shared == 0:
+        pages = torch.arange(b.width, dtype=torch.int32, device="cuda").expand(b.T, 2, b.width).contiguous()
+        results.append(awq.attend_pages(q, cache, seqs, pages))
+    b.v[page, 1, slot, 5] = b.v[page, 0, slot, D - 3] = 0
+    rows = sorted({0, new // 2 - 1, new // 2, new - 1, new})
+    ref, bound, _ = b.expected(rows=rows)
+    for y in results:
+        got = y.cpu().numpy().astype(np.float64)[rows].reshape(len(rows), 8, D)
+        for i, t in enumerate(rows):
+            sees = new // 2 <= t < new
+            assert np.all(np.isposinf(got[i, 4:, 5])) if sees else np.all(np.isfinite(got[i, 4:, 5])), (t, "infinity")
+            assert np.all(np.isnan(got[i, :4, D - 3])) if sees else np.all(np.isfinite(got[i, :4, D - 3])), (t, "NaN")
+            keep = np.ones((8, D), bool)
+            if sees:
+                keep[4:, 5] = keep[:4, D - 3] = False
+            off = np.abs(got[i][keep] - ref[i].reshape(8, D)[keep])
+            assert np.all(off <= bound[i].reshape(8, D)[keep]), (t, float(off.max()))
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+def test_rising_scores_at_every_head_size(D):
+    """The running maximum moves at every block, in waves and in row tiles: sums are rescaled each time."""
+    awq = G.lib()
+    for new, past in ((1, 700), (5, 300), (70, 300)):
+        b = Batch([new, 1], [past, 40], 4, 1, D, 16, seed=new)
+        for s in range(2):
+            for j in range(b.lengths[s]):
+                b.k[b.tables[s, j // 16], :, j % 16] = 0
+                b.k[b.tables[s, j // 16], :, j % 16, 0] = j * 0.5
+        for sign in (1.0, -1.0):
+            b.q[:] = 0
+            b.q.reshape(b.T, 4, D)[:, :, 0] = sign
+            cache, seqs = b.device()
+            b.check(awq.attend(G.dev_f16(b.q), cache, seqs, scale=1.0), f"{new} rows, heads of {D}, {sign}", scale=1.0)
