@@ -196,14 +196,14 @@ __global__ __launch_bounds__(256) void join_slices_kernel(AttendArgs a, SeqArgs 
 }
 
 // The keys' splits over which `tiles` workgroups take the least time, in rounds of two per compute unit (one where
-// a head is 256 wide), a stage being the unit, what a workgroup does besides costing `extra` of them, and writing and
+// a head is 256 wide), a stage being the unit, what a workgroup does besides costing three of them, and writing and
 // reading the parts of a tile 0.0085 (128 rows of fp32 sums, there and back).
-int splits_of(int64_t tiles, int64_t stages, int slots, double extra) {
+int splits_of(int64_t tiles, int64_t stages, int slots) {
   int best = 1;
   double least = 1e300;
   for (int n = 1; n <= 64 && n * 2 <= stages + 1 && (n == 1 || tiles * n <= 16 * slots); ++n) {
     const double rounds = (double)((tiles * n + slots - 1) / slots);
-    const double time = rounds * ((double)((stages + n - 1) / n) + extra) + (n > 1 ? 0.0085 * n * tiles : 0.0);
+    const double time = rounds * ((double)((stages + n - 1) / n) + 3.0) + (n > 1 ? 0.0085 * n * tiles : 0.0);
     if (time < least) {
       least = time;
       best = n;
@@ -231,10 +231,10 @@ AttendPlan plan_of(int T, int B, int q_heads, int kv_heads, int dim, int page_si
   p.rows = p.shared || rows <= 16 * (int64_t)(list ? T : B) ? 16 : 32;
   p.own_splits = p.shared_splits = 1;
   if (p.shared)
-    p.shared_splits = splits_of((rows + 127) / 128 * kv_heads, (shared + stage - 1) / stage, p.both() ? kUnits : slots, 3.0);
+    p.shared_splits = splits_of((rows + 127) / 128 * kv_heads, (shared + stage - 1) / stage, p.both() ? kUnits : slots);
   if (!p.own_few) {
     const int64_t keys = (int64_t)width * page_size - shared;
-    p.own_splits = splits_of(((rows + 127) / 128 + B / 2) * kv_heads, (keys + stage - 1) / stage, slots, 3.0);
+    p.own_splits = splits_of(((rows + 127) / 128 + B / 2) * kv_heads, (keys + stage - 1) / stage, slots);
   }
   return p;
 }

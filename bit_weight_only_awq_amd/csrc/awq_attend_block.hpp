@@ -54,11 +54,10 @@ struct Sources {
   using T = Tile<D>;
   static constexpr int KEPT = D == 96 ? 3 : 1, ROWS = 64 / T::CHUNKS;
   uint32_t keys[KEPT], values[KEPT];
-  // loads `first`, `first` + 1, ... (a multiple of 4)
-  __device__ __forceinline__ Sources(int lane, int first) {
+  __device__ __forceinline__ explicit Sources(int lane) {
 #pragma unroll
     for (int i = 0; i < KEPT; ++i) {
-      const int at = 64 * (first + i) + lane, r = at / T::CHUNKS, c = at % T::CHUNKS;
+      const int at = 64 * i + lane, r = at / T::CHUNKS, c = at % T::CHUNKS;
       keys[i] = (uint32_t)(r * T::ROW + 16 * (c ^ T::key_swizzle(r)));
       values[i] = (uint32_t)(r * T::ROW + 16 * (c ^ T::value_swizzle(r)));
     }

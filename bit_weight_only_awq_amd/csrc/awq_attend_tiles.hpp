@@ -116,7 +116,7 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
   const int sixteen = wave & 1, of_values = wave >> 1;
   uint32_t lane_from[LOADS];
   {
-    const Sources<D> sources(lane, 0);
+    const Sources<D> sources(lane);
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) lane_from[i] = of_values ? sources.value(i) : sources.key(i);
   }

@@ -38,7 +38,7 @@ __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs
   int at = wave * n.each;
   const int end = min(n.total, at + n.each);
 
-  const Sources<D> kept(lane, 0);
+  const Sources<D> kept(lane);
   const Addresses<D, R> places((uint32_t)(uintptr_t)ring, lane);
 
   while (at < end) {
