@@ -7,13 +7,20 @@
 // transposed, keys x queries, so that a lane holds 16 scores of one row (lane %
 // 32) and its partner 32 lanes away the other 16 (of 16 rows: 8, and three
 // partners): maximum and sum need one exchange (two), and a change of the maximum
-// scales a lane's sums by a number it has.  The weights, rounded to fp16 (relative 2^-11, as the values are), are then in
+// scales a lane's sums by a number it has.  The weights, rounded to fp16, are then in
 // place as the second operand of the product with the values, whose first operand
 // comes out of LDS transposed; both follow the same order of keys (lane half h holds
 // keys 8 j + 4 h .. + 3, lane quarter h of 16 rows keys 16 j + 4 h .. + 3), so nothing is exchanged.  Sums are fp32.
 //
 // The maximum lags: sums are rescaled only once a score passes it by a factor of
 // 2^8, which fp16 holds for weights and fp32 for sums.
+//
+// The weights' rounding is to what the matrix cores multiply (bf16 would be 2^-9).  They are held 2^7 times as large (up
+// to 2^15 with the lag, of fp16's 2^16): relative 2^-11 down to 2^-21 of the maximum, below that 2^-32 of it at most, so
+// that 2^17 keys of 2^-26 of a great one still count.  l is the sum of the rounded weights: the result is an average of
+// the values, and no channel passes the greatest of them.  (With l of the weights before rounding, 2000 values of 65504 gave
+// infinity; a product of two halves by 1 and 1 adds them to l now: 13 questions 526 -> 530 us, prompt of 2000: 50.7 -> 51.8,
+// single tokens the same.)
 #pragma once
 
 #include <type_traits>
@@ -29,7 +36,8 @@ typedef short short4_t __attribute__((ext_vector_type(4)));
 typedef AWQ_LDS char lds_char;
 
 constexpr float kLog2E = 1.4426950408889634f;
-constexpr float kLag = 8.0f;  // the maximum lags by at most this power of two
+constexpr float kLag = 8.0f;   // the maximum lags by at most this power of two
+constexpr float kLift = 7.0f;  // the weights are held this power of two larger
 
 // Rows of D halves in LDS, as 16-byte chunks: chunk c of row r is at chunk c ^ swizzle(r), so that what
 // half a wave reads in one instruction lies in different banks (16 rows of one chunk for keys; for values 4 rows of 4
@@ -429,6 +437,7 @@ __device__ __forceinline__ float mask(Scores<R>& s, const Seen& seen) {
 }
 
 // Moves the maximum on to that of 32 scores, whose greatest is `m`; returns what is taken off each, in powers of two.
+// (Every part of a row is lifted alike, so that nothing has to be taken off again where parts are joined.)
 template <int D, int R>
 __device__ __forceinline__ float settle(float m, float c, Gathered<D, R>& g) {
   if (__any((m - g.top) * c > kLag)) {  // (a first score: infinitely above; none yet: NaN, no)
@@ -438,21 +447,24 @@ __device__ __forceinline__ float settle(float m, float c, Gathered<D, R>& g) {
     g.sum *= carry;
     g.scale(carry);
   }
-  return g.top == -INFINITY ? 0.0f : g.top * c;
+  return g.top == -INFINITY ? 0.0f : g.top * c - kLift;
 }
 
 // The weights of 32 scores as the values' second operand.
 template <int R>
 struct Weights {
   half8_t part[R / 16];
-  float pair[R / 4];  // sums of two
   // of scores 2 i and 2 i + 1
   __device__ __forceinline__ void take(int i, const Scores<R>& s, float c, float base) {
     const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s.get(2 * i), c, -base));
     const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s.get(2 * i + 1), c, -base));
-    pair[i] = w0 + w1;
     part[i >> 2][2 * (i & 3)] = (_Float16)w0;
     part[i >> 2][2 * (i & 3) + 1] = (_Float16)w1;
+  }
+  // and their sum, added to `sum`
+  __device__ __forceinline__ float add(int i, float sum) const {
+    const half2_t two{part[i >> 2][2 * (i & 3)], part[i >> 2][2 * (i & 3) + 1]};
+    return __builtin_amdgcn_fdot2(two, half2_t((_Float16)1.0f), sum, false);
   }
 };
 
@@ -491,7 +503,7 @@ __device__ __forceinline__ Weights<R> attend_block(const Addresses<D, R>& at, co
 #pragma unroll
   for (int i = 0; i < Scores<R>::COUNT / 2; ++i) p.take(i, s, c, base);
 #pragma unroll
-  for (int i = 0; i < Scores<R>::COUNT / 2; ++i) g.sum += p.pair[i];
+  for (int i = 0; i < Scores<R>::COUNT / 2; ++i) g.sum = p.add(i, g.sum);
   gather<D, R, V>(at, v, p, g, [](auto) __attribute__((always_inline)) {});
   return p;
 }
@@ -521,7 +533,7 @@ __device__ __forceinline__ Weights<R> attend_next(const Addresses<D, R>& at, con
 #pragma unroll
     for (int n = PAIRS * i / M; n < PAIRS * (i + 1) / M; ++n) {
       most = larger(larger(most, next.get(2 * n)), next.get(2 * n + 1));
-      g.sum += p.pair[n];
+      g.sum = p.add(n, g.sum);
     }
     if constexpr (i % 2 == 0) beside(std::integral_constant<int, i / 2>{});
   });

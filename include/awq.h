@@ -477,8 +477,9 @@ int awq_append_kv(const void* x, int32_t ldx, const int32_t* offsets, const int3
  *            have them.
  * y          out  fp16, row t at y + t * ldy; must not overlap an input.  A row without
  *                 keys gives 0.
- * Products, softmax statistics and sums are fp32; the weights p are rounded to fp16 for
- * the matrix cores, the result once.  Keys and values that a row does not see (past its
+ * Products, softmax statistics and sums are fp32; the weights are rounded for the matrix
+ * cores, relative 2^-11 or 2^-32 of the largest, and divided by the sum of the rounded ones;
+ * the result is rounded once.  Keys and values that a row does not see (past its
  * place, or in a page's unused slots) never touch it, NaN and infinities included.
  * Deterministic: the same bits again for the same call.
  * workspace: awq_attend_workspace_bytes() bytes (NULL when 0), contents not needed

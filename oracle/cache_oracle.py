@@ -4,9 +4,10 @@ infrastructure; numpy only, nothing shared with the kernels).
 Error bounds.  Attention: a score is an fp32 sum of D exact products, off by at
 most D * 2^-24 of the sum of their magnitudes, times the scale (two more
 roundings); a weight is the exponential of that difference (its error there, plus
-4 * 2^-24 of the exponential itself), rounded to fp16 (2^-11, or 2^-25 of the
-largest weight where it is subnormal, 2^-17 with a maximum that may lag by a
-factor of 2^8); sums over n keys add n * 2^-24 at most; the result is rounded once
+4 * 2^-24 of the exponential itself), rounded to fp16 (2^-11; where it is
+subnormal there, half a step of 2^-24, for a weight held 2^7 times as large relative to a
+maximum that is at most the greatest: 2^-32 of the largest weight), the same number for the values and for the sum of
+the weights; sums over n keys add n * 2^-24 at most; the result is rounded once
 (2^-11, or 2^-25 among the subnormals).  Rotation: sine and cosine to 2^-23, four fp32
 roundings, one to fp16.
 """
@@ -51,7 +52,8 @@ def attend_row(q, k, v, scale):
     w /= w.sum()
     y = w @ v
     each = 2.0 ** -11 + 2 * (off.max() + (8 + len(k)) * 2.0 ** -24)
-    bound = each * (w @ np.abs(v)) + each * np.abs(y) + 2.0 ** -25 * np.abs(v).sum(0)
+    small = 2.0 ** -32 * w.max()
+    bound = each * (w @ np.abs(v) + np.abs(y)) + small * (np.abs(v).sum(0) + len(k) * np.abs(y))
     return y, bound + np.abs(y) * 2.0 ** -11 + 2.0 ** -25
 
 
