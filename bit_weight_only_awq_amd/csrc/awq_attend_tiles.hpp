@@ -33,10 +33,19 @@ struct TileRing {
   static constexpr int BLOCKS = 4, BYTES = 2 * BLOCKS * 32 * Tile<D>::ROW;
 };
 
-// All rows of the batch as one sequence that ends with the shared keys.
-__device__ __forceinline__ Sequence all_rows(const SeqArgs& s, int shared_keys) {
+// All rows of the batch as one sequence that ends with the shared keys, with the table of the first that has rows (those
+// before it need not have any pages).
+__device__ __forceinline__ Sequence all_rows(const SeqArgs& s, int shift, int shared_keys) {
   const int from = min(max(s.offsets[0], 0), s.T);
-  return Sequence{0, from, max(min(s.offsets[s.B], s.T) - from, 0), shared_keys};
+  Sequence all{0, from, max(min(s.offsets[s.B], s.T) - from, 0), shared_keys};
+  for (int b0 = 0; b0 < s.B; b0 += 64) {
+    const unsigned long long some = __ballot(sequence_at(s, shift, b0 + __lane_id()).rows > 0);
+    if (some != 0) {
+      all.index = b0 + __builtin_ctzll(some);
+      break;
+    }
+  }
+  return all;
 }
 
 // Workgroup number `index` of 256 threads; a ring of TileRing<D>::BYTES and two words.
@@ -64,7 +73,7 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
     split = nth / x.shared_tiles;
     splits = x.shared_splits;
     slice = x.shared_slice + split;
-    seq = all_rows(s, a.shared);
+    seq = all_rows(s, c.shift, a.shared);
     rows = Rows{kTile * (nth - split * x.shared_tiles), seq.rows * group, seq.row0, 0};
     if (rows.first >= rows.total) return;
     key0 = 0;

@@ -46,7 +46,7 @@ struct AttendArgs {
   float scale;
   const int* list;  // [T][heads][count]: pages of the token's sequence, negative: none; or NULL: all of them
   int count;
-  int shared;  // keys that every sequence begins with, read through the first sequence's table
+  int shared;  // keys that every sequence begins with, read through the table of the first that has rows
   _Float16* y;
   int64_t ldy;
 };
