@@ -936,8 +936,8 @@ def attend(q: torch.Tensor, cache: KvCache, seqs: Sequences, scale: Optional[flo
     """Causal attention of the new tokens' queries ``q`` [T, q_heads * head_dim] over their sequences' pages (their own
     keys appended already): fp16 [T, q_heads * head_dim].  ``scale``: head_dim ** -0.5 by default.  ``shared``: how many
     tokens all sequences begin with (a multiple of the page size); their pages, those of the table of the first
-    sequence that has rows, are read and multiplied once for the whole batch.  A row without keys gives 0; rows of no
-    sequence are left as they are."""
+    sequence that has rows, are read and multiplied once for the whole batch (a new token among them sees those
+    up to its own place).  A row without keys gives 0; rows of no sequence are left as they are."""
     return _attend_rows("awq_attend", q, cache, seqs, scale, y, workspace, (shared,),
                         lambda b, size: (b[4], b[5], b[6], b[7], b[8], b[3], size, shared))
 

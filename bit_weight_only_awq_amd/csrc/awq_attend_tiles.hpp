@@ -34,18 +34,46 @@ struct TileRing {
 };
 
 // All rows of the batch as one sequence that ends with the shared keys, with the table of the first that has rows (those
-// before it need not have any pages).
-__device__ __forceinline__ Sequence all_rows(const SeqArgs& s, int shift, int shared_keys) {
+// before it need not have any pages); `within`: one of those with rows among tokens t0 to t1 has new tokens among the
+// shared keys, which see only those up to their own places.
+struct SharedRows {
+  Sequence all;
+  bool within;
+};
+__device__ __forceinline__ Sequence all_tokens(const SeqArgs& s, int shared_keys) {
   const int from = min(max(s.offsets[0], 0), s.T);
-  Sequence all{0, from, max(min(s.offsets[s.B], s.T) - from, 0), shared_keys};
+  return Sequence{0, from, max(min(s.offsets[s.B], s.T) - from, 0), shared_keys};
+}
+__device__ __forceinline__ SharedRows shared_rows(const SeqArgs& s, int shift, Sequence all, int t0, int t1) {
+  SharedRows r{all, false};
+  bool found = false;
   for (int b0 = 0; b0 < s.B; b0 += 64) {
-    const unsigned long long some = __ballot(sequence_at(s, shift, b0 + __lane_id()).rows > 0);
-    if (some != 0) {
-      all.index = b0 + __builtin_ctzll(some);
-      break;
+    const Sequence q = sequence_at(s, shift, b0 + __lane_id());
+    const unsigned long long some = __ballot(q.rows > 0);
+    if (!found && some != 0) {
+      r.all.index = b0 + __builtin_ctzll(some);
+      found = true;
+    }
+    r.within = r.within || __any(q.rows > 0 && q.row0 <= t1 && q.row0 + q.rows > t0 && q.place0() < all.length);
+  }
+  return r;
+}
+// Where the lane's token t is among the shared keys (the last of them, or its own place if that is before it), of tokens
+// t0 to t1, and the least such place.
+__device__ __forceinline__ int shared_place(const SeqArgs& s, int shift, int last, int t, int t0, int t1, int& least) {
+  int place = last;
+  least = last;
+  for (int b0 = 0; b0 < s.B; b0 += 64) {
+    const Sequence q = sequence_at(s, shift, b0 + __lane_id());
+    unsigned long long here = __ballot(q.rows > 0 && q.row0 <= t1 && q.row0 + q.rows > t0 && q.place0() < last);
+    while (here != 0) {
+      const Sequence of = pick(q, __builtin_ctzll(here));
+      here &= here - 1;
+      if (t >= of.row0 && t < of.row0 + of.rows) place = min(place, of.place0() + t - of.row0);
+      least = min(least, of.place0() + max(t0 - of.row0, 0));
     }
   }
-  return all;
+  return place;
 }
 
 // Workgroup number `index` of 256 threads; a ring of TileRing<D>::BYTES and two words.
@@ -69,13 +97,20 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
   int split, splits, slice, key0, keys;
   Rows rows;  // of the workgroup, then of the wave
   Sequence seq;
+  int token0 = 0, token1 = 0;  // of the shared keys: the workgroup's first and last
+  bool within = false;
   if (shared) {
     split = nth / x.shared_tiles;
     splits = x.shared_splits;
     slice = x.shared_slice + split;
-    seq = all_rows(s, c.shift, a.shared);
+    seq = all_tokens(s, a.shared);
     rows = Rows{kTile * (nth - split * x.shared_tiles), seq.rows * group, seq.row0, 0};
     if (rows.first >= rows.total) return;
+    token0 = seq.row0 + rows.first / group;
+    token1 = seq.row0 + (min(rows.first + kTile, rows.total) - 1) / group;
+    const SharedRows r = shared_rows(s, c.shift, seq, token0, token1);
+    seq = r.all;
+    within = r.within;
     key0 = 0;
     keys = a.shared;
   } else {
@@ -107,14 +142,18 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
   const int from = (int)((long long)blocks * split / splits), to = (int)((long long)blocks * (split + 1) / splits);
 
   // least and greatest place of the workgroup's rows
-  const int tile_least = shared ? a.shared - 1 : rows.place0 + rows.first / group;
+  int tile_least = shared ? a.shared - 1 : rows.place0 + rows.first / group;
   const int tile_most = key0 + keys - 1;
   if (threadIdx.x < 2) strange[threadIdx.x] = 0;
   rows.first += 32 * wave;
   const bool live = rows.first < rows.total;
   const int mine = min(rows.first + (lane & 31), rows.total - 1) / group;
-  const int place = shared ? a.shared - 1 : rows.place0 + mine;
-  const int least = shared ? a.shared - 1 : rows.place0 + min(rows.first, rows.total - 1) / group;
+  int place = shared ? a.shared - 1 : rows.place0 + mine;
+  int least = shared ? a.shared - 1 : rows.place0 + min(rows.first, rows.total - 1) / group;
+  if (within) {
+    place = shared_place(s, c.shift, a.shared - 1, seq.row0 + mine, token0, token1, tile_least);
+    least = tile_least;
+  }
 
   Queries<D, 32> q;
   read_queries(q, a, rows, group, head);

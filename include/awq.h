@@ -473,8 +473,8 @@ int awq_append_kv(const void* x, int32_t ldx, const int32_t* offsets, const int3
  * scale      finite and > 0 (AWQ_ERR_OPTION).
  * shared     keys that all sequences begin with (a common prompt; 0: none), a multiple
  *            of page_size: read once for the whole batch through the table of the first
- *            sequence with rows, whatever the other tables hold there.  Every sequence with
- *            rows must have them.
+ *            sequence with rows, whatever the other tables hold there.  A sequence may end
+ *            or have new tokens among them: each sees those up to its own place.
  * y          out  fp16, row t at y + t * ldy; must not overlap an input.  A row without
  *                 keys gives 0.
  * Products, softmax statistics and sums are fp32; the weights are rounded for the matrix
