@@ -253,6 +253,11 @@ void launch_join(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, bool
 
 }  // namespace
 
+bool attend_fits(int T, int B, int q_heads, int kv_heads, int dim, int page_size, int width, int shared) {
+  const AttendPlan p = plan_of(T, B, q_heads, kv_heads, dim, page_size, width, shared, false);
+  const int64_t tiles = p.shared || !p.own_few ? tile_workgroups(tile_args(p, T, B, q_heads, kv_heads, dim), kv_heads) : 0;
+  return (tiles + (p.both() ? kUnits : 0)) * 256 < (int64_t)1 << 32;
+}
 size_t attend_workspace_bytes(int T, int B, int q_heads, int kv_heads, int dim, int page_size, int width, int shared) {
   return partial_bytes(plan_of(T, B, q_heads, kv_heads, dim, page_size, width, shared, false), (int64_t)T * q_heads, dim);
 }

@@ -55,6 +55,34 @@ hipError_t launch_attend_waves(const AttendArgs& a, const CacheArgs& c, const Se
 hipError_t launch_attend_tiles(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan,
                                const Partials& p, hipStream_t stream);
 
+// How a plan's row tiles (kTile rows each) are numbered: `shared_tiles` workgroup rows of the shared keys first, then the
+// sequences' own.
+constexpr int kTile = 128;
+struct TileArgs {
+  int group, shared_tiles, shared_splits, own_tiles, own_splits, own_slice, shared_slice;
+  int descending;  // of the own tiles (per key head), those that come first, from the last rows up
+};
+inline TileArgs tile_args(const AttendPlan& plan, int T, int B, int q_heads, int kv_heads, int dim) {
+  const int group = q_heads / kv_heads;
+  const int64_t rows = (int64_t)T * group, most = rows / kTile + B;  // (a ragged tile per sequence at most)
+  TileArgs x{group, 0, 1, 0, 1, plan.own_slices() > 0 ? 0 : -1, plan.own_slices(), 0};
+  if (plan.shared) {
+    x.shared_tiles = (int)((rows + kTile - 1) / kTile);
+    x.shared_splits = plan.shared_splits;
+  }
+  if (!plan.own_few) {
+    x.own_tiles = (int)(most < rows ? most : rows);
+    x.own_splits = plan.own_splits;
+    const int first = (kUnits + kv_heads - 1) / kv_heads;
+    const bool twice = x.shared_tiles == 0 && x.own_splits == 1 && x.own_tiles > first && x.own_tiles <= 2 * first;
+    x.descending = twice && dim < 256 ? first : x.own_tiles;
+  }
+  return x;
+}
+inline int64_t tile_workgroups(const TileArgs& x, int kv_heads) {
+  return ((int64_t)x.shared_tiles * x.shared_splits + (int64_t)x.own_tiles * x.own_splits) * kv_heads;
+}
+
 // The units of work of the waves (16 or 32 rows, a key head, 32 keys), in order: sequence after sequence; within one, rows,
 // then key heads, then keys.  Every row has at least one.  Wave w takes the units w * each .. w * each + each - 1.  (The
 // host makes sure that their number stays below kMostUnits.)

@@ -37,8 +37,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_both_kernel(Atte
 template <int D>
 void launch(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan, const Partials& p,
             hipStream_t stream) {
-  const TileArgs x = tile_args(a, c, s, plan);
-  const unsigned grid = tile_workgroups(x, c.heads);
+  const TileArgs x = tile_args(plan, s.T, s.B, a.q_heads, c.heads, c.dim);
+  const unsigned grid = (unsigned)tile_workgroups(x, c.heads);
   if (plan.both())
     hipLaunchKernelGGL((attend_both_kernel<D>), dim3(kUnits + grid), dim3(256), 0, stream, a, c, s, unit_args(a, c, plan), x,
                        p);

@@ -20,14 +20,6 @@
 
 namespace awq {
 
-constexpr int kTile = 128;  // rows of a workgroup
-
-// `shared_tiles` workgroup rows of the shared keys first, then the sequences' own.
-struct TileArgs {
-  int group, shared_tiles, shared_splits, own_tiles, own_splits, own_slice, shared_slice;
-  int descending;  // of the own tiles (per key head), those that come first, from the last rows up
-};
-
 template <int D>
 struct TileRing {
   static constexpr int BLOCKS = 4, BYTES = 2 * BLOCKS * 32 * Tile<D>::ROW;
@@ -260,28 +252,6 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
     });
   wait_loads<0>();  // (those past the end)
   if (live) write_rows(g, scale, a, p, rows, group, head, slice, nullptr, nullptr);
-}
-
-// How a plan's row tiles are numbered.
-inline TileArgs tile_args(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, const AttendPlan& plan) {
-  const int group = a.q_heads / c.heads;
-  const int64_t rows = (int64_t)s.T * group, most = rows / kTile + s.B;  // (a ragged tile per sequence at most)
-  TileArgs x{group, 0, 1, 0, 1, plan.own_slices() > 0 ? 0 : -1, plan.own_slices(), 0};
-  if (plan.shared) {
-    x.shared_tiles = (int)((rows + kTile - 1) / kTile);
-    x.shared_splits = plan.shared_splits;
-  }
-  if (!plan.own_few) {
-    x.own_tiles = (int)(most < rows ? most : rows);
-    x.own_splits = plan.own_splits;
-    const int first = (kUnits + c.heads - 1) / c.heads;
-    const bool twice = x.shared_tiles == 0 && x.own_splits == 1 && x.own_tiles > first && x.own_tiles <= 2 * first;
-    x.descending = twice && c.dim < 256 ? first : x.own_tiles;
-  }
-  return x;
-}
-inline unsigned tile_workgroups(const TileArgs& x, int heads) {
-  return (unsigned)((x.shared_tiles * x.shared_splits + x.own_tiles * x.own_splits) * heads);
 }
 
 }  // namespace awq

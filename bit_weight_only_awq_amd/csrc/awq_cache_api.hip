@@ -88,7 +88,9 @@ int awq_append_kv(const void* x, int32_t ldx, const int32_t* offsets, const int3
 
 size_t awq_attend_workspace_bytes(int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                   int32_t width, int32_t page_size, int32_t shared) {
-  if (!counts_ok(T, B, q_heads, kv_heads, width, page_size) || !dim_known(head_dim) || shared < 0) return 0;
+  if (!counts_ok(T, B, q_heads, kv_heads, width, page_size) || !dim_known(head_dim) || shared < 0 ||
+      !awq::attend_fits(T, B, q_heads, kv_heads, head_dim, page_size, width, shared))
+    return 0;
   return awq::attend_workspace_bytes(T, B, q_heads, kv_heads, head_dim, page_size, width, shared);
 }
 
@@ -102,6 +104,7 @@ int awq_attend(const void* q, int32_t ldq, const int32_t* offsets, const int32_t
   if (!stride_ok(ldq, row) || !stride_ok(ldy, row)) return AWQ_ERR_SHAPE;
   if (!(scale > 0.0f) || isinf(scale)) return AWQ_ERR_OPTION;
   if (shared < 0 || shared % page_size != 0 || shared / page_size > width) return AWQ_ERR_OPTION;
+  if (!awq::attend_fits(T, B, q_heads, kv_heads, head_dim, page_size, width, shared)) return AWQ_ERR_SHAPE;
   st = check_pointers(q, k_pages, v_pages, y);
   if (st != AWQ_OK) return st;
   st = check_workspace(workspace, workspace_bytes,

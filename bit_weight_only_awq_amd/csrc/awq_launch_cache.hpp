@@ -50,6 +50,8 @@ struct AttendArgs {
   _Float16* y;
   int64_t ldy;
 };
+// Whether the launch has less than 2^32 threads (with shared keys beside a row tile for nearly each of 2^24 rows it has not).
+bool attend_fits(int T, int B, int q_heads, int kv_heads, int dim, int page_size, int width, int shared);
 size_t attend_workspace_bytes(int T, int B, int q_heads, int kv_heads, int dim, int page_size, int width, int shared);
 size_t attend_list_workspace_bytes(int T, int q_heads, int kv_heads, int dim, int page_size, int count);
 hipError_t launch_attend(const AttendArgs& a, const CacheArgs& c, const SeqArgs& s, void* workspace, hipStream_t stream);

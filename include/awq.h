@@ -475,6 +475,8 @@ int awq_append_kv(const void* x, int32_t ldx, const int32_t* offsets, const int3
  *            of page_size: read once for the whole batch through the table of the first
  *            sequence with rows, whatever the other tables hold there.  A sequence may end
  *            or have new tokens among them: each sees those up to its own place.
+ *            (AWQ_ERR_SHAPE where the row tiles of both kinds of keys are 2^24 or more,
+ *            which takes nearly 2^24 rows, about as many sequences as tokens, and wide tables.)
  * y          out  fp16, row t at y + t * ldy; must not overlap an input.  A row without
  *                 keys gives 0.
  * Products, softmax statistics and sums are fp32; the weights are rounded for the matrix
