@@ -822,6 +822,13 @@ def _beside(t: Optional[torch.Tensor], shape, dtype, device: int, what: str) -> 
     return t.data_ptr()
 
 
+def _int32(value: int, where: str) -> int:
+    """A number for the library as it is: the call would pass on its lowest 32 bits."""
+    if not -1 << 31 <= value < 1 << 31:
+        raise AwqError(AWQ_ERR_OPTION, where)
+    return value
+
+
 def _cache_call(x: torch.Tensor, cache: KvCache, seqs: Sequences, extra: int, what: str):
     """(device, row address, row stride, the batch's arguments, those of the pages) of rows ``x`` that hold ``extra``
     vectors per key head beside the queries' (keys and values); everything on the rows' device, which is the current
@@ -938,6 +945,7 @@ def attend(q: torch.Tensor, cache: KvCache, seqs: Sequences, scale: Optional[flo
     tokens all sequences begin with (a multiple of the page size); their pages, those of the table of the first
     sequence that has rows, are read and multiplied once for the whole batch (a new token among them sees those
     up to its own place).  A row without keys gives 0; rows of no sequence are left as they are."""
+    _int32(shared, "awq_attend")
     return _attend_rows("awq_attend", q, cache, seqs, scale, y, workspace, (shared,),
                         lambda b, size: (b[4], b[5], b[6], b[7], b[8], b[3], size, shared))
 
@@ -948,12 +956,14 @@ def select_pages(q: torch.Tensor, cache: KvCache, seqs: Sequences, count: int, f
     -1 past the last: all of them up to the token's place if they are at most ``count``, or else the ``first`` first,
     the ``recent`` last, and those between whose bounds allow the largest products with the queries."""
     lib = _lib or load_library()
+    for n in (count, first, recent):
+        _int32(n, "awq_select_pages")
     device, qp, ldq, batch, (_, _, pages, page_size) = _cache_call(q, cache, seqs, 0, "q")
     _workspace_beside(workspace, device)
     if cache.bounds is None:
         raise ValueError("select_pages needs a cache with bounds")
     bp = _page_bounds(cache, device)
-    if not 1 <= count < 1 << 31:
+    if count < 1:
         raise AwqError(AWQ_ERR_OPTION, "awq_select_pages")
     T, kv_heads = q.shape[0], batch[7]
     out = q.new_empty((T, kv_heads, count), dtype=_I32)
