@@ -829,15 +829,21 @@ def _int32(value: int, where: str) -> int:
     return value
 
 
+def _cache_shape(cache: KvCache):
+    """(pages, key heads, page size, head size) of a cache that has any."""
+    shape = cache.k.shape
+    if len(shape) != 4 or 0 in shape or cache.v.shape != shape:
+        raise ValueError("the cache's keys and values must be float16 tensors [pages, kv_heads, page_size, head_dim]")
+    return shape
+
+
 def _cache_call(x: torch.Tensor, cache: KvCache, seqs: Sequences, extra: int, what: str):
     """(device, row address, row stride, the batch's arguments, those of the pages) of rows ``x`` that hold ``extra``
     vectors per key head beside the queries' (keys and values); everything on the rows' device, which is the current
     one for the call."""
     k, v, bounds = cache
     offsets, lengths, tables = seqs
-    pages, kv_heads, page_size, dim = shape = k.shape
-    if v.shape != shape:
-        raise ValueError("the cache's keys and values must be float16 tensors [pages, kv_heads, page_size, head_dim]")
+    pages, kv_heads, page_size, dim = shape = _cache_shape(cache)
     if x.dim() != 2 or x.shape[1] % dim:
         raise ValueError(f"{what} must be a float16 tensor [T, heads * {dim}]")
     T, width = x.shape
@@ -845,9 +851,9 @@ def _cache_call(x: torch.Tensor, cache: KvCache, seqs: Sequences, extra: int, wh
     if heads < 1 or heads % kv_heads:
         raise ValueError(f"{what} must hold a multiple of {kv_heads} query heads")
     xp, ldx = _rows2d(x, None, width, what)
+    if lengths.dim() != 1 or tables.dim() != 2:
+        raise ValueError("seqs.lengths must be an int32 tensor [B], seqs.tables one [B, width]")
     B, device = lengths.shape[0], x.get_device()
-    if tables.dim() != 2:
-        raise ValueError("seqs.tables must be an int32 tensor [B, width]")
     columns = tables.shape[1]
     batch = (_beside(offsets, (B + 1,), _I32, device, "seqs.offsets"),
              _beside(lengths, (B,), _I32, device, "seqs.lengths"),
@@ -981,7 +987,7 @@ def attend_pages(q: torch.Tensor, cache: KvCache, seqs: Sequences, pages: torch.
                  y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """``attend`` over chosen pages only (``select_pages``' int32 [T, kv_heads, count], or any such choice of a
     sequence's pages: each at most once, negative ones last), up to each token's place."""
-    if pages.dim() != 3 or pages.shape[:2] != (q.shape[0], cache.k.shape[1]):
+    if q.dim() != 2 or pages.dim() != 3 or pages.shape[:2] != (q.shape[0], _cache_shape(cache)[1]):
         raise ValueError("pages must be an int32 tensor [T, kv_heads, count]")
     count = pages.shape[2]
     return _attend_rows("awq_attend_pages", q, cache, seqs, scale, y, workspace,
