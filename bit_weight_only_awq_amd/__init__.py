@@ -995,6 +995,42 @@ def attend_pages(q: torch.Tensor, cache: KvCache, seqs: Sequences, pages: torch.
                         lambda b, size: (b[4], b[6], b[7], b[8], size, count))
 
 
+def _check_attention(x, qkv, o, cache, seqs, residual, scale, shared, pages, first, recent) -> None:
+    """What the calls of `attention` behind `append_kv` would refuse, before that writes to the cache."""
+    if pages and shared:
+        raise ValueError("chosen pages are of each sequence's own table: with pages, shared must be 0")
+    _, kv_heads, page_size, dim = _cache_shape(cache)
+    if x.dim() != 2 or seqs.tables.dim() != 2 or seqs.lengths.dim() != 1:
+        raise ValueError("x must be a float16 tensor [T, K], seqs.lengths an int32 tensor [B], seqs.tables one [B, width]")
+    T, width, heads = x.shape[0], seqs.tables.shape[1], qkv.N // dim - 2 * kv_heads
+    if heads < 1 or heads % kv_heads or qkv.N % dim or o.K != heads * dim:
+        raise ValueError(f"qkv must give a multiple of {kv_heads} query heads and {2 * kv_heads} others of {dim} channels "
+                         f"each, and o take the query heads' channels; they are of {qkv.N} and {o.K}")
+    if residual is not None:
+        rp, ldr = _rows2d(residual, T, o.N, "residual")
+        if ldr % 8 or rp % 16:
+            raise AwqError(AWQ_ERR_SHAPE if ldr % 8 else AWQ_ERR_ALIGN, "awq_linear_fused")
+    if scale is not None and not 0.0 < ctypes.c_float(scale).value < float("inf"):
+        raise AwqError(AWQ_ERR_OPTION, "awq_attend")
+    if pages:
+        if cache.bounds is None:
+            raise ValueError("attention to chosen pages needs a cache with bounds")
+        _page_bounds(cache, x.get_device())
+        rows, places = T * kv_heads, pages * page_size
+        if rows >= 1 << 22:
+            raise AwqError(AWQ_ERR_SHAPE, "awq_select_pages")
+        if pages < 1 or first < 0 or recent < 1 or first + recent > pages or rows * pages >= 1 << 31:
+            raise AwqError(AWQ_ERR_OPTION, "awq_select_pages")
+        if places > 1 << 30 or rows * -(-(heads // kv_heads) // 16) * (places // 32 + 1) >= 1 << 30:
+            raise AwqError(AWQ_ERR_OPTION, "awq_attend_pages")
+    elif shared:
+        if shared < 0 or shared % page_size or shared // page_size > width:
+            raise AwqError(AWQ_ERR_OPTION, "awq_attend")
+        # (no workspace: not a shape that is taken, where shared keys always have parts to join)
+        if T > 0 and not _bytes_of("awq_attend", T, seqs.lengths.shape[0], heads, kv_heads, dim, width, page_size, shared):
+            raise AwqError(AWQ_ERR_SHAPE, "awq_attend")
+
+
 def attention(x: torch.Tensor, qkv: PackedWeight, o: PackedWeight, cache: KvCache, seqs: Sequences,
               inv_freq: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
               residual: Optional[torch.Tensor] = None, scale: Optional[float] = None, shared: int = 0,
@@ -1003,9 +1039,8 @@ def attention(x: torch.Tensor, qkv: PackedWeight, o: PackedWeight, cache: KvCach
     """A decoder block's attention for new tokens ``x`` [T, K]: the fused q/k/v layer (``pack_fused([q, k, v])``,
     ``bias`` its own), the tokens' keys and values appended, attention over the cache, the output layer, plus
     ``residual``.  With ``pages`` above 0 each token attends to that many pages only (``select_pages``); these come from
-    the token's own table, so ``shared`` must be 0."""
-    if pages and shared:
-        raise ValueError("chosen pages are of each sequence's own table: with pages, shared must be 0")
+    the token's own table, so ``shared`` must be 0.  Nothing is written if a call is refused."""
+    _check_attention(x, qkv, o, cache, seqs, residual, scale, shared, pages, first, recent)
     rows = linear_fused(x, qkv, bias=bias)
     q = append_kv(rows, cache, seqs, inv_freq, positions, axes, interleaved)
     if pages:

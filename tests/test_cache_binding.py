@@ -20,6 +20,72 @@ def sequences(B=2, width=4):
     return awq.Sequences(whole(B + 1), whole(B), whole(B, width))
 
 
+@pytest.fixture
+def calls(monkeypatch):
+    """The calls of `attention` that write, by name; layers give zeros."""
+    made = []
+
+    def layer(x, pw, bias=None, **kw):
+        made.append("layer")
+        return half(x.shape[0], pw.N)
+
+    monkeypatch.setattr(awq, "linear_fused", layer)
+    monkeypatch.setattr(awq, "append_kv", lambda qkv, cache, *a, **kw: made.append("append") or half(qkv.shape[0], 1024))
+    for name in ("attend", "attend_pages", "select_pages"):
+        monkeypatch.setattr(awq, name, lambda q, *a, **kw: made.append("attend") or q)
+    return made
+
+
+def weight(N, K):
+    return awq.PackedWeight(None, None, None, N, K, 128, True)
+
+
+QKV, O = weight(1536, 512), weight(512, 1024)
+
+
+def block(**kw):
+    a = dict(x=half(3, 512), qkv=QKV, o=O, cache=cache(), seqs=sequences())
+    a.update(kw)
+    return awq.attention(**a)
+
+
+def test_attention_runs_its_calls(calls):
+    for kw in ({}, dict(shared=32), dict(pages=3), dict(pages=4, first=0, recent=4),
+               dict(scale=0.5), dict(cache=cache(bounds=False)), dict(shared=64)):
+        calls.clear()
+        block(**kw)
+        assert calls[:2] == ["layer", "append"] and calls[-1] == "layer", kw
+
+
+@pytest.mark.parametrize("kw", [
+    dict(pages=4, cache=cache(bounds=False)),                                        # nothing to choose from
+    dict(pages=4, cache=cache()._replace(bounds=half(10, 2, 2, 64))),                # bounds of another cache
+    dict(pages=1), dict(pages=2, first=2), dict(pages=4, recent=0), dict(pages=4, first=-1), dict(pages=-3),
+    dict(pages=1 << 32), dict(pages=4, first=1 << 32), dict(pages=4, recent=1 << 32),
+    dict(pages=1 << 28), dict(pages=(1 << 30) // 16 + 1),                            # keys past 2^30
+    dict(shared=8), dict(shared=-16), dict(shared=80), dict(shared=1 << 32), dict(shared=16, pages=4),
+    dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e-50),
+    dict(scale=1e39), dict(pages=4, scale=0.0),
+    dict(residual=half(2, 512)), dict(residual=half(3, 520)), dict(residual=torch.zeros((3, 512))),
+    dict(residual=half(3, 1024)[:, ::2]),
+    dict(o=weight(512, 768)), dict(qkv=weight(1024, 512)), dict(qkv=weight(512, 512)), dict(qkv=weight(1500, 512)),
+])
+def test_attention_refuses_before_it_writes(calls, kw):
+    with pytest.raises((ValueError, awq.AwqError)):
+        block(**kw)
+    assert "append" not in calls
+
+
+def test_many_rows_are_refused_before_they_are_written(calls):
+    for kw, T, N, K in ((dict(pages=4, cache=cache(dim=64)), 1 << 21, 6 * 64, 128),       # 2^22 choices
+                        (dict(pages=2048, cache=cache(dim=64)), 1 << 19, 6 * 64, 128),    # 2^31 chosen pages
+                        (dict(pages=1024, cache=cache(dim=64, size=64)), 1 << 18, 6 * 64, 128),  # 2^30 units of work
+                        (dict(shared=16, cache=cache(heads=256, dim=64), seqs=sequences(65536, 128)), 65535, 768 * 64, 16384)):
+        with pytest.raises(awq.AwqError):
+            block(x=half(1, 8).expand(T, 8), qkv=weight(N, 8), o=weight(8, K), **kw)
+        assert "layer" not in calls
+
+
 @pytest.mark.parametrize("call", [
     lambda n: awq.attend(half(4, 1024), cache(), sequences(), shared=n),
     lambda n: awq.select_pages(half(4, 1024), cache(), sequences(), n),
@@ -38,7 +104,8 @@ def test_numbers_past_32_bits_are_refused(call, n):
 def test_caches_of_no_size_are_value_errors(bad):
     for call in (lambda: awq.attend(half(4, 1024), bad, sequences()), lambda: awq.append_kv(half(4, 1536), bad, sequences()),
                  lambda: awq.select_pages(half(4, 1024), bad, sequences(), 4),
-                 lambda: awq.attend_pages(half(4, 1024), bad, sequences(), whole(4, 2, 3))):
+                 lambda: awq.attend_pages(half(4, 1024), bad, sequences(), whole(4, 2, 3)),
+                 lambda: awq.attention(half(3, 512), QKV, O, bad, sequences())):
         with pytest.raises(ValueError):
             call()
 
