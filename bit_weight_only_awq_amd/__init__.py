@@ -889,7 +889,9 @@ def append_kv(qkv: torch.Tensor, cache: KvCache, seqs: Sequences, inv_freq: Opti
     [T, q_heads * head_dim].  ``inv_freq`` (fp32 [R / 2]): pair i of the first R channels turns by position *
     inv_freq[i]; None: no rotation.  ``positions`` int32 [T] or [T, axes]: None takes each token's place in its
     sequence.  With several axes ``axes`` (int32 [R / 2]) says which one pair i turns by.  Pairs are channels
-    (i, R / 2 + i), or (2 i, 2 i + 1) with ``interleaved``.  ``q`` may be the queries' columns of ``qkv``."""
+    (i, R / 2 + i), or (2 i, 2 i + 1) with ``interleaved``.  ``q`` may be the queries' columns of ``qkv``; its rows of
+    tokens without a place (behind the last sequence) are left as they are, uninitialised in a new one.  A page's bounds
+    only grow until its first slot is written again."""
     lib = _lib or load_library()
     device, xp, ldx, batch, (kp, vp, pages, page_size) = _cache_call(qkv, cache, seqs, 2, "qkv")
     bp = _page_bounds(cache, device)
@@ -1039,7 +1041,8 @@ def attention(x: torch.Tensor, qkv: PackedWeight, o: PackedWeight, cache: KvCach
     """A decoder block's attention for new tokens ``x`` [T, K]: the fused q/k/v layer (``pack_fused([q, k, v])``,
     ``bias`` its own), the tokens' keys and values appended, attention over the cache, the output layer, plus
     ``residual``.  With ``pages`` above 0 each token attends to that many pages only (``select_pages``); these come from
-    the token's own table, so ``shared`` must be 0.  Nothing is written if a call is refused."""
+    the token's own table, so ``shared`` must be 0.  Nothing is written if a call is refused.  Rows of no sequence come
+    back as anything."""
     _check_attention(x, qkv, o, cache, seqs, residual, scale, shared, pages, first, recent)
     rows = linear_fused(x, qkv, bias=bias)
     q = append_kv(rows, cache, seqs, inv_freq, positions, axes, interleaved)

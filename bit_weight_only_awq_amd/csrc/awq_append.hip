@@ -57,7 +57,8 @@ __device__ __forceinline__ Unit unit_of(int u, int rotary, int dim) {
   return 2 * lo < rotary ? Unit{lo, rotary / 2 + lo} : Unit{rotary / 2 + lo, dim / 2 + lo};
 }
 // Where a token's pair p is among its turns: quarters of units side by side (a
-// thread reads its four with its neighbours', without bank conflicts).
+// thread reads its four with its neighbours'; four conflict cycles per access are
+// counted, writing the turns among them).
 __device__ __forceinline__ int place_of(int p, int rotary, bool interleaved) {
   const int units = rotary / 16, far = interleaved && p >= rotary / 4, q = p - (far ? rotary / 4 : 0);
   const int u = interleaved ? q / 4 : q / 8, quarter = interleaved ? 2 * far + q % 4 / 2 : q % 8 / 2;

@@ -197,7 +197,8 @@ __global__ __launch_bounds__(256) void join_slices_kernel(AttendArgs a, SeqArgs 
 
 // The keys' splits over which `tiles` workgroups take the least time, in rounds of two per compute unit (one where
 // a head is 256 wide), a stage being the unit, what a workgroup does besides costing three of them, and writing and
-// reading the parts of a tile 0.0085 (128 rows of fp32 sums, there and back).
+// reading the parts of a tile 0.0085 (128 rows of fp32 sums, there and back).  (Both costs are those of heads of 128
+// channels, taken for the others too.)
 int splits_of(int64_t tiles, int64_t stages, int slots) {
   int best = 1;
   double least = 1e300;
@@ -214,12 +215,20 @@ int splits_of(int64_t tiles, int64_t stages, int slots) {
 
 // Which kernels, measured on both sides (us; sequences x new tokens x query heads of a key head):
 // Up to 32 rows per sequence on average (a row: a token and a query head of one key head) the waves, which share ragged
-// batches out evenly; past that they would read the keys twice.  8 x 4 x 8, 4000 before: waves 34.9, row tiles 38.5;
-// 48 x 1 x 8, 7 to 4000 before: 96, 111; 8 x 5 x 8: 45, 33.3.  (Many key heads with several tokens each, 30 x 16 x 1 of 32
-// heads: 102, 85: the join's rows.)
+// batches out evenly; past that they would read the keys twice.  Waves, row tiles, with as many tokens before each
+// sequence / with 7 to twice as many:
+//   8 x 1 x 8, 4000     35.2, 38.0 / 41.3, 48.2     16 x 1 x 4, 3000   45.1, 48.4 / 52.9, 62.3
+//   8 x 4 x 8           39.7, 42.2 / 46.7, 52.2     16 x 8 x 4         52.2, 53.5 / 61.0, 66.5
+//   8 x 8 x 8 (tiles)   57.4, 44.6 / 65.1, 52.1     16 x 16 x 4 (tiles)  75.1, 52.6 / 92.8, 70.4
+//   20 x 8 x 3, 2000    45.5, 46.2 / 50.6, 56.8     20 x 16 x 3 (tiles)  69.4, 46.5 / 78.8, 60.0
+//   30 x 1 x 1, 1000    96.4, 95.6 / 119, 120       30 x 8 x 1         105, 97 / 134, 125
+//   30 x 4 x 1          99.5, 96.1 / 123, 123       30 x 32 x 1        135, 105 / 169, 135
+// So for a single query head per key head (the last two lines) the rule is off: from about four tokens on the join of
+// their many rows costs more than the waves save, up to 29 %.
 // Up to 16 rows the waves' products are of 16: 8 x 2 x 8 32.0, of 32 32.4; 8 x 4 x 8 43.1, 33.9.
 // Shared keys always by row tiles: 1 x 1 x 8 after 8192 19.0, by waves 30.9; 16 x 1 x 8 26.1, 61.4; and in one launch with
-// the waves, whose products are of 16 rows there: 16 x 1 x 8 25.9, in two 38.2; 61 x 1 x 8 47, 68; 1 x 6 x 3 after 1600 18, 23.
+// the waves, whose products are of 16 rows there: 16 x 1 x 8 25.9, in two 38.2; 61 x 1 x 8 47, 68; 1 x 6 x 3 after 1600 18, 23;
+// 61 x 1 x 8 with heads of 64: 30, 47, of 96: 36, 56, of 256, where row tiles begin as the waves end: 99, 104.
 AttendPlan plan_of(int T, int B, int q_heads, int kv_heads, int dim, int page_size, int width, int shared, bool list) {
   const int group = q_heads / kv_heads, stage = dim == 256 ? 32 : 64, slots = dim == 256 ? kUnits : 2 * kUnits;
   const int64_t rows = (int64_t)T * group;

@@ -9,7 +9,9 @@ namespace awq {
 constexpr int kUnits = 256;  // compute units
 // Waves on their own of a unit, each with a ring of two blocks.  (With five a unit's LDS is full, and HBM serves their
 // many streams less well: 1 token of 8191 40.5 us, with two 32.4; 48 tokens 103, 96, with four 93.4; 32 tokens on chosen
-// pages 102, 92; 1 token of 30000 46, 36.  Rings of three or four blocks: the same or slower.)
+// pages 102, 92; 1 token of 30000 46, 36.  Rings of three or four blocks: the same or slower.  With one, two, four at
+// the other head sizes, 1 token of 8191 / 48 tokens: of 64 25.9, 18.4, 18.8 / 86, 56, 53; of 96 29.9, 24.3, 25.5 / 99, 76, 73; of
+// 256, where a unit has room for two, 32.9, 35.1, 43.0 / 184, 174, 178.)
 constexpr int kWavesOfUnit = 2, kWaves = kUnits * kWavesOfUnit;
 constexpr int kLeastUnits = 2;  // key blocks that a wave takes at least
 

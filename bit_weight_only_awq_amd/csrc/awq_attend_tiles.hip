@@ -1,8 +1,10 @@
 // Attention of many rows (awq_attend_tiles.hpp), and of many rows of shared keys
 // together with few rows per sequence (awq_attend_waves.hpp): the first is bound by
 // the matrix cores, the second by HBM, and in one launch each compute unit holds a
-// workgroup of either kind (61 tokens of 64 query heads after 8192: 34 us; one launch
-// after the other, with their joins, 68 us for 47).
+// workgroup of either kind (61 tokens of 64 query heads after 8192: 34-36 us; one launch
+// after the other, with their joins, 68 us for 46).  With heads of 256 channels a
+// workgroup's ring is 128 KB, so a unit holds one at a time: the row tiles
+// begin as waves end, still without the second launch (99 us, 104).
 #include "awq_attend_tiles.hpp"
 #include "awq_attend_waves.hpp"
 

@@ -9,8 +9,8 @@
 // others are joined by a second launch.
 //
 // Bound: HBM, each key and value once (1 token of 8191, 134 MB: 24.5 us, 5.5 TB/s; 48
-// tokens of up to 4000, 451 MB: 90 us, 5.0; 32 tokens on 64 chosen pages, 268 MB: 51
-// us, 5.3).  Keys and values go straight to LDS
+// tokens of up to 4000, 451 MB: 90 us, 5.0; 32 tokens on 64 chosen pages, 268 MB: 53
+// us, 5.1).  Keys and values go straight to LDS
 // (16 bytes per lane, whole rows), one block of 32 keys ahead of the products; a
 // workgroup is one wave, so nothing waits for a barrier.
 #pragma once

@@ -8,14 +8,14 @@
 // the channels of max(q lo, q hi), q hi where q > 0 and q lo where q < 0; a page's
 // score is the sum of that over the key head's query heads.  Split by the sign of q it is Q+ . hi + Q- . lo, Q+ and Q-
 // the sums of the heads' positive and negative parts: two multiply-adds per
-// channel whatever the number of heads, in 64 bits, where the products of two
-// halves are exact.  So a choice depends on the numbers, not on the order of the
-// additions, and equal pages get equal scores (the lower page goes first).  A
-// score that is not a number counts as the lowest.
+// channel whatever the number of heads, in 64 bits, where a sum is rounded only if it
+// takes more than 53 of them.  Every page's sums are made in the same order, so equal
+// pages get equal scores (the lower page goes first).  A score that is not a number
+// counts as the lowest.
 //
 // Bound: HBM, each page's bounds once, in the first kernel (32 tokens of up to 1024
 // pages, 95 MB: 26 us, 3.7 TB/s, 10 of them fp64 instructions; 1 token of 6251
-// pages, 26 MB: 9.0); the second finds the wanted number of largest scores by their
+// pages, 26 MB: 9.6); the second finds the wanted number of largest scores by their
 // bits, 8 at a time from the highest in which they differ, one workgroup per token and
 // key head: a chain of reads and rounds (8.5 us in both cases).  Narrow tables take
 // both steps in one launch.

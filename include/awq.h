@@ -453,10 +453,13 @@ size_t awq_combine_experts_workspace_bytes(int32_t T, int32_t top_k, int32_t E, 
  * axis       in   int32 [rotary / 2] (device): the axis whose position pair i turns by
  *                 (time, height, width); may be NULL with one axis.  1 <= axes <= 16.
  * q          out  fp16, row t at q + t * ldq: the rotated queries.  May be the queries in
- *                 x (same address and stride).
+ *                 x (same address and stride).  Rows of tokens without a place (of no sequence,
+ *                 or a negative one) are left as they are.
  * k_pages, v_pages  the new tokens' slots are written, nothing else.
  * bounds     NULL, or kept up to date: a page whose first slot is written starts anew,
  *            any other page's grow to hold the new keys (as stored; NaN is passed over).
+ *            They only grow: a slot that is written again (tokens taken back) leaves its old
+ *            key within them until the page's first slot is written.
  * A page that two sequences' new tokens fall into is a race.  Deterministic.
  */
 int awq_append_kv(const void* x, int32_t ldx, const int32_t* offsets, const int32_t* lengths, const int32_t* tables,
