@@ -19,8 +19,8 @@
 // to 2^15 with the lag, of fp16's 2^16): relative 2^-11 down to 2^-21 of the maximum, below that 2^-32 of it at most, so
 // that 2^17 keys of 2^-26 of a great one still count.  l is the sum of the rounded weights: the result is an average of
 // the values, and no channel passes the greatest of them.  (With l of the weights before rounding, 2000 values of 65504 gave
-// infinity; a product of two halves by 1 and 1 adds them to l now: 13 questions 526 -> 530 us, prompt of 2000: 50.7 -> 51.8,
-// single tokens the same.)
+// infinity; products of two halves by 1 and 1 add eight of them up now: 13 questions 520 -> 527 us, prompt of 2000: 50.7 ->
+// 51.0, single tokens the same.)
 #pragma once
 
 #include <type_traits>
@@ -454,17 +454,15 @@ __device__ __forceinline__ float settle(float m, float c, Gathered<D, R>& g) {
 template <int R>
 struct Weights {
   half8_t part[R / 16];
+  float eights[R / 16];  // sums of eight, as rounded (added to l one after the other, they move the scores' registers: two
+                         // sets of the three that a loop of row tiles takes in turn then share a pair)
   // of scores 2 i and 2 i + 1
   __device__ __forceinline__ void take(int i, const Scores<R>& s, float c, float base) {
-    const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s.get(2 * i), c, -base));
-    const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s.get(2 * i + 1), c, -base));
-    part[i >> 2][2 * (i & 3)] = (_Float16)w0;
-    part[i >> 2][2 * (i & 3) + 1] = (_Float16)w1;
-  }
-  // and their sum, added to `sum`
-  __device__ __forceinline__ float add(int i, float sum) const {
-    const half2_t two{part[i >> 2][2 * (i & 3)], part[i >> 2][2 * (i & 3) + 1]};
-    return __builtin_amdgcn_fdot2(two, half2_t((_Float16)1.0f), sum, false);
+    const half2_t two{(_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(s.get(2 * i), c, -base)),
+                      (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(s.get(2 * i + 1), c, -base))};
+    eights[i / 4] = __builtin_amdgcn_fdot2(two, half2_t((_Float16)1.0f), i % 4 ? eights[i / 4] : 0.0f, false);
+    part[i >> 2][2 * (i & 3)] = two[0];
+    part[i >> 2][2 * (i & 3) + 1] = two[1];
   }
 };
 
@@ -503,7 +501,7 @@ __device__ __forceinline__ Weights<R> attend_block(const Addresses<D, R>& at, co
 #pragma unroll
   for (int i = 0; i < Scores<R>::COUNT / 2; ++i) p.take(i, s, c, base);
 #pragma unroll
-  for (int i = 0; i < Scores<R>::COUNT / 2; ++i) g.sum = p.add(i, g.sum);
+  for (int i = 0; i < Scores<R>::COUNT / 8; ++i) g.sum += p.eights[i];
   gather<D, R, V>(at, v, p, g, [](auto) __attribute__((always_inline)) {});
   return p;
 }
@@ -533,7 +531,7 @@ __device__ __forceinline__ Weights<R> attend_next(const Addresses<D, R>& at, con
 #pragma unroll
     for (int n = PAIRS * i / M; n < PAIRS * (i + 1) / M; ++n) {
       most = larger(larger(most, next.get(2 * n)), next.get(2 * n + 1));
-      g.sum = p.add(n, g.sum);
+      if (n % 4 == 3) g.sum += p.eights[n / 4];
     }
     if constexpr (i % 2 == 0) beside(std::integral_constant<int, i / 2>{});
   });
