@@ -9,8 +9,8 @@
 // Bound: the matrix cores (4 D operations per row and key) beside the
 // exponentials: 13 questions after 16384 shared tokens 496-542 us back to back with their
 // join, 0.92-1.0 PFLOP/s by the part, with two workgroups per unit at the power limit
-// (549-596 without it in a trace, at lower clocks); a wave that has its SIMD to
-// itself takes 0.8 us per block (a prompt of 2000, whose last tiles see 64 of them: 55
+// (549-588 without it in a trace, at lower clocks); a wave that has its SIMD to
+// itself takes 0.8 us per block (a prompt of 2000, whose last tiles see 64 of them: 54
 // us).  A block of keys and values goes straight to LDS while the one before it is
 // multiplied, with one barrier per block.  Where the row tiles are
 // too few for the chip, the keys are split as well and the parts joined by a second

@@ -15,7 +15,7 @@
 //
 // Bound: HBM, each page's bounds once, in the first kernel (32 tokens of up to 1024
 // pages, 95 MB: 26 us, 3.7 TB/s, 10 of them fp64 instructions; 1 token of 6251
-// pages, 26 MB: 9.6); the second finds the wanted number of largest scores by their
+// pages, 26 MB: 9.6-10.8); the second finds the wanted number of largest scores by their
 // bits, 8 at a time from the highest in which they differ, one workgroup per token and
 // key head: a chain of reads and rounds (8.5 us in both cases).  Narrow tables take
 // both steps in one launch.
