@@ -5,8 +5,8 @@
 // workgroups of 128 rows (awq_attend_tiles.hip), and shared keys to these, with the
 // rows of all sequences together.
 //
-// Joining: with m the greatest of the parts' maxima, y = sum_i 2^(m_i - m) o_i / sum_i
-// 2^(m_i - m) l_i over the parts, in a fixed order, in fp32.  Bound: a launch and the
+// Joining: with m the greatest of the parts' maxima, y = sum_i 2^((m_i - m) c) o_i / sum_i
+// 2^((m_i - m) c) l_i over the parts, in a fixed order, in fp32.  Bound: a launch and the
 // chain offsets -> which parts -> parts (4.6-6.7 us); 16 to 30 MB of parts of many rows
 // 14 us.
 #include "awq_attend.hpp"
@@ -72,6 +72,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
   const int parts = placed ? pieces + max(j.slices - slice0, 0) : 0;
 
   float4_t sums = float4_t(0.0f);
+  const float c2 = a.scale * kLog2E;
   float top = -INFINITY, total = 0.0f;
   const int channel = 4 * (lane & (LANES - 1));
   const bool live = channel < D;
@@ -108,11 +109,11 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, CacheArgs c, Se
     for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
     m = fmaxf(m, top);
     // (a part that saw no key counts nothing, also where none did)
-    const float share = stat.x == -INFINITY && stat.y == 0.0f ? 0.0f : stat.x == m ? 1.0f : __builtin_amdgcn_exp2f(stat.x - m);
+    const float share = stat.x == -INFINITY && stat.y == 0.0f ? 0.0f : stat.x == m ? 1.0f : __builtin_amdgcn_exp2f((stat.x - m) * c2);
     float sum = share * stat.y;
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
-    const float carry = top == m ? 1.0f : __builtin_amdgcn_exp2f(top - m);
+    const float carry = top == m ? 1.0f : __builtin_amdgcn_exp2f((top - m) * c2);
     total = total * carry + sum;
     if (i0 > 0) sums *= carry;
     top = m;
@@ -150,6 +151,7 @@ __global__ __launch_bounds__(256) void join_slices_kernel(AttendArgs a, SeqArgs 
   const int t = row / a.q_heads, at = row - t * a.q_heads;
   if (t < s.offsets[0] || t >= min(s.offsets[s.B], s.T) || channel >= D) return;
   float4_t sums = float4_t(0.0f);
+  const float c2 = a.scale * kLog2E;
   float top = -INFINITY, total = 0.0f;
   bool placed = true;
   float2 next_stat[AHEAD];
@@ -175,14 +177,14 @@ __global__ __launch_bounds__(256) void join_slices_kernel(AttendArgs a, SeqArgs 
       placed = placed && stat[i].y != kNoPlace;
       m = fmaxf(m, stat[i].x);
     }
-    const float carry = top == m ? 1.0f : __builtin_amdgcn_exp2f(top - m);
+    const float carry = top == m ? 1.0f : __builtin_amdgcn_exp2f((top - m) * c2);
     total *= carry;
     sums *= carry;
     top = m;
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       if (i0 + i >= slices || (stat[i].x == -INFINITY && stat[i].y == 0.0f)) continue;
-      const float share = stat[i].x == m ? 1.0f : __builtin_amdgcn_exp2f(stat[i].x - m);
+      const float share = stat[i].x == m ? 1.0f : __builtin_amdgcn_exp2f((stat[i].x - m) * c2);
       total += stat[i].y * share;
       sums += part[i] * share;
     }

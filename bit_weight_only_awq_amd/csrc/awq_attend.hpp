@@ -26,9 +26,9 @@ struct AttendPlan {
   int slices() const { return own_slices() + (shared ? shared_splits : 0); }
 };
 
-// Partial results: for each row's query head (numbered t * q_heads + head) and slice the maximum (in powers of two),
-// the sum and the values' sums: slice 0 (to own_splits - 1) the own keys, the rest the shared ones; and two of
-// those of 32 rows per wave (or of its 16), for a piece that starts within a segment and one that ends within one.
+// Partial results: for each row's query head (numbered t * q_heads + head) and slice the maximum (of the scores as they
+// are, which differ exactly), the sum and the values' sums: slice 0 (to own_splits - 1) the own keys, the rest the shared
+// ones; and two of those of 32 rows per wave (or of its 16), for a piece that starts within a segment and one that ends within one.
 struct Partials {
   float2* stat;    // [slices][rows]
   float* sums;     // [slices][rows][dim]
@@ -178,7 +178,7 @@ constexpr float kNoPlace = -1.0f;  // a sum that no row can have
 // Results of a wave's R rows: to y (`slice` below 0), or unfinished to a slice of the rows, or to `wave_stat` and
 // `wave_sums` of R rows.
 template <int D, int R>
-__device__ __forceinline__ void write_rows(const Gathered<D, R>& g, float c, const AttendArgs& a, const Partials& p,
+__device__ __forceinline__ void write_rows(const Gathered<D, R>& g, const AttendArgs& a, const Partials& p,
                                            const Rows& r, int group, int head, int slice, float2* wave_stat,
                                            float* wave_sums) {
   const int lane = __lane_id(), row = r.first + (lane & (R - 1)), token = row / group, h = lane / R;
@@ -201,7 +201,7 @@ __device__ __forceinline__ void write_rows(const Gathered<D, R>& g, float c, con
   const int64_t to = wave_stat ? lane & (R - 1) : (int64_t)slice * p.rows + t * a.q_heads + at;
   // (a row without a place is marked: shared keys, which it does not have, must not count for it)
   if (h == 0)
-    (wave_stat ? wave_stat : p.stat)[to] = r.place0 + token < 0 ? float2{0.0f, kNoPlace} : float2{g.top * c, sum};
+    (wave_stat ? wave_stat : p.stat)[to] = r.place0 + token < 0 ? float2{0.0f, kNoPlace} : float2{g.top, sum};
   float* sums = (wave_stat ? wave_sums : p.sums) + to * D + 4 * h;
 #pragma unroll
   for (int n = 0; n < Gathered<D, R>::QUADS; ++n) {

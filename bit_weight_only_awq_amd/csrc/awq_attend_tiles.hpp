@@ -252,7 +252,7 @@ __device__ __forceinline__ void attend_tile(const AttendArgs& a, const CacheArgs
       if (block + i < to) step(block + i, slot, std::false_type{});
     });
   wait_loads<0>();  // (those past the end)
-  if (live) write_rows(g, scale, a, p, rows, group, head, slice, nullptr, nullptr);
+  if (live) write_rows(g, a, p, rows, group, head, slice, nullptr, nullptr);
 }
 
 }  // namespace awq

@@ -157,7 +157,7 @@ __device__ __forceinline__ void attend_wave(const AttendArgs& a, const CacheArgs
     }
     const bool whole = here == blocks;
     const int64_t slot = 2 * (int64_t)wave + (block0 > 0 ? 0 : 1);
-    write_rows(g, scale, a, p, rows, group, head, a.shared > 0 ? 0 : -1,
+    write_rows(g, a, p, rows, group, head, a.shared > 0 ? 0 : -1,
                whole ? nullptr : p.wave_stat + slot * 32, p.wave_sums + slot * 32 * D);
   }
 }
