@@ -1012,7 +1012,8 @@ def _check_attention(x, qkv, o, cache, seqs, residual, scale, shared, pages, fir
         rp, ldr = _rows2d(residual, T, o.N, "residual")
         if ldr % 8 or rp % 16:
             raise AwqError(AWQ_ERR_SHAPE if ldr % 8 else AWQ_ERR_ALIGN, "awq_linear_fused")
-    if scale is not None and not 0.0 < ctypes.c_float(scale).value < float("inf"):
+    f32 = lambda v: ctypes.c_float(v).value  # noqa: E731
+    if scale is not None and not (f32(scale) > 0.0 and f32(scale * 1.4426950408889634) < float("inf")):
         raise AwqError(AWQ_ERR_OPTION, "awq_attend")
     if pages:
         if cache.bounds is None:

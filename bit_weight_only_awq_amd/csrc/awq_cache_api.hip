@@ -38,6 +38,9 @@ int check_cache(const int32_t* offsets, const int32_t* lengths, const int32_t* t
   return aligned4(offsets) && aligned4(lengths) && aligned4(tables) ? AWQ_OK : AWQ_ERR_ALIGN;
 }
 
+// (the kernels work in powers of two: the scale times log2(e) must be finite as well)
+bool scale_ok(float scale) { return scale > 0.0f && !isinf(scale * 1.4426950408889634f); }
+
 bool stride_ok(int32_t ld, int64_t row) { return ld >= row && ld <= kMaxDim && (ld & 7) == 0; }
 
 int check_pointers(const void* a, const void* b, const void* c, const void* d) {
@@ -102,7 +105,7 @@ int awq_attend(const void* q, int32_t ldq, const int32_t* offsets, const int32_t
   if (st != AWQ_OK) return st;
   const int64_t row = (int64_t)q_heads * head_dim;
   if (!stride_ok(ldq, row) || !stride_ok(ldy, row)) return AWQ_ERR_SHAPE;
-  if (!(scale > 0.0f) || isinf(scale)) return AWQ_ERR_OPTION;
+  if (!scale_ok(scale)) return AWQ_ERR_OPTION;
   if (shared < 0 || shared % page_size != 0 || shared / page_size > width) return AWQ_ERR_OPTION;
   if (!awq::attend_fits(T, B, q_heads, kv_heads, head_dim, page_size, width, shared)) return AWQ_ERR_SHAPE;
   st = check_pointers(q, k_pages, v_pages, y);
@@ -158,7 +161,7 @@ int awq_attend_pages(const void* q, int32_t ldq, const int32_t* offsets, const i
   if (st != AWQ_OK) return st;
   const int64_t row = (int64_t)q_heads * head_dim;
   if (!stride_ok(ldq, row) || !stride_ok(ldy, row)) return AWQ_ERR_SHAPE;
-  if (!(scale > 0.0f) || isinf(scale)) return AWQ_ERR_OPTION;
+  if (!scale_ok(scale)) return AWQ_ERR_OPTION;
   if (count < 1 || (int64_t)count * page_size > ((int64_t)1 << 30) ||
       (int64_t)T * kv_heads * ((q_heads / kv_heads + 15) / 16) * ((int64_t)count * page_size / 32 + 1) >= ((int64_t)1 << 30))
     return AWQ_ERR_OPTION;

@@ -473,7 +473,7 @@ int awq_append_kv(const void* x, int32_t ldx, const int32_t* offsets, const int3
  *   y[t][h] = sum_j p_j v_j,  p = softmax over the keys j <= place(t) of scale (q[t][h] . k_j)
  * (the keys of a batch's new tokens are in the cache already: awq_append_kv).
  * q          in   fp16, row t at q + t * ldq: q_heads vectors.
- * scale      finite and > 0 (AWQ_ERR_OPTION).
+ * scale      > 0, and finite times log2(e), which is up to 2.35e38 (AWQ_ERR_OPTION).
  * shared     keys that all sequences begin with (a common prompt; 0: none), a multiple
  *            of page_size: read once for the whole batch through the table of the first
  *            sequence with rows, whatever the other tables hold there.  A sequence may end

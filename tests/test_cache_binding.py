@@ -65,7 +65,7 @@ def test_attention_runs_its_calls(calls):
     dict(pages=1 << 28), dict(pages=(1 << 30) // 16 + 1),                            # keys past 2^30
     dict(shared=8), dict(shared=-16), dict(shared=80), dict(shared=1 << 32), dict(shared=16, pages=4),
     dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e-50),
-    dict(scale=1e39), dict(pages=4, scale=0.0),
+    dict(scale=1e39), dict(scale=2.4e38), dict(pages=4, scale=0.0),
     dict(residual=half(2, 512)), dict(residual=half(3, 520)), dict(residual=torch.zeros((3, 512))),
     dict(residual=half(3, 1024)[:, ::2]),
     dict(o=weight(512, 768)), dict(qkv=weight(1024, 512)), dict(qkv=weight(512, 512)), dict(qkv=weight(1500, 512)),

@@ -4,7 +4,7 @@ from __future__ import annotations
 
 import pytest
 
-from tests.test_cache_abi import attending, awq, lib  # noqa: F401  (lib: the library's fixture)
+from tests.test_cache_abi import attending, attending_pages, awq, lib  # noqa: F401  (lib: the library's fixture)
 
 # as many sequences, tokens and heads as there may be, over tables so wide that row tiles take the own keys: a workgroup of
 # 256 threads for every token and head, and more for the shared keys
@@ -27,3 +27,12 @@ def test_what_fits_is_taken(lib):  # noqa: F811
     """(By the workspace's size: parts of both kinds of keys.)"""
     for kw in (dict(B=60000, T=65535 - 5536), dict(width=16), dict(Hq=128, Hkv=128), dict(T=32768, B=32768)):
         assert workspace(lib, 64, **kw) >= 2 * dict(MANY, **kw)["T"] * dict(MANY, **kw)["Hq"] * (64 * 4 + 8), kw
+
+
+@pytest.mark.parametrize("call", [attending, attending_pages])
+def test_scales_past_the_powers_of_two_are_refused(lib, call):  # noqa: F811
+    """Times log2(e) they are infinite: every row would be NaN.  (What is taken is told by the check that follows.)"""
+    for scale in (2.36e38, 3.4e38):
+        assert call(lib, scale=scale) == awq.AWQ_ERR_OPTION, scale
+    for scale in (2.35e38, 1e-30, 1e-45):
+        assert call(lib, scale=scale, y=0) == awq.AWQ_ERR_NULL, scale
