@@ -830,9 +830,9 @@ def _int32(value: int, where: str) -> int:
 
 
 def _cache_shape(cache: KvCache):
-    """(pages, key heads, page size, head size) of a cache that has any."""
+    """(pages, key heads, page size, head size) of a cache; it may be without pages where there are no tokens."""
     shape = cache.k.shape
-    if len(shape) != 4 or 0 in shape or cache.v.shape != shape:
+    if len(shape) != 4 or 0 in shape[1:] or cache.v.shape != shape:
         raise ValueError("the cache's keys and values must be float16 tensors [pages, kv_heads, page_size, head_dim]")
     return shape
 

@@ -129,3 +129,11 @@ def test_pages_of_another_shape_are_value_errors():
             awq.attend_pages(half(4, 1024), cache(), sequences(), bad)
     with pytest.raises(ValueError):
         awq.attend_pages(torch.zeros((), dtype=torch.float16), cache(), sequences(), whole(4, 2, 3))
+
+
+def test_a_cache_without_pages_is_one_where_there_are_no_tokens(monkeypatch):
+    monkeypatch.setattr(awq, "_rows2d", lambda t, rows, width, what: (0, width))  # (the rows are taken to be on the GPU)
+    monkeypatch.setattr(awq, "_handle", lambda t: 0)
+    assert awq.attend(half(0, 1024), cache(pages=0), sequences()).shape == (0, 1024)
+    assert awq.append_kv(half(0, 1536), cache(pages=0), sequences()).shape == (0, 1024)
+    assert awq.select_pages(half(0, 1024), cache(pages=0), sequences(), 4).shape == (0, 2, 4)

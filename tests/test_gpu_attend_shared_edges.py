@@ -32,3 +32,31 @@ def test_sequences_without_rows_come_first(new, D):
         b.tables[s] = np.array([-1, 1 << 30, 3, -(1 << 31)])[(s + np.arange(b.width)) % 4]
     y = attend(b)
     b.check(y, f"new tokens {new}, heads of {D}")
+
+
+def test_a_first_sequence_that_empties_between_replays():
+    """Captured with rows in every sequence; replayed without any in the first, and its table of no page."""
+    awq = G.lib()
+    for D, new in ((128, 1), (256, 2), (128, 60)):
+        b = Batch([new] * 3, [9, 30, 4], 8, 2, D, 16, shared=160, seed=new)
+        cache, seqs = b.device()
+        q = G.dev_f16(b.q)
+        eager = awq.attend(q, cache, seqs, shared=160)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            y = awq.attend(q, cache, seqs, shared=160)
+        kept = [t.clone() for t in seqs]
+        for empty in (False, True, False, True):
+            for t, was in zip(seqs, kept):
+                t.copy_(was)
+            if empty:
+                seqs.offsets[0] = new
+                seqs.lengths[0] = 0
+                seqs.tables[0] = -1
+            y.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y[new:], eager[new:]), (D, new, empty)
+            assert bool((y[:new] == 7.0).all()) if empty else torch.equal(y[:new], eager[:new]), (D, new, empty)
